@@ -217,6 +217,91 @@ q8_status q8_bsa_attention(const uint16_t* q, const uint16_t* k, const uint16_t*
                            cudaStream_t stream);
 
 /*
+ * The attention layer around the linears, for serving.  The post runs its Q8_0 linears inside
+ * GDN + attention blocks and has an attention kernel of its own ("CUDA inference engine for
+ * running Qwen3.5/3.6 hybrid models on mining cards (CMP 100-210)", news.hada.io topic
+ * 29953, feature list); the operations here are q8_qk_norm_rope on the outputs of the
+ * projections, q8_prompt_attention for whole prompts, q8_prefix_attention for the next token
+ * of each request of a batch.  H query heads share Hkv key/value heads (head h reads
+ * h / (H / Hkv)).  Strides are host values in elements; the d channels of a head are
+ * contiguous, every stride is a multiple of 16 bytes and a stride of 0 repeats an input.
+ *
+ * q8_qk_norm_rope -- RMSNorm of every query and key head and the rotation of its first rot
+ * channels by the token's position, in one pass.
+ *   q [T][H][d], k [T][Hkv][d] of type xtype, tokens q_stride and k_stride elements apart
+ *     (views of a fused projection's rows are fine), heads d elements apart;
+ *   q_weight, k_weight [d] float: z = x * r * weight, r = 1 / sqrt(mean_d x^2 + eps); NULL:
+ *     those heads are not normalised (z = x); eps finite and > 0 where a weight is given
+ *     (else Q8_ERR_VALUE);
+ *   positions [T] int32, inv_freq [rot / 2] double: pair i of a head turns by the angle
+ *     positions[t] * inv_freq[i] (any scaling of the frequencies is the caller's), kept exact
+ *     to 2^-32 turns for |position| < 2^31 and frequencies up to 1;  pair (a, b) becomes
+ *     (a cos - b sin, a sin + b cos).  interleaved 0: pair i is channels (i, i + rot / 2);
+ *     1: channels (2 i, 2 i + 1);
+ *   q_out, k_out: bfloat16 bits, rounded once (to nearest even), tokens q_out_stride and
+ *     k_out_stride elements apart.  q_out may be q itself and k_out k itself (bfloat16
+ *     inputs, the same strides); they may not overlap an input in another way.
+ *   d % 16 == 0, 16 <= d <= 256;  rot % 16 == 0, 0 <= rot <= d (else Q8_ERR_SHAPE).
+ *   positions 4-byte aligned, inv_freq 8-byte, the rest 16-byte.
+ */
+q8_status q8_qk_norm_rope(const void* q, const void* k, q8_dtype xtype, int64_t q_stride,
+                          int64_t k_stride, const float* q_weight, const float* k_weight,
+                          float eps, const int32_t* positions, const double* inv_freq,
+                          int64_t rot, int interleaved, uint16_t* q_out, uint16_t* k_out,
+                          int64_t q_out_stride, int64_t k_out_stride, int64_t T, int64_t H,
+                          int64_t Hkv, int64_t d, cudaStream_t stream);
+
+/*
+ * q8_prompt_attention -- causal attention over B packed sequences of any lengths.
+ *   q [Tq][H][d], k and v [Tk][Hkv][d], o [Tq][H][d]: bfloat16 bits; d = 64 or 128;
+ *     H / Hkv <= 128; strides[8] = {q token, q head, k token, k head, v token, v head, o token,
+ *     o head}, NULL for the contiguous layouts above (each head's tokens behind one another,
+ *     as in q8_bsa_attention, is {d, T d, ...});
+ *   cu_q, cu_k [B + 1] int32 (device): sequence s has the queries cu_q[s] .. cu_q[s + 1] - 1
+ *     and the keys cu_k[s] .. cu_k[s + 1] - 1.  Lengths may be 0.  With lq queries and lk
+ *     keys its query i sees its keys j <= i + lk - lq: the queries are the last lq tokens of
+ *     the context (lk > lq: the earlier keys were cached before).  A query that sees no key
+ *     gets 0.  Rows of o outside every sequence are left as they are, and nothing outside a
+ *     sequence's own keys reaches its outputs.  A sequence that is not inside [0, Tq] x
+ *     [0, Tk] or has a negative length is skipped and sets bit 9 of the device error word;
+ *   o = sum_j p_j v_j / sum_j p_j, p_j = exp(scale * (q . k_j) - max); scale finite and > 0
+ *     (else Q8_ERR_VALUE).
+ * Scores, maxima, sums and o are binary32; the weights p enter the product with v rounded to
+ * bfloat16 (as in q8_bsa_attention), and o is rounded to bfloat16 once.
+ * workspace: at least q8_prompt_attention_workspace_size() bytes, 16-byte aligned (partial
+ * results where the keys are split among several blocks; NULL where that size is 0).  Calls
+ * that overlap in time need one each.  Never allocates.
+ */
+q8_status q8_prompt_attention(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                              const int32_t* cu_q, const int32_t* cu_k, uint16_t* o, int64_t B,
+                              int64_t Tq, int64_t Tk, int64_t H, int64_t Hkv, int64_t d,
+                              float scale, const int64_t* strides, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+size_t q8_prompt_attention_workspace_size(int64_t B, int64_t Tq, int64_t Tk, int64_t H,
+                                          int64_t Hkv, int64_t d);
+
+/*
+ * q8_prefix_attention -- one query for each of B requests that share a prefix of P tokens:
+ * request b sees the P shared keys and the first own_len[b] keys of its own cache.  The
+ * shared keys are read for all requests together.
+ *   q, o [B][H][d]; k_prefix, v_prefix [P][Hkv][d]; k_own, v_own [B][cap][Hkv][d]: bfloat16
+ *     bits; d = 64 or 128; H / Hkv <= 128; strides[14] = {q request, q head, k_prefix token,
+ *     head, v_prefix token, head, k_own request, token, head, v_own request, token, head,
+ *     o request, o head}, NULL for these contiguous layouts;
+ *   own_len [B] int32 (device), 0 <= own_len[b] <= cap; a length outside that range is taken
+ *     as the nearest one inside and sets bit 9 of the device error word.  P and cap may be 0.
+ *     Cache rows at and behind own_len[b] are not read.  A request without any key gets 0.
+ * Arithmetic, scale and workspace as q8_prompt_attention.
+ */
+q8_status q8_prefix_attention(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* v_prefix,
+                              const uint16_t* k_own, const uint16_t* v_own, const int32_t* own_len,
+                              uint16_t* o, int64_t B, int64_t P, int64_t cap, int64_t H,
+                              int64_t Hkv, int64_t d, float scale, const int64_t* strides,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t q8_prefix_attention_workspace_size(int64_t B, int64_t P, int64_t cap, int64_t H,
+                                          int64_t Hkv, int64_t d);
+
+/*
  * Prepared weights for the tensor-core path.  The tensor path feeds the MMA binary16
  * copies of the int8 codes (exact: |q| <= 127); q8_linear / q8_linear_ex / q8_linear_fused
  * widen the codes on every call (read N*K bytes, write and re-read 2*N*K).  For weights

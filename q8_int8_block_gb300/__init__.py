@@ -16,6 +16,9 @@ this package fails.
     B16 = q8_weights_to_f16(Wq)                        # once per weight matrix
     y = q8_linear_prepared(x, B16, Wd)                 # tensor-core path, no per-call widening
     o = q8_bsa_attention(q, k, v, row_ptr, col_idx)    # block-sparse causal attention
+    q, k = q8_qk_norm_rope(q, k, positions, inv_freq, q_weight=wq, k_weight=wk)  # heads' norm + rotation
+    o = q8_prompt_attention(q, k, v, cu_q)             # causal, packed sequences of any lengths
+    o = q8_prefix_attention(q, kp, vp, ko, vo, n)      # one new token a request, shared prefix
     codes, scales = q8_kv3_encode(kv)                  # kv [..., 128] -> 3-bit codes + scales
     kv_hat = q8_kv3_decode(codes, scales, torch.bfloat16)
     isum = q8_block_sums(xq, Wq, path="decode")  # int32 [M,N,K/32]
@@ -28,7 +31,9 @@ import torch
 __all__ = ["Q8Error", "q8_quantize_weights", "q8_quantize_act", "q8_quantize_act_rmsnorm",
            "q8_linear", "q8_linear_ex", "q8_kv3_encode", "q8_kv3_decode", "KV3_GROUP",
            "q8_weights_to_f16", "q8_linear_prepared", "q8_linear_prepared_workspace_size",
-           "q8_bsa_attention",
+           "q8_bsa_attention", "q8_qk_norm_rope", "q8_prompt_attention",
+           "q8_prompt_attention_workspace_size", "q8_prefix_attention",
+           "q8_prefix_attention_workspace_size",
            "q8_linear_fused", "EPILOGUES",
            "q8_linear_workspace_size", "q8_block_sums", "q8_device_error", "q8_release",
            "q8_set_timing_events", "q8_linear_noalloc", "NOALLOC_SCRATCH_BYTES",
@@ -74,6 +79,9 @@ def _load():
         "q8_kv3_decode": [p, p, p, i32, i64, p],
         "q8_weights_to_f16": [p, p, i64, i64, p],
         "q8_bsa_attention": [p, p, p, p, p, i64, p, i32, i64, i64, i64, i64, p],
+        "q8_qk_norm_rope": [p, p, i32, i64, i64, p, p, f32, p, p, i64, i32, p, p, i64, i64, i64, i64, i64, i64, p],
+        "q8_prompt_attention": [p, p, p, p, p, p, i64, i64, i64, i64, i64, i64, f32, p, p, sz, p],
+        "q8_prefix_attention": [p, p, p, p, p, p, p, i64, i64, i64, i64, i64, i64, f32, p, p, sz, p],
         "q8_linear_prepared": [p, i32, p, f32, p, p, i32, p, p, i32, i64, i64, i64, p, sz, p],
     }
     for name, args in sigs.items():
@@ -86,6 +94,9 @@ def _load():
     L.q8_linear_workspace_size.restype = sz
     L.q8_linear_prepared_workspace_size.argtypes = [i64, i64, i64]
     L.q8_linear_prepared_workspace_size.restype = sz
+    for name in ("q8_prompt_attention_workspace_size", "q8_prefix_attention_workspace_size"):
+        getattr(L, name).argtypes = [i64] * 6
+        getattr(L, name).restype = sz
     L.q8_device_error.argtypes = [ctypes.POINTER(i32)]
     L.q8_device_error.restype = ctypes.c_uint32
     L.q8_status_string.argtypes = [i32]
@@ -372,6 +383,154 @@ def q8_bsa_attention(q, k, v, row_ptr, col_idx, out_dtype=torch.float32, o=None,
     _check(_L.q8_bsa_attention(_ptr(q), _ptr(k), _ptr(v), _ptr(row_ptr), _ptr(col_idx),
                                col_idx.numel(), _ptr(o), DTYPES[out_dtype], H, Hkv, T, d,
                                _stream(stream)), "q8_bsa_attention")
+    return o
+
+
+def _heads(name, t, dtype, shape, d):
+    """t: a CUDA tensor on the current device of this type and shape whose innermost dimension
+    (a head's d channels) is contiguous; its other strides are passed on."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != d:
+        raise ValueError(f"{name}: must be a CUDA tensor on the current device (cuda:{d})")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+
+
+def _lengths(name, t, n, d):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name}: expected torch.int32, got {t.dtype}")
+    if t.shape != (n,):
+        raise ValueError(f"{name}: expected shape {(n,)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != d or not t.is_contiguous():
+        raise ValueError(f"{name}: must be a contiguous CUDA tensor on the current device (cuda:{d})")
+
+
+_STRIDES8, _STRIDES14 = ctypes.c_int64 * 8, ctypes.c_int64 * 14
+
+
+def _workspace(workspace, need, device, d):
+    """(tensor or None, bytes): the caller's workspace, else one that torch allocates."""
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=device) if need else None), need
+    if not workspace.is_cuda or workspace.get_device() != d or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be a contiguous CUDA tensor on the current device (cuda:{d})")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def q8_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
+                    interleaved=False, q_out=None, k_out=None, stream=None):
+    """RMSNorm of every query and key head and the rotation of its first channels by position:
+    q [T,H,d], k [T,Hkv,d] bfloat16 or float32 (views of a projection's rows are fine),
+    positions int32 [T], inv_freq float64 [rot/2], weights float32 [d] or None (no norm)
+    -> (q_out, k_out) bfloat16.  q_out=q, k_out=k work in place (bfloat16)."""
+    dev = torch.cuda.current_device()
+    T, H, d = q.shape
+    Hkv = k.shape[1]
+    if q.dtype not in DTYPES:
+        raise TypeError(f"q: expected bfloat16 or float32, got {q.dtype}")
+    _heads("q", q, q.dtype, (T, H, d), dev)
+    _heads("k", k, q.dtype, (T, Hkv, d), dev)
+    if q_out is None:
+        q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _heads("q_out", q_out, torch.bfloat16, (T, H, d), dev)
+    if k_out is None:
+        k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _heads("k_out", k_out, torch.bfloat16, (T, Hkv, d), dev)
+    for name, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)):
+        if t.shape[1] > 1 and t.stride(1) != d:
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+    _lengths("positions", positions, T, dev)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq: a 1-D float64 CUDA tensor")
+    _need(inv_freq, torch.float64, inv_freq.shape, "inv_freq")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _need(w, torch.float32, (d,), name)
+    _on_device(inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight)
+    many = T > 1
+    _check(_L.q8_qk_norm_rope(q.data_ptr(), k.data_ptr(), DTYPES[q.dtype], q.stride(0) if many else H * d,
+                              k.stride(0) if many else Hkv * d, _ptr(q_weight), _ptr(k_weight), float(eps),
+                              positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0],
+                              1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(),
+                              q_out.stride(0) if many else H * d, k_out.stride(0) if many else Hkv * d,
+                              T, H, Hkv, d, _stream(stream)), "q8_qk_norm_rope")
+    return q_out, k_out
+
+
+def q8_prompt_attention_workspace_size(B, Tq, Tk, H, Hkv, d) -> int:
+    return int(_L.q8_prompt_attention_workspace_size(B, Tq, Tk, H, Hkv, d))
+
+
+def q8_prompt_attention(q, k, v, cu_q, cu_k=None, scale=None, o=None, workspace=None, stream=None):
+    """Causal attention over packed sequences: q [Tq,H,d], k and v [Tk,Hkv,d] bfloat16 (d 64 or
+    128; strided views are fine), cu_q and cu_k int32 [B+1] on the device: sequence s holds the
+    queries cu_q[s]:cu_q[s+1], the last ones of its keys cu_k[s]:cu_k[s+1] (None: cu_q)
+    -> o [Tq,H,d] bfloat16 (a new o is not initialised outside the sequences).  scale None:
+    1/sqrt(d).  workspace None: allocated here with torch."""
+    dev = torch.cuda.current_device()
+    Tq, H, d = q.shape
+    Tk, Hkv, _ = k.shape
+    _heads("q", q, torch.bfloat16, (Tq, H, d), dev)
+    _heads("k", k, torch.bfloat16, (Tk, Hkv, d), dev)
+    _heads("v", v, torch.bfloat16, (Tk, Hkv, d), dev)
+    if cu_k is None:
+        cu_k = cu_q
+    n = cu_q.numel()
+    if n < 1:
+        raise ValueError("cu_q: expected at least one entry")
+    _lengths("cu_q", cu_q, n, dev)
+    _lengths("cu_k", cu_k, n, dev)
+    if o is None:
+        o = torch.empty((Tq, H, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _heads("o", o, torch.bfloat16, (Tq, H, d), dev)
+    need = _L.q8_prompt_attention_workspace_size(n - 1, Tq, Tk, H, Hkv, d)
+    workspace, nbytes = _workspace(workspace, need, q.device, dev)
+    st = _STRIDES8(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2])
+    _check(_L.q8_prompt_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
+                                  o.data_ptr(), n - 1, Tq, Tk, H, Hkv, d,
+                                  d ** -0.5 if scale is None else float(scale), st, _ptr(workspace), nbytes,
+                                  _stream(stream)), "q8_prompt_attention")
+    return o
+
+
+def q8_prefix_attention_workspace_size(B, P, cap, H, Hkv, d) -> int:
+    return int(_L.q8_prefix_attention_workspace_size(B, P, cap, H, Hkv, d))
+
+
+def q8_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, scale=None, o=None,
+                        workspace=None, stream=None):
+    """One query for each of B requests behind a shared prefix: q [B,H,d], k_prefix and
+    v_prefix [P,Hkv,d], k_own and v_own [B,cap,Hkv,d] bfloat16 (d 64 or 128; strided views are
+    fine), own_len int32 [B] on the device: request b sees the prefix and its first own_len[b]
+    own keys -> o [B,H,d] bfloat16.  scale None: 1/sqrt(d).  workspace None: allocated here."""
+    dev = torch.cuda.current_device()
+    B, H, d = q.shape
+    P, Hkv, _ = k_prefix.shape
+    cap = k_own.shape[1]
+    _heads("q", q, torch.bfloat16, (B, H, d), dev)
+    _heads("k_prefix", k_prefix, torch.bfloat16, (P, Hkv, d), dev)
+    _heads("v_prefix", v_prefix, torch.bfloat16, (P, Hkv, d), dev)
+    _heads("k_own", k_own, torch.bfloat16, (B, cap, Hkv, d), dev)
+    _heads("v_own", v_own, torch.bfloat16, (B, cap, Hkv, d), dev)
+    _lengths("own_len", own_len, B, dev)
+    if o is None:
+        o = torch.empty((B, H, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _heads("o", o, torch.bfloat16, (B, H, d), dev)
+    need = _L.q8_prefix_attention_workspace_size(B, P, cap, H, Hkv, d)
+    workspace, nbytes = _workspace(workspace, need, q.device, dev)
+    st = _STRIDES14(*q.stride()[:2], *k_prefix.stride()[:2], *v_prefix.stride()[:2], *k_own.stride()[:3],
+                    *v_own.stride()[:3], *o.stride()[:2])
+    _check(_L.q8_prefix_attention(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_own.data_ptr(),
+                                  v_own.data_ptr(), own_len.data_ptr(), o.data_ptr(), B, P, cap, H, Hkv, d,
+                                  d ** -0.5 if scale is None else float(scale), st, _ptr(workspace), nbytes,
+                                  _stream(stream)), "q8_prefix_attention")
     return o
 
 

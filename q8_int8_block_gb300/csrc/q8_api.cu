@@ -175,6 +175,39 @@ q8_status library_workspace(const DeviceInfo& dev, cudaStream_t stream, size_t b
   return Q8_OK;
 }
 
+// ---- checks of the attention layer's entry points --------------------------------------
+constexpr int64_t kSizeLimit = 0x7FFFFFFF;
+constexpr double kRowLimit = 2147483647.0;           // query rows (tokens x heads)
+constexpr int64_t kStrideLimit = int64_t{1} << 38;   // elements: byte strides below 2^40 (TMA)
+
+// a stride between the n items of a dimension (not used when n < 2)
+bool stride_ok(int64_t stride, int64_t n) {
+  return stride >= 0 && stride < kStrideLimit &&
+         static_cast<double>(stride) * static_cast<double>(n) < 281474976710656.0;
+}
+
+bool heads_ok(int64_t H, int64_t Hkv, int64_t d) {
+  return (d == 64 || d == 128) && H >= 0 && Hkv > 0 && H <= kSizeLimit && Hkv <= kSizeLimit && H % Hkv == 0 &&
+         H / Hkv <= 128;
+}
+
+// The caller's strides, or the contiguous ones; a dimension of one item (or none) takes the
+// contiguous stride.  The last two (o's) may not let two rows share elements.
+q8_status take_strides(int64_t* st, const int64_t* plain, const int64_t* given, const int64_t* extent, int n,
+                       int out) {
+  for (int i = 0; i < n; ++i) {
+    st[i] = given != nullptr && extent[i] > 1 ? given[i] : plain[i];
+    if (!stride_ok(st[i], extent[i])) return Q8_ERR_SHAPE;
+    if (st[i] % 8 != 0) return Q8_ERR_ALIGN;
+  }
+  const int64_t d = plain[out + 1];
+  const int64_t big = st[out] > st[out + 1] ? out : out + 1, small = big == out ? out + 1 : out;
+  if ((extent[small] > 1 && st[small] < d) ||
+      (extent[big] > 1 && st[big] < (extent[small] > 1 ? (extent[small] - 1) * st[small] : 0) + d))
+    return Q8_ERR_SHAPE;
+  return Q8_OK;
+}
+
 q8_status launch_status(cudaError_t e) { return e == cudaSuccess ? Q8_OK : cuda_fail(e); }
 
 // ---- timing hook (q8_set_timing_events) ----------------------------------------------
@@ -475,6 +508,123 @@ q8_status q8_bsa_attention(const uint16_t* q, const uint16_t* k, const uint16_t*
   if (st != Q8_OK) return st;
   return launch_status(
       launch_bsa(q, k, v, row_ptr, col_idx, nnz, o, static_cast<int>(otype), H, Hkv, T, dev, stream));
+}
+
+q8_status q8_qk_norm_rope(const void* q, const void* k, q8_dtype xtype, int64_t q_stride,
+                          int64_t k_stride, const float* q_weight, const float* k_weight,
+                          float eps, const int32_t* positions, const double* inv_freq,
+                          int64_t rot, int interleaved, uint16_t* q_out, uint16_t* k_out,
+                          int64_t q_out_stride, int64_t k_out_stride, int64_t T, int64_t H,
+                          int64_t Hkv, int64_t d, cudaStream_t stream) {
+  if (xtype != Q8_F32 && xtype != Q8_BF16) return Q8_ERR_DTYPE;
+  if (T < 0 || H < 0 || Hkv < 0 || d < 16 || d > 256 || d % 16 != 0 || rot < 0 || rot > d || rot % 16 != 0 ||
+      T > kSizeLimit || H > kSizeLimit || Hkv > kSizeLimit || H + Hkv > kSizeLimit)
+    return Q8_ERR_SHAPE;
+  // an input's tokens may repeat (stride 0), an output's may not overlap
+  if (!stride_ok(q_stride, T) || !stride_ok(k_stride, T) || !stride_ok(q_out_stride, T) ||
+      !stride_ok(k_out_stride, T) ||
+      (T > 1 && ((H > 0 && q_out_stride < H * d) || (Hkv > 0 && k_out_stride < Hkv * d))))
+    return Q8_ERR_SHAPE;
+  if ((q_weight != nullptr || k_weight != nullptr) && (!(eps > 0.0f) || !std::isfinite(eps)))
+    return Q8_ERR_VALUE;
+  const bool any_q = T > 0 && H > 0, any_k = T > 0 && Hkv > 0;
+  if ((any_q && (q == nullptr || q_out == nullptr)) || (any_k && (k == nullptr || k_out == nullptr)) ||
+      ((any_q || any_k) && (positions == nullptr || (rot > 0 && inv_freq == nullptr))))
+    return Q8_ERR_NULL;
+  const int64_t per16 = xtype == Q8_F32 ? 4 : 8;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(q_weight) ||
+      !aligned16(k_weight) || q_stride % per16 != 0 || k_stride % per16 != 0 || q_out_stride % 8 != 0 ||
+      k_out_stride % 8 != 0 || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0)
+    return Q8_ERR_ALIGN;
+  DeviceInfo dev;
+  const q8_status st = current_device(&dev);
+  if (st != Q8_OK) return st;
+  return launch_status(launch_qk_norm_rope(q, k, static_cast<int>(xtype), q_stride, k_stride, q_weight, k_weight,
+                                           eps, positions, inv_freq, static_cast<int>(rot), interleaved != 0,
+                                           q_out, k_out, q_out_stride, k_out_stride, T, H, Hkv,
+                                           static_cast<int>(d), dev, stream));
+}
+
+q8_status q8_prompt_attention(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                              const int32_t* cu_q, const int32_t* cu_k, uint16_t* o, int64_t B,
+                              int64_t Tq, int64_t Tk, int64_t H, int64_t Hkv, int64_t d,
+                              float scale, const int64_t* strides, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+  if (!heads_ok(H, Hkv, d) || B < 0 || Tq < 0 || Tk < 0 || B >= kSizeLimit || Tq > kSizeLimit ||
+      Tk > kSizeLimit || static_cast<double>(Tq) * H > kRowLimit)
+    return Q8_ERR_SHAPE;
+  PromptArgs a = {q, k, v, cu_q, cu_k, o, B, Tq, Tk, H, Hkv, d, scale, {}, workspace, nullptr};
+  const int64_t plain[8] = {H * d, d, Hkv * d, d, Hkv * d, d, H * d, d};
+  const int64_t extent[8] = {Tq, H, Tk, Hkv, Tk, Hkv, Tq, H};
+  q8_status st = take_strides(a.st, plain, strides, extent, 8, 6);
+  if (st != Q8_OK) return st;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return Q8_ERR_VALUE;
+  const bool any = B > 0 && Tq > 0 && H > 0;
+  if (any && (q == nullptr || o == nullptr || cu_q == nullptr || cu_k == nullptr ||
+              (Tk > 0 && (k == nullptr || v == nullptr))))
+    return Q8_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(cu_q) & 3u) != 0 || (reinterpret_cast<uintptr_t>(cu_k) & 3u) != 0)
+    return Q8_ERR_ALIGN;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != Q8_OK) return st;
+  if (!any) return Q8_OK;
+  const size_t need = prompt_ws_bytes(B, Tq, Tk, H, Hkv, d, dev);
+  if (need > 0 && workspace == nullptr) return Q8_ERR_NULL;
+  if (workspace_bytes < need) return Q8_ERR_NOMEM;
+  return launch_status(launch_prompt_attention(a, dev, stream));
+}
+
+size_t q8_prompt_attention_workspace_size(int64_t B, int64_t Tq, int64_t Tk, int64_t H,
+                                          int64_t Hkv, int64_t d) {
+  if (!heads_ok(H, Hkv, d) || B <= 0 || Tq <= 0 || Tk < 0 || H == 0 || B >= kSizeLimit || Tq > kSizeLimit ||
+      Tk > kSizeLimit || static_cast<double>(Tq) * H > kRowLimit)
+    return 0;
+  DeviceInfo dev;
+  if (current_device(&dev) != Q8_OK) return 0;
+  return prompt_ws_bytes(B, Tq, Tk, H, Hkv, d, dev);
+}
+
+q8_status q8_prefix_attention(const uint16_t* q, const uint16_t* k_prefix, const uint16_t* v_prefix,
+                              const uint16_t* k_own, const uint16_t* v_own, const int32_t* own_len,
+                              uint16_t* o, int64_t B, int64_t P, int64_t cap, int64_t H,
+                              int64_t Hkv, int64_t d, float scale, const int64_t* strides,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!heads_ok(H, Hkv, d) || B < 0 || P < 0 || cap < 0 || B > kSizeLimit || P > kSizeLimit ||
+      cap > kSizeLimit || static_cast<double>(B) * H > kRowLimit)
+    return Q8_ERR_SHAPE;
+  PrefixArgs a = {q, k_prefix, v_prefix, k_own, v_own, own_len, o, B, P, cap, H, Hkv, d, scale, {}, workspace, nullptr};
+  const int64_t plain[14] = {H * d, d, Hkv * d, d, Hkv * d, d, cap * Hkv * d, Hkv * d, d, cap * Hkv * d, Hkv * d, d,
+                             H * d, d};
+  const int64_t extent[14] = {B, H, P, Hkv, P, Hkv, B, cap, Hkv, B, cap, Hkv, B, H};
+  q8_status st = take_strides(a.st, plain, strides, extent, 14, 12);
+  if (st != Q8_OK) return st;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return Q8_ERR_VALUE;
+  const bool any = B > 0 && H > 0;
+  if (any && (q == nullptr || o == nullptr || own_len == nullptr || (P > 0 && (k_prefix == nullptr || v_prefix == nullptr)) ||
+              (cap > 0 && (k_own == nullptr || v_own == nullptr))))
+    return Q8_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k_prefix) || !aligned16(v_prefix) || !aligned16(k_own) || !aligned16(v_own) ||
+      !aligned16(o) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(own_len) & 3u) != 0)
+    return Q8_ERR_ALIGN;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != Q8_OK) return st;
+  if (!any) return Q8_OK;
+  const size_t need = prefix_ws_bytes(B, P, cap, H, Hkv, d, dev);
+  if (need > 0 && workspace == nullptr) return Q8_ERR_NULL;
+  if (workspace_bytes < need) return Q8_ERR_NOMEM;
+  return launch_status(launch_prefix_attention(a, dev, stream));
+}
+
+size_t q8_prefix_attention_workspace_size(int64_t B, int64_t P, int64_t cap, int64_t H,
+                                          int64_t Hkv, int64_t d) {
+  if (!heads_ok(H, Hkv, d) || B <= 0 || P < 0 || cap < 0 || H == 0 || B > kSizeLimit || P > kSizeLimit ||
+      cap > kSizeLimit || static_cast<double>(B) * H > kRowLimit)
+    return 0;
+  DeviceInfo dev;
+  if (current_device(&dev) != Q8_OK) return 0;
+  return prefix_ws_bytes(B, P, cap, H, Hkv, d, dev);
 }
 
 q8_status q8_kv3_encode(const void* x, q8_dtype xtype, uint32_t* codes, float* scales,

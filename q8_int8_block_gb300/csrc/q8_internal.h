@@ -120,6 +120,45 @@ cudaError_t launch_bsa(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                        int otype, int64_t H, int64_t Hkv, int64_t T, const DeviceInfo& dev,
                        cudaStream_t stream);
 
+// ---- q8_rope.cu ------------------------------------------------------------------
+// Heads' RMSNorm and rotation by position (strides in elements between tokens).
+cudaError_t launch_qk_norm_rope(const void* q, const void* k, int xtype, int64_t q_stride,
+                                int64_t k_stride, const float* q_weight, const float* k_weight,
+                                float eps, const int32_t* positions, const double* inv_freq,
+                                int rot, bool interleaved, uint16_t* q_out, uint16_t* k_out,
+                                int64_t q_out_stride, int64_t k_out_stride, int64_t T, int64_t H,
+                                int64_t Hkv, int d, const DeviceInfo& dev, cudaStream_t stream);
+
+// ---- q8_attn.cu ------------------------------------------------------------------
+// Arguments of q8_prompt_attention and q8_prefix_attention, checked; st: strides in elements
+// in the order of the public header; part: workspace.
+struct PromptArgs {
+  const uint16_t *q, *k, *v;
+  const int32_t *cu_q, *cu_k;
+  uint16_t* o;
+  int64_t B, Tq, Tk, H, Hkv, d;
+  float scale;
+  int64_t st[8];
+  void* part;
+  uint32_t* err;
+};
+struct PrefixArgs {
+  const uint16_t *q, *kp, *vp, *ko, *vo;
+  const int32_t* own_len;
+  uint16_t* o;
+  int64_t B, P, cap, H, Hkv, d;
+  float scale;
+  int64_t st[14];
+  void* part;
+  uint32_t* err;
+};
+size_t prompt_ws_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t H, int64_t Hkv, int64_t d,
+                       const DeviceInfo& dev);
+size_t prefix_ws_bytes(int64_t B, int64_t P, int64_t cap, int64_t H, int64_t Hkv, int64_t d,
+                       const DeviceInfo& dev);
+cudaError_t launch_prompt_attention(PromptArgs a, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_prefix_attention(PrefixArgs a, const DeviceInfo& dev, cudaStream_t stream);
+
 // ---- q8_gemm.cu -------------------------------------------------------------------
 // Tensor-core GEMM on binary16 codes: A16 [M,K] activation codes, B16 [N,K] weight codes,
 // xd [M,K/32] f32, Wd [N,K/32] binary16 bits.  Writes y [M,N] (rescaled sum) or, when
