@@ -224,7 +224,10 @@ q8_status q8_bsa_attention(const uint16_t* q, const uint16_t* k, const uint16_t*
  * projections, q8_prompt_attention for whole prompts, q8_prefix_attention for the next token
  * of each request of a batch.  H query heads share Hkv key/value heads (head h reads
  * h / (H / Hkv)).  Strides are host values in elements; the d channels of a head are
- * contiguous, every stride is a multiple of 16 bytes and a stride of 0 repeats an input.
+ * contiguous, every stride is a multiple of 16 bytes and not negative (else Q8_ERR_ALIGN,
+ * Q8_ERR_SHAPE).  A stride of 0 repeats an input: the tokens of q8_qk_norm_rope, the heads of
+ * k and v, the requests of the own caches; elsewhere, and between rows of an output that would
+ * overlap, it is refused (Q8_ERR_SHAPE).
  *
  * q8_qk_norm_rope -- RMSNorm of every query and key head and the rotation of its first rot
  * channels by the token's position, in one pass.

@@ -177,7 +177,7 @@ q8_status library_workspace(const DeviceInfo& dev, cudaStream_t stream, size_t b
 
 // ---- checks of the attention layer's entry points --------------------------------------
 constexpr int64_t kSizeLimit = 0x7FFFFFFF;
-constexpr double kRowLimit = 2147483647.0;           // query rows (tokens x heads)
+constexpr double kRowLimit = 2147483647.0;           // query rows (tokens and sequences x heads)
 constexpr int64_t kStrideLimit = int64_t{1} << 38;   // elements: byte strides below 2^40 (TMA)
 
 // a stride between the n items of a dimension (not used when n < 2)
@@ -192,12 +192,13 @@ bool heads_ok(int64_t H, int64_t Hkv, int64_t d) {
 }
 
 // The caller's strides, or the contiguous ones; a dimension of one item (or none) takes the
-// contiguous stride.  The last two (o's) may not let two rows share elements.
+// contiguous stride.  A stride of 0 is taken where bit i of `repeat` allows it.  The last two
+// (o's) may not let two rows share elements.
 q8_status take_strides(int64_t* st, const int64_t* plain, const int64_t* given, const int64_t* extent, int n,
-                       int out) {
+                       int out, unsigned repeat) {
   for (int i = 0; i < n; ++i) {
     st[i] = given != nullptr && extent[i] > 1 ? given[i] : plain[i];
-    if (!stride_ok(st[i], extent[i])) return Q8_ERR_SHAPE;
+    if (!stride_ok(st[i], extent[i]) || (extent[i] > 1 && st[i] == 0 && ((repeat >> i) & 1u) == 0)) return Q8_ERR_SHAPE;
     if (st[i] % 8 != 0) return Q8_ERR_ALIGN;
   }
   const int64_t d = plain[out + 1];
@@ -552,12 +553,12 @@ q8_status q8_prompt_attention(const uint16_t* q, const uint16_t* k, const uint16
                               float scale, const int64_t* strides, void* workspace,
                               size_t workspace_bytes, cudaStream_t stream) {
   if (!heads_ok(H, Hkv, d) || B < 0 || Tq < 0 || Tk < 0 || B >= kSizeLimit || Tq > kSizeLimit ||
-      Tk > kSizeLimit || static_cast<double>(Tq) * H > kRowLimit)
+      Tk > kSizeLimit || static_cast<double>(Tq + B) * H > kRowLimit)
     return Q8_ERR_SHAPE;
   PromptArgs a = {q, k, v, cu_q, cu_k, o, B, Tq, Tk, H, Hkv, d, scale, {}, workspace, nullptr};
   const int64_t plain[8] = {H * d, d, Hkv * d, d, Hkv * d, d, H * d, d};
   const int64_t extent[8] = {Tq, H, Tk, Hkv, Tk, Hkv, Tq, H};
-  q8_status st = take_strides(a.st, plain, strides, extent, 8, 6);
+  q8_status st = take_strides(a.st, plain, strides, extent, 8, 6, 1u << 3 | 1u << 5);
   if (st != Q8_OK) return st;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return Q8_ERR_VALUE;
   const bool any = B > 0 && Tq > 0 && H > 0;
@@ -579,7 +580,7 @@ q8_status q8_prompt_attention(const uint16_t* q, const uint16_t* k, const uint16
 size_t q8_prompt_attention_workspace_size(int64_t B, int64_t Tq, int64_t Tk, int64_t H,
                                           int64_t Hkv, int64_t d) {
   if (!heads_ok(H, Hkv, d) || B <= 0 || Tq <= 0 || Tk < 0 || H == 0 || B >= kSizeLimit || Tq > kSizeLimit ||
-      Tk > kSizeLimit || static_cast<double>(Tq) * H > kRowLimit)
+      Tk > kSizeLimit || static_cast<double>(Tq + B) * H > kRowLimit)
     return 0;
   DeviceInfo dev;
   if (current_device(&dev) != Q8_OK) return 0;
@@ -598,7 +599,8 @@ q8_status q8_prefix_attention(const uint16_t* q, const uint16_t* k_prefix, const
   const int64_t plain[14] = {H * d, d, Hkv * d, d, Hkv * d, d, cap * Hkv * d, Hkv * d, d, cap * Hkv * d, Hkv * d, d,
                              H * d, d};
   const int64_t extent[14] = {B, H, P, Hkv, P, Hkv, B, cap, Hkv, B, cap, Hkv, B, H};
-  q8_status st = take_strides(a.st, plain, strides, extent, 14, 12);
+  q8_status st = take_strides(a.st, plain, strides, extent, 14, 12,
+                              1u << 3 | 1u << 5 | 1u << 6 | 1u << 8 | 1u << 9 | 1u << 11);
   if (st != Q8_OK) return st;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return Q8_ERR_VALUE;
   const bool any = B > 0 && H > 0;

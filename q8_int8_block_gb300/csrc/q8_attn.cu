@@ -4,13 +4,15 @@
 // Qwen3.5/3.6 hybrid models on mining cards (CMP 100-210)" (news.hada.io topic 29953) runs:
 // o = softmax(scale q . k) v over the keys a query sees, H query heads over Hkv key/value
 // heads.
-//
-// One warp per query row (token and head) walks the row's keys with the running maximum and
-// sum of the softmax: the dot product is split over the lanes, each of which holds d / 32
-// channels of q and o.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
 #include "q8_internal.h"
+#include "q8_ptx.cuh"
 
 namespace q8 {
 namespace {
@@ -64,32 +66,6 @@ struct Row {
 };
 
 template <int D>
-__global__ void __launch_bounds__(128) prompt_rows_kernel(const PromptArgs a) {
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) / 32;
-  const int lane = threadIdx.x & 31;
-  if (row >= a.Tq * a.H) return;
-  if (row == 0)  // one warp looks every sequence over
-    for (int64_t s = lane; s < a.B; s += 32)
-      if (!sequence_ok(a, s)) atomicOr(a.err, kErrBadLength);
-  const int64_t t = row / a.H, h = row - t * a.H, hk = h / (a.H / a.Hkv);
-  // the last sequence that begins at or before t and holds it
-  int64_t lo = 0, hi = a.B;  // cu_q[lo] <= t < cu_q[hi]
-  if (a.cu_q[0] > t || a.cu_q[a.B] <= t) return;
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (a.cu_q[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  const int64_t q0 = a.cu_q[lo], q1 = a.cu_q[lo + 1], k0 = a.cu_k[lo], k1 = a.cu_k[lo + 1];
-  if (!sequence_ok(a, lo) || t < q0 || t >= q1) return;
-  const int64_t seen = (t - q0) + (k1 - k0) - (q1 - q0) + 1;
-  Row<D> r;
-  r.begin(a.q + t * a.st[0] + h * a.st[1], a.scale, lane);
-  r.attend(a.k + k0 * a.st[2] + hk * a.st[3], a.v + k0 * a.st[4] + hk * a.st[5], a.st[2], a.st[4], seen, lane);
-  r.end(a.o + t * a.st[6] + h * a.st[7], lane);
-}
-
-template <int D>
 __global__ void __launch_bounds__(128) prefix_rows_kernel(const PrefixArgs a) {
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) / 32;
   const int lane = threadIdx.x & 31;
@@ -107,18 +83,654 @@ __global__ void __launch_bounds__(128) prefix_rows_kernel(const PrefixArgs a) {
   r.end(a.o + b * a.st[12] + h * a.st[13], lane);
 }
 
+// ---- the tile kernel ---------------------------------------------------------------------
+constexpr int kRows = 128;     // query rows of a tile: 128 / G tokens x G heads
+constexpr int kKeys = 128;     // keys of a block
+constexpr int kTileThreads = 320;  // warps 0-3 and 4-7: softmax of streams A and B; 8 loads; 9 MMAs
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+constexpr float kRescaleLog2 = 8.0f;  // move the exponent reference when a row's maximum gains > 2^8
+
+template <int D, bool kTwo>
+struct TileShape {
+  static constexpr uint32_t kTile = kRows * D * 2;           // a Q tile
+  static constexpr uint32_t kStage = kKeys * D * 2;          // a K or V block
+  static constexpr uint32_t kHalf = kKeys * 128;             // 64 channels of 128 rows
+  static constexpr int kStages = D == 128 ? (kTwo ? 5 : 6) : 8;
+  static constexpr uint32_t kOffRing = (kTwo ? 2 : 1) * kTile;
+  static constexpr uint32_t kOffMl = kOffRing + kStages * kStage;  // (reference, sum) of each row, both streams
+  static constexpr uint32_t kOffBar = kOffMl + 2 * kRows * 8;
+  static constexpr uint32_t kSmem = kOffBar + 256;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+  // the one-tile form joins its two streams through the ring
+  static_assert(kTwo || kStages * kStage >= kRows * (D * 4 + 16), "exchange buffer");
+};
+
+struct TileParams {
+  PromptArgs a;            // strides of q, k, v, o; for the prefix B, Tq are the requests and Tk is P
+  int G, nt;               // heads of a group, tokens of a tile
+  int64_t nslots;
+  int splits;              // blocks of keys are dealt to this many CTAs; 1: o is written here
+  int k_head, v_head;      // 0: all key / value heads are one (stride 0)
+  float scale_log2;
+  float* part_o;           // [splits][Tq * H][D]
+  float2* part_ml;         // [splits][Tq * H]
+};
+
+// 3-D tile load
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16: A's rows are TMEM lanes, two values a column
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Which queries and keys a CTA works on.
+struct Item {
+  int64_t tok;      // first query token of stream A's tile
+  int64_t tok_end;  // behind the last query token of the sequence
+  int64_t key0;     // row of the sequence's first key
+  int64_t lk;       // its keys
+  int64_t off;      // query token t sees min(lk, t + off) keys (none if that is negative)
+};
+
+__device__ __forceinline__ int64_t visible(const Item& it, int64_t t) {
+  const int64_t n = t + it.off;
+  return n < 0 ? 0 : n < it.lk ? n : it.lk;
+}
+
+// Slots: sequence s owns the slots from cu_q[s] / n + s on, at least as many as it has groups
+// of n tokens, so a slot finds its sequence by a search over cu_q alone, without a plan.  All
+// lanes of a warp search together, 32 probes a round.
+__device__ __forceinline__ bool prompt_item(const PromptArgs& a, int64_t slot, int n, int lane, Item* it) {
+  auto first = [&](int64_t s) { return static_cast<int64_t>(a.cu_q[s]) / n + s; };
+  int64_t lo = 0, hi = a.B;
+  while (true) {
+    const int64_t step = (hi - lo + 31) / 32, s = lo + lane * step;
+    const unsigned ok = __ballot_sync(0xFFFFFFFFu, s < hi && first(s) <= slot);
+    if (ok == 0) return false;
+    lo += (31 - __clz(ok)) * step;
+    if (lo + step < hi) hi = lo + step;
+    if (step == 1) break;
+  }
+  if (!sequence_ok(a, lo)) return false;
+  const int64_t q0 = a.cu_q[lo], q1 = a.cu_q[lo + 1], k0 = a.cu_k[lo], lk = a.cu_k[lo + 1] - k0;
+  const int64_t tile = slot - first(lo);
+  if (tile < 0 || q0 + tile * n >= q1) return false;
+  it->tok = q0 + tile * n;
+  it->tok_end = q1;
+  it->key0 = k0;
+  it->lk = lk;
+  it->off = 1 - q0 + lk - (q1 - q0);
+  return true;
+}
+
+template <bool kPrefix>
+__device__ __forceinline__ bool find_item(const TileParams& p, int64_t slot, int n, int lane, Item* it) {
+  if constexpr (kPrefix) {  // the requests are the tokens, all of them see all keys
+    it->tok = slot * n;
+    it->tok_end = p.a.Tq;
+    it->key0 = 0;
+    it->lk = p.a.Tk;
+    it->off = p.a.Tk;
+    return it->tok < it->tok_end;
+  } else {
+    return prompt_item(p.a, slot, n, lane, it);
+  }
+}
+
+// Key blocks that the tile of n tokens from tok on needs, and the ones of a split.
+__device__ __forceinline__ int tile_blocks(const Item& it, int64_t tok, int n) {
+  if (tok >= it.tok_end) return 0;
+  const int64_t last = tok + n < it.tok_end ? tok + n - 1 : it.tok_end - 1;
+  return static_cast<int>((visible(it, last) + kKeys - 1) / kKeys);
+}
+__device__ __forceinline__ int blocks_per_split(int blocks, int splits) { return (blocks + splits - 1) / splits; }
+
+template <int D, bool kTwo, bool kPrefix>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    attn_tile_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TileParams p) {
+  using Sh = TileShape<D, kTwo>;
+  constexpr int NS = Sh::kStages;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int hk = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.a.Hkv));
+  const int64_t slot = p.nslots - 1 - blockIdx.x / static_cast<unsigned>(p.a.Hkv);
+  const int split = static_cast<int>(blockIdx.y);
+  if constexpr (!kPrefix) {
+    if (blockIdx.x == 0 && split == 0)  // one CTA looks every sequence over
+      for (int64_t s = threadIdx.x; s < p.a.B; s += kTileThreads)
+        if (!sequence_ok(p.a, s)) atomicOr(p.a.err, kErrBadLength);
+  }
+  if ((smem_u32(sm) & 1023u) != 0) {  // the whole CTA leaves before touching anything
+    if (threadIdx.x == 0) atomicOr(p.a.err, kErrBadLaunch);
+    return;
+  }
+  constexpr int kTiles = kTwo ? 2 : 1;
+  Item it;
+  if (!find_item<kPrefix>(p, slot, kTiles * p.nt, lane, &it)) return;  // the same for every warp
+  const int nbA = tile_blocks(it, it.tok, p.nt), nbB = kTwo ? tile_blocks(it, it.tok + p.nt, p.nt) : nbA;
+  const int nb = nbA > nbB ? nbA : nbB;
+  const int per = blocks_per_split(nb, p.splits);
+  const int b0 = split * per;
+  const int cnt = nb - b0 < per ? nb - b0 : per;  // blocks of this CTA (<= 0: none)
+  if (split > 0 && cnt <= 0) return;
+  // blocks of each stream: both tiles walk the same blocks, or one tile's are dealt in turn
+  auto clampn = [](int x, int hi) { return x < 0 ? 0 : x < hi ? x : hi; };
+  const int nA = kTwo ? clampn(nbA - b0, cnt) : (cnt + 1) / 2, nB = kTwo ? clampn(nbB - b0, cnt) : cnt / 2;
+  // rows of the last block behind the sequence's keys
+  const int tail = cnt > 0 && static_cast<int64_t>(b0 + cnt) * kKeys > it.lk
+                       ? static_cast<int>(it.lk - static_cast<int64_t>(b0 + cnt - 1) * kKeys) : kKeys;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::kOffBar);
+  uint64_t* q_full = bars;         // [1]
+  uint64_t* tail_done = bars + 1;  // [1] the last V block's rows behind the keys are zero
+  uint64_t* s_full = bars + 2;     // [2] S of a stream computed (and its earlier P V done)
+  uint64_t* p_full = bars + 4;     // [2] P written, O rescaled: 4 arrivals
+  uint64_t* o_full = bars + 6;     // [2] a stream's last P V done
+  uint64_t* full = bars + 8;       // [NS]
+  uint64_t* empty = bars + 8 + NS; // [NS]
+  uint64_t* end_bar = bars + 8 + 2 * NS;
+  uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(bars + 9 + 2 * NS);
+  int& abort_flag = *reinterpret_cast<int*>(bars + 10 + 2 * NS);
+  static_assert((11 + 2 * NS) * 8 <= 256, "barriers");
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(tail_done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(end_bar, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = tmem_slot;
+  constexpr uint32_t kColO = 256;
+
+  // The ring holds the K and V blocks in the order of their use.  Two tiles: K0 V0 K1 V1 ...;
+  // one tile with two streams: K0 K1 V0 K2 V1 K3 V2 ...  (u: place in that order)
+  auto use_k = [&](int j) { return kTwo ? 2 * j : j < 2 ? j : 2 * j - 1; };
+  auto use_v = [&](int j) { return kTwo ? 2 * j + 1 : j + 2 <= cnt - 1 ? 2 * j + 2 : cnt + j; };
+  if (warp == 8) {
+    // ---------------- loads ----------------
+    bool ok = true;
+    if (lane == 0 && cnt > 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      const uint32_t box = 128u * static_cast<uint32_t>(p.G * p.nt);
+      mbar_arrive_expect_tx(q_full, kTiles * (D / 64) * box);
+      for (int t = 0; t < kTiles; ++t)
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(sm + t * Sh::kTile + c * Sh::kHalf, &tmQ, q_full, 64 * c, hk * p.G,
+                      static_cast<int32_t>(it.tok + t * p.nt));
+      int issued = 0;
+      auto load = [&](int u, bool isK, int j) {
+        const int st = u % NS, turn = u / NS;
+        if (ok && turn > 0) ok = mbar_wait_sleep(&empty[st], static_cast<uint32_t>(turn - 1) & 1, &abort_flag);
+        if (!ok) return;
+        issued = u + 1;
+        mbar_arrive_expect_tx(&full[st], Sh::kStage);
+        const int32_t row = static_cast<int32_t>(it.key0 + static_cast<int64_t>(b0 + j) * kKeys);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(sm + Sh::kOffRing + st * Sh::kStage + c * Sh::kHalf, isK ? &tmK : &tmV, &full[st], 64 * c,
+                      isK ? (p.k_head ? hk : 0) : (p.v_head ? hk : 0), row);
+      };
+      if constexpr (kTwo) {
+        for (int j = 0; j < cnt; ++j) {
+          load(2 * j, true, j);
+          load(2 * j + 1, false, j);
+        }
+      } else {
+        int u = 0;
+        load(u++, true, 0);
+        if (cnt > 1) load(u++, true, 1);
+        for (int j = 0; j < cnt; ++j) {
+          load(u++, false, j);
+          if (j + 2 < cnt) load(u++, true, j + 2);
+        }
+      }
+      if (!ok) report_error(p.a.err, kErrWaitTimeout, &abort_flag);
+      // no copy may still be landing in shared memory when the CTA ends
+      mbar_wait(q_full, 0, nullptr);
+      for (int u = issued > NS ? issued - NS : 0; u < issued; ++u)
+        mbar_wait(&full[u % NS], static_cast<uint32_t>(u / NS) & 1, nullptr);
+    }
+    ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+    if (tail < kKeys && ok) {
+      // a weight of 0 does not silence a NaN behind the sequence: those rows of V become 0
+      const int st = use_v(cnt - 1) % NS;
+      uint8_t* v = sm + Sh::kOffRing + st * Sh::kStage;
+      for (int c = 0; c < D / 64; ++c)
+        for (int i = tail * 8 + lane; i < kKeys * 8; i += 32)
+          reinterpret_cast<uint4*>(v + c * Sh::kHalf)[i] = make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tail_done);
+    }
+  } else if (warp == 9) {
+    // ---------------- MMAs ----------------
+    if (lane == 0 && cnt > 0) {
+      constexpr uint32_t idS = idesc_bf16(kRows, kKeys, 0, 0), idO = idesc_bf16(kRows, D, 0, 1);
+      const uint64_t dQ = sdesc_k_sw128(smem_u32(sm)), dK = sdesc_k_sw128(smem_u32(sm + Sh::kOffRing));
+      const uint64_t dV = sdesc_mn_sw128(smem_u32(sm + Sh::kOffRing), Sh::kHalf, 1024);
+      bool ok = mbar_wait(q_full, 0, &abort_flag);
+      auto wait_use = [&](int u) {
+        ok = ok && mbar_wait(&full[u % NS], static_cast<uint32_t>(u / NS) & 1, &abort_flag);
+        tc_fence_after();
+      };
+      auto issue_s = [&](int s, int j) {  // stream s, block j
+        const int u = use_k(j);
+        wait_use(u);
+        if (!ok) return;
+        const uint64_t a = dQ + static_cast<uint64_t>(((kTwo ? s : 0) * Sh::kTile) >> 4);
+        const uint64_t b = dK + static_cast<uint64_t>(((u % NS) * Sh::kStage) >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t o = static_cast<uint64_t>(((k >> 2) * Sh::kHalf + (k & 3) * 32) >> 4);
+          mma_f16_ss(tbase + s * kKeys, a + o, b + o, idS, k > 0 ? 1u : 0u);
+        }
+        mma_commit(&s_full[s]);
+      };
+      auto issue_pv = [&](int s, int j, int i, bool last) {  // i: the stream's own count of blocks
+        const int u = use_v(j);
+        ok = ok && mbar_wait(&p_full[s], static_cast<uint32_t>(i) & 1, &abort_flag);
+        wait_use(u);
+        if (j == cnt - 1 && tail < kKeys) ok = ok && mbar_wait(tail_done, 0, &abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t b = dV + static_cast<uint64_t>(((u % NS) * Sh::kStage) >> 4);
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 8 columns of P, 16 rows of V
+          mma_f16_ts(tbase + kColO + s * D, tbase + s * kKeys + 8 * k, b + static_cast<uint64_t>(k * (2048 >> 4)), idO,
+                     i > 0 || k > 0 ? 1u : 0u);
+        if (last) mma_commit(&o_full[s]);
+      };
+      auto release = [&](int u) {
+        if (ok) mma_commit(&empty[u % NS]);
+      };
+      if constexpr (kTwo) {
+        if (nA > 0) issue_s(0, 0);
+        if (nB > 0) issue_s(1, 0);
+        release(use_k(0));
+        for (int j = 0; ok && j < cnt; ++j) {
+          if (j < nA) issue_pv(0, j, j, j == nA - 1);
+          if (j + 1 < nA) issue_s(0, j + 1);
+          if (j < nB) issue_pv(1, j, j, j == nB - 1);
+          release(use_v(j));
+          if (j + 1 < nB) issue_s(1, j + 1);
+          if (j + 1 < cnt) release(use_k(j + 1));
+        }
+      } else {
+        issue_s(0, 0);
+        release(use_k(0));
+        if (cnt > 1) {
+          issue_s(1, 1);
+          release(use_k(1));
+        }
+        for (int j = 0; ok && j < cnt; ++j) {
+          issue_pv(j & 1, j, j >> 1, j >= cnt - 2);
+          release(use_v(j));
+          if (j + 2 < cnt) {
+            issue_s(j & 1, j + 2);
+            release(use_k(j + 2));
+          }
+        }
+      }
+      if (!ok) report_error(p.a.err, kErrWaitTimeout, &abort_flag);
+      // every MMA issued has finished before the CTA frees TMEM and shared memory
+      mma_commit(end_bar);
+      mbar_wait(end_bar, 0, nullptr);
+    }
+  } else {
+    // ---------------- softmax, one row a thread ----------------
+    const int s = warp >> 2, qd = warp & 3;
+    const int r = 32 * qd + lane;
+    const uint32_t tl = tbase + (static_cast<uint32_t>(32 * qd) << 16);
+    const uint32_t tS = tl + s * kKeys, tO = tl + kColO + s * D;
+    const int rt = r / p.G;
+    const int64_t tok = it.tok + (kTwo ? s * p.nt : 0) + rt;
+    const bool valid = rt < p.nt && tok < it.tok_end;
+    const int n = s == 0 ? nA : nB;
+    const float sl2 = p.scale_log2;
+    // keys this row sees, counted from the CTA's first block
+    const int64_t seen = (valid ? visible(it, tok) : 0) - static_cast<int64_t>(b0) * kKeys;
+    const int lim = seen < 0 ? 0 : seen > 0x7FFFFF00 ? 0x7FFFFF00 : static_cast<int>(seen);
+    const int whole = __reduce_min_sync(0xFFFFFFFFu, valid ? lim : 0x7FFFFF00);  // the warp's rows see all keys below
+    float ref = -INFINITY, l = 0.0f;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int j = kTwo ? i : 2 * i + s;  // block, counted from b0
+      if (!warp_wait(&s_full[s], static_cast<uint32_t>(i) & 1, &abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t x[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + 32 * c, x[c]);
+      tmem_ld_wait();
+      if ((j + 1) * kKeys > whole) {
+        const int rem = lim - j * kKeys;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * c + e >= rem) x[c][e] = 0xFF800000u;  // -inf
+      }
+      float m4[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        m4[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+        for (int e = 1; e < 32; ++e) m4[c] = fmaxf(m4[c], __uint_as_float(x[c][e]));
+      }
+      const float mn = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
+      const bool resc = mn > ref + kRescaleLog2;  // the first block with a visible key always
+      float alpha = 1.0f;
+      if (resc) {
+        alpha = ex2(ref - mn);  // 0 on the first
+        ref = mn;
+      }
+      const float base = ref == -INFINITY ? 0.0f : ref;  // no key seen so far: every weight is 2^-inf = 0
+      const float2 sc2 = make_float2(sl2, sl2), nb2 = make_float2(-base, -base);
+      float2 sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float2 t = __ffma2_rn(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sc2, nb2);
+          t.x = ex2(t.x);
+          t.y = ex2(t.y);
+          sum2 = __fadd2_rn(sum2, t);
+          pk[e] = pack_bf16(t.x, t.y);
+        }
+        tmem_st_32x32b_x16(tS + 16 * c, pk);
+      }
+      l = fmaf(l, alpha, sum2.x + sum2.y);
+      if (i > 0 && __any_sync(0xFFFFFFFFu, resc)) {
+        // a row's reference moved: scale its O, which holds all earlier P V (they were done
+        // before this S was)
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(tO + c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st_32x32b_x32(tO + c, o);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[s]);
+    }
+    if (ok && n > 0) {
+      ok = warp_wait(&o_full[s], 0, &abort_flag);
+      tc_fence_after();
+    }
+    if (!ok) report_error(p.a.err, kErrWaitTimeout, &abort_flag);
+    bool have = ok && n > 0;  // O holds something
+    float scale = 1.0f;
+    float4* xrow = reinterpret_cast<float4*>(sm + Sh::kOffRing + r * (D * 4 + 16));
+    if constexpr (!kTwo) {
+      // join the two streams: references and sums first, then O through the ring, which both
+      // streams' MMAs and copies have left
+      if (nB > 0) {
+        float2* ml = reinterpret_cast<float2*>(sm + Sh::kOffMl);
+        ml[s * kRows + r] = make_float2(have ? ref : -INFINITY, have ? l : 0.0f);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float2 other = ml[(s ^ 1) * kRows + r];
+        const float top = fmaxf(ref, other.x);
+        scale = ref == -INFINITY ? 0.0f : ex2(ref - top);
+        l = l * scale + (other.x == -INFINITY ? 0.0f : other.y * ex2(other.x - top));
+        ref = top;
+        if (s == 1) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(tO + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              xrow[c / 4 + e] = make_float4(__uint_as_float(o[4 * e]) * scale, __uint_as_float(o[4 * e + 1]) * scale,
+                                            __uint_as_float(o[4 * e + 2]) * scale, __uint_as_float(o[4 * e + 3]) * scale);
+          }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+      }
+    }
+    if (kTwo || s == 0) {
+      const bool final_out = p.splits == 1;
+      const int head = hk * p.G + (r - rt * p.G);
+      const float inv = final_out ? (l > 0.0f || l != l ? scale / l : 0.0f) : scale;
+      const int64_t row = tok * p.a.H + head;
+      uint16_t* orow = p.a.o + tok * p.a.st[6] + head * p.a.st[7];
+      float* prow = p.part_o + (static_cast<int64_t>(split) * p.a.Tq * p.a.H + row) * D;
+      if (!final_out && valid && cnt > 0)
+        p.part_ml[static_cast<int64_t>(split) * p.a.Tq * p.a.H + row] = make_float2(ref, l);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (have) {
+          tmem_ld_32x32b_x32(tO + c, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;  // no key: 0
+        }
+        float f[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
+        if (!kTwo && nB > 0) {
+          const float w = final_out ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 y = xrow[c / 4 + e];
+            f[4 * e] = fmaf(y.x, w, f[4 * e]);
+            f[4 * e + 1] = fmaf(y.y, w, f[4 * e + 1]);
+            f[4 * e + 2] = fmaf(y.z, w, f[4 * e + 2]);
+            f[4 * e + 3] = fmaf(y.w, w, f[4 * e + 3]);
+          }
+        }
+        if (valid) {
+          if (final_out) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              reinterpret_cast<uint4*>(orow + c)[e] =
+                  make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
+                             pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+          } else if (cnt > 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<float4*>(prow + c)[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tbase, 512);
+}
+
+// ---- joining the splits of a row -----------------------------------------------------------
+// o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, one warp a row.
+template <int D, bool kTwo>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ TileParams p) {
+  constexpr int E = D / 32;
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int hk = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.a.Hkv));
+  const int64_t slot = p.nslots - 1 - blockIdx.x / static_cast<unsigned>(p.a.Hkv);
+  const int ntok = (kTwo ? 2 : 1) * p.nt;
+  Item it;
+  if (!prompt_item(p.a, slot, ntok, lane, &it)) return;
+  const int nbA = tile_blocks(it, it.tok, p.nt), nbB = kTwo ? tile_blocks(it, it.tok + p.nt, p.nt) : 0;
+  const int nb = nbA > nbB ? nbA : nbB;
+  const int per = blocks_per_split(nb, p.splits), used = per > 0 ? (nb + per - 1) / per : 0;
+  const int64_t rows = p.a.Tq * p.a.H;
+  for (int r = blockIdx.y * 8 + warp; r < ntok * p.G; r += 8 * gridDim.y) {
+    const int64_t tok = it.tok + r / p.G;
+    if (tok >= it.tok_end) break;
+    const int64_t head = hk * p.G + r % p.G, row = tok * p.a.H + head;
+    float top = -INFINITY;
+    for (int s = lane; s < used; s += 32) top = fmaxf(top, p.part_ml[s * rows + row].x);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    float l = 0.0f, acc[E] = {};
+    if (top != -INFINITY)
+      for (int s = 0; s < used; ++s) {
+        const float2 ml = p.part_ml[s * rows + row];
+        const float w = ex2(ml.x - top);
+        l = fmaf(ml.y, w, l);
+        const float* src = p.part_o + (s * rows + row) * D + E * lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(src[e], w, acc[e]);
+      }
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.a.o + tok * p.a.st[6] + head * p.a.st[7] + E * lane);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
+// ---- host ----------------------------------------------------------------------------------
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn attn_encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+// [tokens][heads][d] bfloat16 with the given strides, loaded as 64 channels x bh heads x bt
+// tokens with 128-byte swizzle.  A dimension of one item gets a stride that any array has.
+bool encode_rows(CUtensorMap* map, const void* ptr, int64_t d, int64_t heads, int64_t tokens, int64_t head_stride,
+                 int64_t tok_stride, int bh, int bt) {
+  EncodeTiledFn enc = attn_encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? head_stride : d) * 2,
+                                 static_cast<cuuint64_t>(tokens > 1 ? tok_stride : d) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(bh), static_cast<cuuint32_t>(bt)}, estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kTwo, bool kPrefix>
+cudaError_t launch_tiles(TileParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  const PromptArgs& a = p.a;
+  CUtensorMap mq, mk, mv;
+  p.k_head = a.Hkv > 1 && a.st[3] > 0;
+  p.v_head = a.Hkv > 1 && a.st[5] > 0;
+  const bool keys = a.Tk > 0;  // without any key nothing is loaded: the maps only have to be valid
+  if (!encode_rows(&mq, a.q, D, a.H, a.Tq, a.st[1], a.st[0], p.G, p.nt) ||
+      !encode_rows(&mk, keys ? a.k : a.q, D, p.k_head ? a.Hkv : 1, keys ? a.Tk : 1, a.st[3], a.st[2], 1, kKeys) ||
+      !encode_rows(&mv, keys ? a.v : a.q, D, p.v_head ? a.Hkv : 1, keys ? a.Tk : 1, a.st[5], a.st[4], 1, kKeys))
+    return cudaErrorInvalidValue;
+  const auto kernel = attn_tile_kernel<D, kTwo, kPrefix>;
+  constexpr uint32_t smem = TileShape<D, kTwo>::kSmem;
+  const cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), smem, dev.device);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(p.nslots * a.Hkv), static_cast<unsigned>(p.splits));
+  kernel<<<grid, kTileThreads, smem, stream>>>(mq, mk, mv, p);
+  return cudaGetLastError();
+}
+
+// How a prompt call is cut up.
+struct PromptPlan {
+  bool two;
+  int64_t nslots;
+  int splits;
+};
+PromptPlan prompt_plan(int64_t B, int64_t Tq, int64_t Tk, int64_t H, int64_t Hkv, const DeviceInfo& dev) {
+  const int64_t nt = kRows / (H / Hkv);
+  PromptPlan pl;
+  pl.two = (Tq / (2 * nt) + 1) * Hkv >= dev.sm_count;
+  const int64_t n = pl.two ? 2 * nt : nt;
+  pl.nslots = Tq / n + B;
+  const int64_t busy = (Tq / n + 1) * Hkv, blocks = (Tk + kKeys - 1) / kKeys;
+  pl.splits = static_cast<int>(std::max<int64_t>(1, std::min(dev.sm_count / busy, blocks / 8)));
+  return pl;
+}
+
+template <int D>
+cudaError_t prompt_attention(const PromptArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+  TileParams p = {};
+  p.a = a;
+  const PromptPlan pl = prompt_plan(a.B, a.Tq, a.Tk, a.H, a.Hkv, dev);
+  p.G = static_cast<int>(a.H / a.Hkv);
+  p.nt = kRows / p.G;
+  p.nslots = pl.nslots;
+  p.splits = pl.splits;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.part_o = static_cast<float*>(a.part);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<int64_t>(pl.splits) * a.Tq * a.H * D);
+  cudaError_t e = pl.two ? launch_tiles<D, true, false>(p, dev, stream) : launch_tiles<D, false, false>(p, dev, stream);
+  if (e != cudaSuccess || pl.splits == 1) return e;
+  const dim3 grid(static_cast<unsigned>(pl.nslots * a.Hkv), 4);
+  if (pl.two) prompt_join_kernel<D, true><<<grid, 256, 0, stream>>>(p);
+  else prompt_join_kernel<D, false><<<grid, 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
-size_t prompt_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, const DeviceInfo&) { return 0; }
+size_t prompt_ws_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t H, int64_t Hkv, int64_t d, const DeviceInfo& dev) {
+  const int64_t splits = prompt_plan(B, Tq, Tk, H, Hkv, dev).splits;
+  return splits == 1 ? 0 : static_cast<size_t>(splits * Tq * H * (d + 2)) * 4;
+}
 size_t prefix_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, const DeviceInfo&) { return 0; }
 
 cudaError_t launch_prompt_attention(PromptArgs a, const DeviceInfo& dev, cudaStream_t stream) {
   if (a.Tq == 0 || a.H == 0 || a.B == 0) return cudaSuccess;
   a.err = dev.err_word;
-  const unsigned grid = static_cast<unsigned>((a.Tq * a.H + 3) / 4);
-  if (a.d == 64) prompt_rows_kernel<64><<<grid, 128, 0, stream>>>(a);
-  else prompt_rows_kernel<128><<<grid, 128, 0, stream>>>(a);
-  return cudaGetLastError();
+  return a.d == 64 ? prompt_attention<64>(a, dev, stream) : prompt_attention<128>(a, dev, stream);
 }
 
 cudaError_t launch_prefix_attention(PrefixArgs a, const DeviceInfo& dev, cudaStream_t stream) {

@@ -75,26 +75,6 @@ struct BsaParams {
   uint32_t* err;
 };
 
-// tcgen05 instruction descriptor, kind::f16 with bfloat16 A and B, f32 D; A and B K-major,
-// or (a_mn, b_mn) MN-major.
-__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) |
-         ((M >> 4) << 24);
-}
-
-// Shared-memory descriptor of an MN-major operand with 128-byte swizzle: 64-element-wide
-// atoms of 8 K rows (1024 bytes); lbo = byte stride between atoms along MN, sbo = between
-// 8-row groups along K.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
 // 16 TMEM lanes x 32 columns, twice: thread i < 16 gets lane (base + i), columns
 // col .. col+31; thread i >= 16 gets lane (base + i - 16), columns col+kSplit .. +31.
 template <int kSplit>
@@ -128,17 +108,6 @@ __device__ __forceinline__ void tmem_st_16x32bx2_x32(uint32_t taddr, const uint3
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_wait() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// 2^x on the special-function unit (hardware approximation, subnormals flushed; 2^-inf = 0)
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -148,11 +117,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ int listed_block(const int32_t* col_idx, int64_t e, int qb) {
   const int kb = __ldg(col_idx + e);
   return (kb >= 0 && kb <= qb) ? kb : -1;
-}
-
-// every lane of the warp waits; the warp leaves together if any lane's wait gave up
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
 }
 
 __global__ void __launch_bounds__(kThreads, 2)

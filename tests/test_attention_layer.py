@@ -84,7 +84,8 @@ def test_prompt_attention_rejects_bad_arguments(L):
     assert call(_3=P(FAKE + 2)) == ALIGN and call(_4=P(FAKE + 1)) == ALIGN
     # strides: negative, too long for the tile copies, not whole 16-byte pieces, rows of o that overlap
     ok = dict(_0=512, _1=128, _2=256, _3=128, _4=256, _5=128, _6=512, _7=128)
-    for bad, want in ((dict(_0=-512), SHAPE), (dict(_2=1 << 38), SHAPE), (dict(_3=132), ALIGN), (dict(_0=4), ALIGN),
+    for bad, want in ((dict(_0=-512), SHAPE), (dict(_0=0), SHAPE), (dict(_4=0), SHAPE), (dict(_1=0), SHAPE),
+                      (dict(_2=1 << 38), SHAPE), (dict(_3=132), ALIGN), (dict(_0=4), ALIGN),
                       (dict(_6=0), SHAPE), (dict(_6=504), SHAPE), (dict(_7=64), SHAPE), (dict(_6=128, _7=1272), SHAPE)):
         assert call(_13=_strides(8, **{**ok, **bad})) == want, bad
     if not torch.cuda.is_available():  # these arguments pass: o with each head's tokens together
