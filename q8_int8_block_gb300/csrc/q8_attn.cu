@@ -19,69 +19,16 @@ namespace {
 
 constexpr uint32_t kErrBadLength = 1u << 9;  // a sequence or cache length outside its array
 
-__device__ __forceinline__ float bf16_f32(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
-
 // whether sequence s lies inside the arrays
 __device__ __forceinline__ bool sequence_ok(const PromptArgs& a, int64_t s) {
   const int64_t q0 = a.cu_q[s], q1 = a.cu_q[s + 1], k0 = a.cu_k[s], k1 = a.cu_k[s + 1];
   return 0 <= q0 && q0 <= q1 && q1 <= a.Tq && 0 <= k0 && k0 <= k1 && k1 <= a.Tk;
 }
 
-template <int D>
-struct Row {
-  static constexpr int E = D / 32;
-  float q[E], o[E], m, l;
-
-  __device__ void begin(const uint16_t* src, float scale, int lane) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      q[i] = bf16_f32(src[E * lane + i]) * scale;
-      o[i] = 0.0f;
-    }
-    m = -INFINITY;
-    l = 0.0f;
-  }
-
-  __device__ void attend(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, int64_t n,
-                         int lane) {
-    for (int64_t j = 0; j < n; ++j) {
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < E; ++i) s = fmaf(q[i], bf16_f32(k[j * k_stride + E * lane + i]), s);
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-      const float mn = fmaxf(m, s), a = __expf(m - mn), p = __expf(s - mn);
-      l = fmaf(l, a, p);
-#pragma unroll
-      for (int i = 0; i < E; ++i) o[i] = fmaf(o[i], a, p * bf16_f32(v[j * v_stride + E * lane + i]));
-      m = mn;
-    }
-  }
-
-  __device__ void end(uint16_t* dst, int lane) {
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) dst[E * lane + i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
-  }
-};
-
-template <int D>
-__global__ void __launch_bounds__(128) prefix_rows_kernel(const PrefixArgs a) {
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) / 32;
-  const int lane = threadIdx.x & 31;
-  if (row >= a.B * a.H) return;
-  const int64_t b = row / a.H, h = row - b * a.H, hk = h / (a.H / a.Hkv);
-  int64_t n = a.own_len[b];
-  if (n < 0 || n > a.cap) {
-    if (lane == 0) atomicOr(a.err, kErrBadLength);
-    n = n < 0 ? 0 : a.cap;
-  }
-  Row<D> r;
-  r.begin(a.q + b * a.st[0] + h * a.st[1], a.scale, lane);
-  r.attend(a.kp + hk * a.st[3], a.vp + hk * a.st[5], a.st[2], a.st[4], a.P, lane);
-  r.attend(a.ko + b * a.st[6] + hk * a.st[8], a.vo + b * a.st[9] + hk * a.st[11], a.st[7], a.st[10], n, lane);
-  r.end(a.o + b * a.st[12] + h * a.st[13], lane);
+__device__ __forceinline__ void pdl_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- the tile kernel ---------------------------------------------------------------------
 constexpr int kRows = 128;     // query rows of a tile: 128 / G tokens x G heads
@@ -114,7 +61,8 @@ struct TileParams {
   PromptArgs a;            // strides of q, k, v, o; for the prefix B, Tq are the requests and Tk is P
   int G, nt;               // heads of a group, tokens of a tile
   int64_t nslots;
-  int splits;              // blocks of keys are dealt to this many CTAs; 1: o is written here
+  int splits;              // blocks of keys are dealt to this many CTAs
+  int to_parts;            // 0: o is written here (one split), 1: partial results
   int k_head, v_head;      // 0: all key / value heads are one (stride 0)
   float scale_log2;
   float* part_o;           // [splits][Tq * H][D]
@@ -210,6 +158,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TileParams p) {
   using Sh = TileShape<D, kTwo>;
   constexpr int NS = Sh::kStages;
+  if constexpr (kPrefix) pdl_launch_dependents();  // the requests' own keys may start
   extern __shared__ __align__(1024) uint8_t sm[];
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int hk = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.a.Hkv));
@@ -534,7 +483,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
     if (kTwo || s == 0) {
-      const bool final_out = p.splits == 1;
+      const bool final_out = p.to_parts == 0;
       const int head = hk * p.G + (r - rt * p.G);
       const float inv = final_out ? (l > 0.0f || l != l ? scale / l : 0.0f) : scale;
       const int64_t row = tok * p.a.H + head;
@@ -627,6 +576,273 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
   }
 }
 
+// ---- the requests' own keys ---------------------------------------------------------------
+// Few rows (the G heads of one request) over keys that no other request reads: bound by the
+// bytes of the cache.  One CTA for a request, a key/value head, 16 of its query heads and a
+// range of keys; each of its four warps walks 16-key pieces of that range by itself (pieces w,
+// w + 4, ...) with a ring of asynchronous copies of its own, so the loop has no barrier, and
+// three CTAs on an SM keep 192 KB in flight.  The products run on mma.sync: 16 rows are all
+// there is, and the tensor pipe is not what bounds this.  Rows behind the request's keys are
+// not read (zeros are filled in).
+constexpr int kOwnWarps = 4, kOwnKeys = 16, kOwnStages = 2, kOwnRows = 16;
+
+struct OwnParams {
+  PrefixArgs a;
+  int G, chunks;   // heads of a group; 16-head chunks of it
+  int splits;      // at most so many CTAs share a request's keys
+  int prefix_splits, prefix_used;  // partial results of the prefix: allocated, written
+  float scale_log2;
+  float* part_o;    // [prefix_splits + splits][B * H][D]
+  float2* part_ml;
+};
+
+template <int D>
+struct OwnShape {
+  static constexpr int kPiece = kOwnKeys * D * 2;                 // K or V of a piece
+  static constexpr int kWarp = kOwnStages * 2 * kPiece;           // a warp's ring
+  static constexpr int kSmem = kOwnWarps * kWarp;
+  static constexpr int kPad = D + 4;                              // floats of an exchanged row
+  static_assert(kWarp >= kOwnRows * kPad * 4, "exchange buffer");
+};
+
+// Keys of a split of a request with n keys (whole pieces for every warp).
+__device__ __forceinline__ int64_t own_per_split(int64_t n, int splits) {
+  constexpr int64_t kUnit = kOwnWarps * kOwnKeys;
+  const int64_t per = (n + splits - 1) / splits;
+  return (per + kUnit - 1) / kUnit * kUnit;
+}
+
+__device__ __forceinline__ int64_t own_length(const PrefixArgs& a, int64_t b) {
+  const int64_t n = a.own_len[b];
+  return n < 0 ? 0 : n < a.cap ? n : a.cap;
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <int D>
+__global__ void __launch_bounds__(32 * kOwnWarps, 3) attn_own_kernel(const __grid_constant__ OwnParams p) {
+  using Sh = OwnShape<D>;
+  constexpr int KS = D / 16, C16 = D / 8;  // k steps of a score; 16-byte chunks of a row
+  pdl_launch_dependents();
+  extern __shared__ __align__(1024) uint8_t sm[];
+  __shared__ float2 ml_s[kOwnWarps][kOwnRows];
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int g = lane >> 2, t = lane & 3;
+  const PrefixArgs& a = p.a;
+  const int64_t per_b = a.Hkv * p.chunks;
+  const int64_t b = blockIdx.x / per_b;
+  const int rem = static_cast<int>(blockIdx.x - b * per_b);
+  const int hk = rem / p.chunks, chunk = rem - hk * p.chunks, split = static_cast<int>(blockIdx.y);
+  const int64_t n = own_length(a, b), per = own_per_split(n, p.splits);
+  if (threadIdx.x == 0 && rem == 0 && split == 0 && n != a.own_len[b]) atomicOr(a.err, kErrBadLength);
+  const int64_t k0 = split * per, k1 = k0 + per < n ? k0 + per : n;
+  const bool direct = p.splits == 1 && p.prefix_splits == 0;  // nothing to join: o is written here
+  if (k0 >= k1 && !(direct && split == 0)) {
+    pdl_wait();
+    return;
+  }
+  const int nrows = p.G - chunk * kOwnRows < kOwnRows ? p.G - chunk * kOwnRows : kOwnRows;
+  const int64_t head0 = static_cast<int64_t>(hk) * p.G + chunk * kOwnRows;
+  const int npieces = static_cast<int>((k1 - k0 + kOwnKeys - 1) / kOwnKeys);
+  const int mine = npieces > warp ? (npieces - warp + kOwnWarps - 1) / kOwnWarps : 0;
+  uint8_t* ring = sm + warp * Sh::kWarp;
+  const uint16_t* kbase = a.ko + b * a.st[6] + hk * a.st[8];
+  const uint16_t* vbase = a.vo + b * a.st[9] + hk * a.st[11];
+  auto load = [&](int i) {  // the warp's i-th piece
+    if (i < mine) {
+      uint8_t* dst = ring + (i % kOwnStages) * 2 * Sh::kPiece;
+      const int64_t key = k0 + static_cast<int64_t>(warp + i * kOwnWarps) * kOwnKeys;
+#pragma unroll
+      for (int c = lane; c < kOwnKeys * C16; c += 32) {
+        const int row = c / C16, col = c % C16;
+        const bool on = key + row < k1;
+        const int64_t at = on ? key + row : k0;
+        const int off = row * D * 2 + ((col ^ (row & 7)) << 4);
+        cp_async16(dst + off, kbase + at * a.st[7] + 8 * col, on);
+        cp_async16(dst + Sh::kPiece + off, vbase + at * a.st[10] + 8 * col, on);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kOwnStages; ++i) load(i);
+  // Q: rows g and g + 8 of the 16, zeros behind the group
+  uint32_t q[KS][4];
+  {
+    const uint16_t* q0 = a.q + b * a.st[0] + (head0 + g) * a.st[1] + 2 * t;
+    const uint16_t* q8 = q0 + 8 * a.st[1];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      q[k][0] = g < nrows ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k) : 0u;
+      q[k][1] = g + 8 < nrows ? *reinterpret_cast<const uint32_t*>(q8 + 16 * k) : 0u;
+      q[k][2] = g < nrows ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k + 8) : 0u;
+      q[k][3] = g + 8 < nrows ? *reinterpret_cast<const uint32_t*>(q8 + 16 * k + 8) : 0u;
+    }
+  }
+  float o[D / 8][4] = {};
+  float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  const float sl2 = p.scale_log2;
+  // a lane's row in an ldmatrix of four 8 x 8 matrices: keys (lane & 7) + 8 [bit], chunk [bit]
+  const int krow = (lane & 7) + ((lane >> 4) << 3), kbit = (lane >> 3) & 1;   // K: matrices (k lo, k hi) x keys
+  const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vbit = lane >> 4;   // V: matrices (keys lo, hi) x channels
+  for (int i = 0; i < mine; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kOwnStages - 1) : "memory");
+    __syncwarp();
+    const uint32_t ks = smem_u32(ring + (i % kOwnStages) * 2 * Sh::kPiece), vs = ks + Sh::kPiece;
+    float s[2][4] = {};
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      uint32_t r[4];
+      ldmatrix_x4(r, ks + krow * D * 2 + (((2 * k + kbit) ^ (krow & 7)) << 4));
+      mma_16816(s[0], q[k], r[0], r[1]);
+      mma_16816(s[1], q[k], r[2], r[3]);
+    }
+    const int64_t left = k1 - (k0 + static_cast<int64_t>(warp + i * kOwnWarps) * kOwnKeys);
+    if (left < kOwnKeys) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (8 * x + 2 * t + (e & 1) >= left) s[x][e] = -INFINITY;
+    }
+    float alpha[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float m = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)) * sl2;
+      alpha[h] = 1.0f;
+      if (m > ref[h]) {  // a piece holds a visible key, so the reference is finite from the first on
+        alpha[h] = ex2(ref[h] - m);
+        ref[h] = m;
+      }
+    }
+    uint32_t pa[4];
+    float w[2][4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[x][e] = ex2(fmaf(s[x][e], sl2, -ref[e >> 1]));
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      l[h] = fmaf(l[h], alpha[h], (w[0][2 * h] + w[0][2 * h + 1]) + (w[1][2 * h] + w[1][2 * h + 1]));
+    pa[0] = pack_bf16(w[0][0], w[0][1]);
+    pa[1] = pack_bf16(w[0][2], w[0][3]);
+    pa[2] = pack_bf16(w[1][0], w[1][1]);
+    pa[3] = pack_bf16(w[1][2], w[1][3]);
+    if (__any_sync(0xFFFFFFFFu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[c][e] *= alpha[e >> 1];
+    }
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t r[4];
+      ldmatrix_x4_trans(r, vs + vrow * D * 2 + (((2 * c + vbit) ^ (vrow & 7)) << 4));
+      mma_16816(o[2 * c], pa, r[0], r[1]);
+      mma_16816(o[2 * c + 1], pa, r[2], r[3]);
+    }
+    __syncwarp();  // every lane has read the stage
+    load(i + kOwnStages);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  // the warps' results meet in shared memory, each in its own ring
+  float* mineo = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
+    if (t == 0) ml_s[warp][g + 8 * h] = make_float2(ref[h], l[h]);
+    if (g + 8 * h < nrows) {
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+        *reinterpret_cast<float2*>(mineo + (g + 8 * h) * Sh::kPad + 8 * c + 2 * t) = make_float2(o[c][2 * h], o[c][2 * h + 1]);
+    }
+  }
+  __syncthreads();
+  constexpr int E = D / 32;
+  for (int r = warp; r < nrows; r += kOwnWarps) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kOwnWarps; ++w) top = fmaxf(top, ml_s[w][r].x);
+    float sum = 0.0f, acc[E] = {};
+#pragma unroll
+    for (int w = 0; w < kOwnWarps; ++w) {
+      const float2 ml = ml_s[w][r];
+      const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
+      if (f == 0.0f && ml.y == 0.0f) continue;  // a warp without a piece
+      sum = fmaf(ml.y, f, sum);
+      const float* src = reinterpret_cast<const float*>(sm + w * Sh::kWarp) + r * Sh::kPad + E * lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(src[e], f, acc[e]);
+    }
+    const int64_t head = head0 + r, row = b * a.H + head;
+    if (direct) {
+      const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + b * a.st[12] + head * a.st[13] + E * lane);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    } else {
+      const int64_t at = static_cast<int64_t>(p.prefix_splits + split) * a.B * a.H + row;
+      if (lane == 0) p.part_ml[at] = make_float2(top, sum);
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<float2*>(p.part_o + at * D + E * lane + e) = make_float2(acc[e], acc[e + 1]);
+    }
+  }
+  pdl_wait();  // the join waits for this kernel only: it has to end after the prefix's
+}
+
+// A row's partial results: the splits of the prefix, then those of the request's own keys.
+template <int D>
+__global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant__ OwnParams p) {
+  constexpr int E = D / 32;
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const PrefixArgs& a = p.a;
+  const int64_t rows = a.B * a.H, row = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) / 32;
+  if (row >= rows) return;
+  const int64_t b = row / a.H, head = row - b * a.H;
+  const int64_t n = own_length(a, b), per = own_per_split(n, p.splits);
+  const int own = per > 0 ? static_cast<int>((n + per - 1) / per) : 0, used = p.prefix_used + own;
+  auto place = [&](int s) { return (s < p.prefix_used ? s : p.prefix_splits + s - p.prefix_used) * rows + row; };
+  pdl_wait();
+  float top = -INFINITY;
+  for (int s = lane; s < used; s += 32) top = fmaxf(top, p.part_ml[place(s)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  float l = 0.0f, acc[E] = {};
+  for (int s = 0; s < used; ++s) {
+    const int64_t at = place(s);
+    const float2 ml = p.part_ml[at];
+    const float w = ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : ex2(ml.x - top);
+    l = fmaf(ml.y, w, l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(p.part_o[at * D + E * lane + e], w, acc[e]);
+  }
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + b * a.st[12] + head * a.st[13] + E * lane);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+}
+
 // ---- host ----------------------------------------------------------------------------------
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -708,6 +924,7 @@ cudaError_t prompt_attention(const PromptArgs& a, const DeviceInfo& dev, cudaStr
   p.nt = kRows / p.G;
   p.nslots = pl.nslots;
   p.splits = pl.splits;
+  p.to_parts = pl.splits > 1;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.part_o = static_cast<float*>(a.part);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<int64_t>(pl.splits) * a.Tq * a.H * D);
@@ -719,13 +936,110 @@ cudaError_t prompt_attention(const PromptArgs& a, const DeviceInfo& dev, cudaStr
   return cudaGetLastError();
 }
 
+// How a prefix call is cut up.
+struct PrefixPlan {
+  bool two;                   // two tiles of requests a block
+  int64_t nslots;
+  int prefix_splits, prefix_used, own_splits, chunks;
+  bool direct() const { return prefix_splits == 0 && own_splits == 1; }
+  size_t partials() const { return direct() ? 0 : static_cast<size_t>(prefix_splits + own_splits); }
+};
+PrefixPlan prefix_plan(int64_t B, int64_t P, int64_t cap, int64_t H, int64_t Hkv, const DeviceInfo& dev) {
+  const int64_t G = H / Hkv, nt = kRows / G;
+  PrefixPlan pl;
+  pl.two = B > nt;
+  const int64_t n = pl.two ? 2 * nt : nt, blocks = (P + kKeys - 1) / kKeys;
+  pl.nslots = (B + n - 1) / n;
+  pl.prefix_splits = 0;
+  pl.prefix_used = 0;
+  if (P > 0) {
+    const int64_t s = std::max<int64_t>(1, std::min(dev.sm_count / (pl.nslots * Hkv), blocks / 2));
+    const int64_t per = (blocks + s - 1) / s;
+    pl.prefix_splits = pl.prefix_used = static_cast<int>((blocks + per - 1) / per);
+  }
+  pl.chunks = static_cast<int>((G + kOwnRows - 1) / kOwnRows);
+  const int64_t busy = B * Hkv * pl.chunks;
+  pl.own_splits = static_cast<int>(std::max<int64_t>(1, std::min(3 * dev.sm_count / busy, cap / 256)));
+  return pl;
+}
+
+template <typename K, typename... A>
+cudaError_t launch_dependent(K kernel, dim3 grid, unsigned threads, size_t smem, bool dependent, cudaStream_t stream,
+                             const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D>
+cudaError_t prefix_attention(const PrefixArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+  const PrefixPlan pl = prefix_plan(a.B, a.P, a.cap, a.H, a.Hkv, dev);
+  float* part_o = static_cast<float*>(a.part);
+  float2* part_ml = reinterpret_cast<float2*>(part_o + pl.partials() * a.B * a.H * D);
+  const float scale_log2 = a.scale * 1.4426950408889634f;
+  const int G = static_cast<int>(a.H / a.Hkv);
+  cudaError_t e;
+  if (a.P > 0) {
+    TileParams t = {};
+    t.a.q = a.q;
+    t.a.k = a.kp;
+    t.a.v = a.vp;
+    t.a.B = 1;
+    t.a.Tq = a.B;
+    t.a.Tk = a.P;
+    t.a.H = a.H;
+    t.a.Hkv = a.Hkv;
+    t.a.d = D;
+    std::copy(a.st, a.st + 6, t.a.st);
+    t.a.err = a.err;
+    t.G = G;
+    t.nt = kRows / G;
+    t.nslots = pl.nslots;
+    t.splits = pl.prefix_splits;
+    t.to_parts = 1;
+    t.scale_log2 = scale_log2;
+    t.part_o = part_o;
+    t.part_ml = part_ml;
+    e = pl.two ? launch_tiles<D, true, true>(t, dev, stream) : launch_tiles<D, false, true>(t, dev, stream);
+    if (e != cudaSuccess) return e;
+  }
+  OwnParams p = {};
+  p.a = a;
+  p.G = G;
+  p.chunks = pl.chunks;
+  p.splits = pl.own_splits;
+  p.prefix_splits = pl.prefix_splits;
+  p.prefix_used = pl.prefix_used;
+  p.scale_log2 = scale_log2;
+  p.part_o = part_o;
+  p.part_ml = part_ml;
+  constexpr int smem = OwnShape<D>::kSmem;
+  e = ensure_smem(reinterpret_cast<const void*>(attn_own_kernel<D>), smem, dev.device);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(attn_own_kernel<D>,
+                       dim3(static_cast<unsigned>(a.B * a.Hkv * pl.chunks), static_cast<unsigned>(pl.own_splits)),
+                       32 * kOwnWarps, smem, a.P > 0, stream, p);
+  if (e != cudaSuccess || pl.direct()) return e;
+  return launch_dependent(prefix_join_kernel<D>, dim3(static_cast<unsigned>((a.B * a.H + 3) / 4)), 128, 0, true, stream, p);
+}
+
 }  // namespace
 
 size_t prompt_ws_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t H, int64_t Hkv, int64_t d, const DeviceInfo& dev) {
   const int64_t splits = prompt_plan(B, Tq, Tk, H, Hkv, dev).splits;
   return splits == 1 ? 0 : static_cast<size_t>(splits * Tq * H * (d + 2)) * 4;
 }
-size_t prefix_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, const DeviceInfo&) { return 0; }
+size_t prefix_ws_bytes(int64_t B, int64_t P, int64_t cap, int64_t H, int64_t Hkv, int64_t d, const DeviceInfo& dev) {
+  return prefix_plan(B, P, cap, H, Hkv, dev).partials() * static_cast<size_t>(B * H * (d + 2)) * 4;
+}
 
 cudaError_t launch_prompt_attention(PromptArgs a, const DeviceInfo& dev, cudaStream_t stream) {
   if (a.Tq == 0 || a.H == 0 || a.B == 0) return cudaSuccess;
@@ -736,10 +1050,7 @@ cudaError_t launch_prompt_attention(PromptArgs a, const DeviceInfo& dev, cudaStr
 cudaError_t launch_prefix_attention(PrefixArgs a, const DeviceInfo& dev, cudaStream_t stream) {
   if (a.B == 0 || a.H == 0) return cudaSuccess;
   a.err = dev.err_word;
-  const unsigned grid = static_cast<unsigned>((a.B * a.H + 3) / 4);
-  if (a.d == 64) prefix_rows_kernel<64><<<grid, 128, 0, stream>>>(a);
-  else prefix_rows_kernel<128><<<grid, 128, 0, stream>>>(a);
-  return cudaGetLastError();
+  return a.d == 64 ? prefix_attention<64>(a, dev, stream) : prefix_attention<128>(a, dev, stream);
 }
 
 }  // namespace q8
