@@ -33,7 +33,8 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // ---- the tile kernel ---------------------------------------------------------------------
 constexpr int kRows = 128;     // query rows of a tile: 128 / G tokens x G heads
 constexpr int kKeys = 128;     // keys of a block
-constexpr int kTileThreads = 320;  // warps 0-3 and 4-7: softmax of streams A and B; 8 loads; 9 MMAs
+constexpr int kSoftWarps = 16;  // softmax: 8 warps a stream, two (a half of the keys each) for 32 rows
+constexpr int kTileThreads = 32 * (kSoftWarps + 2);  // and one warp for the loads, one for the MMAs
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -49,8 +50,8 @@ struct TileShape {
   static constexpr uint32_t kHalf = kKeys * 128;             // 64 channels of 128 rows
   static constexpr int kStages = D == 128 ? (kTwo ? 5 : 6) : 8;
   static constexpr uint32_t kOffRing = (kTwo ? 2 : 1) * kTile;
-  static constexpr uint32_t kOffMl = kOffRing + kStages * kStage;  // (reference, sum) of each row, both streams
-  static constexpr uint32_t kOffBar = kOffMl + 2 * kRows * 8;
+  static constexpr uint32_t kOffMax = kOffRing + kStages * kStage;  // float [2 streams][2 halves][rows]
+  static constexpr uint32_t kOffBar = kOffMax + 4 * kRows * 4;
   static constexpr uint32_t kSmem = kOffBar + 256;
   static_assert(kSmem <= 227 * 1024, "shared memory of a block");
   // the one-tile form joins its two streams through the ring
@@ -79,6 +80,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// true on one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], kind::f16: A's rows are TMEM lanes, two values a column
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -88,6 +96,34 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// A value that is the same on all lanes, told to the compiler as such: the MMA warp's loop and
+// its descriptors then stay in uniform registers.  Without it each MMA took ~90 cycles to issue
+// next to the softmax warps, with it the tensor pipe's 64.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+// A test of a barrier's phase that does not suspend: polling with it sees a phase complete about
+// 100 cycles sooner than try_wait does.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// warp_wait that polls (bounded as mbar_wait)
+__device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (!__all_sync(0xFFFFFFFFu, mbar_test(bar, parity)))
+    if (__any_sync(0xFFFFFFFFu, *abort_flag != 0 || clock64() - t0 > kWaitBudgetCycles)) return false;
+  return true;
 }
 
 // Which queries and keys a CTA works on.
@@ -160,7 +196,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   constexpr int NS = Sh::kStages;
   if constexpr (kPrefix) pdl_launch_dependents();  // the requests' own keys may start
   extern __shared__ __align__(1024) uint8_t sm[];
-  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = static_cast<int>(threadIdx.x & 31);
   const int hk = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.a.Hkv));
   const int64_t slot = p.nslots - 1 - blockIdx.x / static_cast<unsigned>(p.a.Hkv);
   const int split = static_cast<int>(blockIdx.y);
@@ -176,7 +212,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   constexpr int kTiles = kTwo ? 2 : 1;
   Item it;
   if (!find_item<kPrefix>(p, slot, kTiles * p.nt, lane, &it)) return;  // the same for every warp
-  const int nbA = tile_blocks(it, it.tok, p.nt), nbB = kTwo ? tile_blocks(it, it.tok + p.nt, p.nt) : nbA;
+  const int nbA = uniform(tile_blocks(it, it.tok, p.nt)), nbB = kTwo ? uniform(tile_blocks(it, it.tok + p.nt, p.nt)) : nbA;
   const int nb = nbA > nbB ? nbA : nbB;
   const int per = blocks_per_split(nb, p.splits);
   const int b0 = split * per;
@@ -186,14 +222,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto clampn = [](int x, int hi) { return x < 0 ? 0 : x < hi ? x : hi; };
   const int nA = kTwo ? clampn(nbA - b0, cnt) : (cnt + 1) / 2, nB = kTwo ? clampn(nbB - b0, cnt) : cnt / 2;
   // rows of the last block behind the sequence's keys
-  const int tail = cnt > 0 && static_cast<int64_t>(b0 + cnt) * kKeys > it.lk
-                       ? static_cast<int>(it.lk - static_cast<int64_t>(b0 + cnt - 1) * kKeys) : kKeys;
+  const int tail = uniform(cnt > 0 && static_cast<int64_t>(b0 + cnt) * kKeys > it.lk
+                               ? static_cast<int>(it.lk - static_cast<int64_t>(b0 + cnt - 1) * kKeys) : kKeys);
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::kOffBar);
   uint64_t* q_full = bars;         // [1]
   uint64_t* tail_done = bars + 1;  // [1] the last V block's rows behind the keys are zero
   uint64_t* s_full = bars + 2;     // [2] S of a stream computed (and its earlier P V done)
-  uint64_t* p_full = bars + 4;     // [2] P written, O rescaled: 4 arrivals
+  uint64_t* p_full = bars + 4;     // [2] P written, O rescaled: an arrival of each warp
   uint64_t* o_full = bars + 6;     // [2] a stream's last P V done
   uint64_t* full = bars + 8;       // [NS]
   uint64_t* empty = bars + 8 + NS; // [NS]
@@ -206,7 +242,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     mbar_init(tail_done, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], kSoftWarps / 2);
       mbar_init(&o_full[i], 1);
     }
     for (int i = 0; i < NS; ++i) {
@@ -217,21 +253,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 9) {
+  if (warp == kSoftWarps + 1) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = tmem_slot;
+  const uint32_t tbase = static_cast<uint32_t>(uniform(static_cast<int>(tmem_slot)));
   constexpr uint32_t kColO = 256;
 
   // The ring holds the K and V blocks in the order of their use.  Two tiles: K0 V0 K1 V1 ...;
   // one tile with two streams: K0 K1 V0 K2 V1 K3 V2 ...  (u: place in that order)
   auto use_k = [&](int j) { return kTwo ? 2 * j : j < 2 ? j : 2 * j - 1; };
   auto use_v = [&](int j) { return kTwo ? 2 * j + 1 : j + 2 <= cnt - 1 ? 2 * j + 2 : cnt + j; };
-  if (warp == 8) {
+  if (warp == kSoftWarps) {
     // ---------------- loads ----------------
     bool ok = true;
     if (lane == 0 && cnt > 0) {
@@ -288,23 +324,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(tail_done);
     }
-  } else if (warp == 9) {
+  } else if (warp == kSoftWarps + 1) {
     // ---------------- MMAs ----------------
-    if (lane == 0 && cnt > 0) {
+    // the whole warp walks the loop, so that descriptors stay in uniform registers; one lane issues
+    if (cnt > 0) {
+      const bool leader = elect_one();
       constexpr uint32_t idS = idesc_bf16(kRows, kKeys, 0, 0), idO = idesc_bf16(kRows, D, 0, 1);
       const uint64_t dQ = sdesc_k_sw128(smem_u32(sm)), dK = sdesc_k_sw128(smem_u32(sm + Sh::kOffRing));
       const uint64_t dV = sdesc_mn_sw128(smem_u32(sm + Sh::kOffRing), Sh::kHalf, 1024);
-      bool ok = mbar_wait(q_full, 0, &abort_flag);
-      auto wait_use = [&](int u) {
-        ok = ok && mbar_wait(&full[u % NS], static_cast<uint32_t>(u / NS) & 1, &abort_flag);
-        tc_fence_after();
+      bool ok = warp_wait(q_full, 0, &abort_flag);
+      auto landed = [&](int u) { ok = ok && warp_poll(&full[u % NS], static_cast<uint32_t>(u / NS) & 1, &abort_flag); };
+      // several at once: one latency where all are there, which is the rule for loads
+      auto all_there = [&](int u0, int u1, int s, int i) {
+        const bool there = mbar_test(&full[u0 % NS], static_cast<uint32_t>(u0 / NS) & 1) &
+                           mbar_test(&full[u1 % NS], static_cast<uint32_t>(u1 / NS) & 1) &
+                           mbar_test(&p_full[s], static_cast<uint32_t>(i) & 1);
+        if (__all_sync(0xFFFFFFFFu, there)) return;
+        landed(u0);
+        landed(u1);
+        ok = ok && warp_poll(&p_full[s], static_cast<uint32_t>(i) & 1, &abort_flag);
       };
-      auto issue_s = [&](int s, int j) {  // stream s, block j
-        const int u = use_k(j);
-        wait_use(u);
-        if (!ok) return;
+      auto issue_s = [&](int s, int j) {  // stream s, block j, whose K has landed
         const uint64_t a = dQ + static_cast<uint64_t>(((kTwo ? s : 0) * Sh::kTile) >> 4);
-        const uint64_t b = dK + static_cast<uint64_t>(((u % NS) * Sh::kStage) >> 4);
+        const uint64_t b = dK + static_cast<uint64_t>(((use_k(j) % NS) * Sh::kStage) >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint64_t o = static_cast<uint64_t>(((k >> 2) * Sh::kHalf + (k & 3) * 32) >> 4);
@@ -312,62 +354,72 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         mma_commit(&s_full[s]);
       };
-      auto issue_pv = [&](int s, int j, int i, bool last) {  // i: the stream's own count of blocks
-        const int u = use_v(j);
-        ok = ok && mbar_wait(&p_full[s], static_cast<uint32_t>(i) & 1, &abort_flag);
-        wait_use(u);
-        if (j == cnt - 1 && tail < kKeys) ok = ok && mbar_wait(tail_done, 0, &abort_flag);
+      auto issue_pv = [&](int s, int j, bool first) {  // 16 keys a step: 8 columns of P, 16 rows of V
+        const uint64_t b = dV + static_cast<uint64_t>(((use_v(j) % NS) * Sh::kStage) >> 4);
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)  // the second 64 keys' P begins at column 64
+          mma_f16_ts(tbase + kColO + s * D, tbase + s * kKeys + 8 * k + (k >= 4 ? 32 : 0),
+                     b + static_cast<uint64_t>(k * (2048 >> 4)), idO, k > 0 || !first ? 1u : 0u);
+      };
+      // P V of block j (the stream's i-th) and, in the same go, S of the stream's next block
+      auto turn = [&](int s, int j, int i, int next, bool more, bool release_v, bool release_k) {
+        all_there(use_v(j), more ? use_k(next) : use_v(j), s, i);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t b = dV + static_cast<uint64_t>(((u % NS) * Sh::kStage) >> 4);
-#pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 8 columns of P, 16 rows of V
-          mma_f16_ts(tbase + kColO + s * D, tbase + s * kKeys + 8 * k, b + static_cast<uint64_t>(k * (2048 >> 4)), idO,
-                     i > 0 || k > 0 ? 1u : 0u);
-        if (last) mma_commit(&o_full[s]);
-      };
-      auto release = [&](int u) {
-        if (ok) mma_commit(&empty[u % NS]);
-      };
-      if constexpr (kTwo) {
-        if (nA > 0) issue_s(0, 0);
-        if (nB > 0) issue_s(1, 0);
-        release(use_k(0));
-        for (int j = 0; ok && j < cnt; ++j) {
-          if (j < nA) issue_pv(0, j, j, j == nA - 1);
-          if (j + 1 < nA) issue_s(0, j + 1);
-          if (j < nB) issue_pv(1, j, j, j == nB - 1);
-          release(use_v(j));
-          if (j + 1 < nB) issue_s(1, j + 1);
-          if (j + 1 < cnt) release(use_k(j + 1));
+        if (leader) {
+          issue_pv(s, j, i == 0);
+          if (!more) mma_commit(&o_full[s]);
+          if (release_v) mma_commit(&empty[use_v(j) % NS]);
+          if (more) {
+            issue_s(s, next);
+            if (release_k) mma_commit(&empty[use_k(next) % NS]);
+          }
         }
-      } else {
-        issue_s(0, 0);
-        release(use_k(0));
-        if (cnt > 1) {
-          issue_s(1, 1);
-          release(use_k(1));
-        }
-        for (int j = 0; ok && j < cnt; ++j) {
-          issue_pv(j & 1, j, j >> 1, j >= cnt - 2);
-          release(use_v(j));
-          if (j + 2 < cnt) {
-            issue_s(j & 1, j + 2);
-            release(use_k(j + 2));
+        __syncwarp();
+      };
+      landed(use_k(0));
+      if (!kTwo && cnt > 1) landed(use_k(1));
+      tc_fence_after();
+      if (ok && leader) {
+        if constexpr (kTwo) {
+          if (nA > 0) issue_s(0, 0);
+          if (nB > 0) issue_s(1, 0);
+          mma_commit(&empty[use_k(0) % NS]);
+        } else {
+          issue_s(0, 0);
+          mma_commit(&empty[use_k(0) % NS]);
+          if (cnt > 1) {
+            issue_s(1, 1);
+            mma_commit(&empty[use_k(1) % NS]);
           }
         }
       }
-      if (!ok) report_error(p.a.err, kErrWaitTimeout, &abort_flag);
+      __syncwarp();
+      for (int j = 0; ok && j < cnt; ++j) {
+        if constexpr (kTwo) {
+          // the last stream that walks a block releases it
+          if (j == cnt - 1 && tail < kKeys) ok = ok && warp_wait(tail_done, 0, &abort_flag);
+          if (j < nA) turn(0, j, j, j + 1, j + 1 < nA, j >= nB, j + 1 >= nB);
+          if (j < nB) turn(1, j, j, j + 1, j + 1 < nB, true, true);
+        } else {
+          if (j == cnt - 1 && tail < kKeys) ok = ok && warp_wait(tail_done, 0, &abort_flag);
+          turn(j & 1, j, j >> 1, j + 2, j + 2 < cnt, true, true);
+        }
+      }
+      if (!ok && leader) report_error(p.a.err, kErrWaitTimeout, &abort_flag);
       // every MMA issued has finished before the CTA frees TMEM and shared memory
-      mma_commit(end_bar);
+      if (leader) mma_commit(end_bar);
       mbar_wait(end_bar, 0, nullptr);
     }
   } else {
-    // ---------------- softmax, one row a thread ----------------
-    const int s = warp >> 2, qd = warp & 3;
+    // ---------------- softmax, half a row a thread ----------------
+    const int s = warp >> 3, qd = warp & 3, hf = (warp >> 2) & 1;
     const int r = 32 * qd + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(32 * qd) << 16);
-    const uint32_t tS = tl + s * kKeys, tO = tl + kColO + s * D;
+    const uint32_t tS = tl + s * kKeys + 64 * hf, tO = tl + kColO + s * D + (D / 2) * hf;
+    const int pair_bar = 1 + 4 * s + qd;  // named barrier of the two warps of these rows
+    float* mx_own = reinterpret_cast<float*>(sm + Sh::kOffMax) + (2 * s + hf) * kRows + r;
+    float* mx_other = reinterpret_cast<float*>(sm + Sh::kOffMax) + (2 * s + (hf ^ 1)) * kRows + r;
     const int rt = r / p.G;
     const int64_t tok = it.tok + (kTwo ? s * p.nt : 0) + rt;
     const bool valid = rt < p.nt && tok < it.tok_end;
@@ -381,19 +433,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const int j = kTwo ? i : 2 * i + s;  // block, counted from b0
-      if (!warp_wait(&s_full[s], static_cast<uint32_t>(i) & 1, &abort_flag)) {
-        ok = false;
-        break;
-      }
+      // a wait that gave up is met by all warps of a stream: each goes on to the pair's barrier
+      ok = ok && warp_wait(&s_full[s], static_cast<uint32_t>(i) & 1, &abort_flag);
       tc_fence_after();
-      uint32_t x[4][32];
+      uint32_t x[2][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + 32 * c, x[c]);
+      for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32(tS + 32 * c, x[c]);
       tmem_ld_wait();
       if ((j + 1) * kKeys > whole) {
-        const int rem = lim - j * kKeys;
+        const int rem = lim - j * kKeys - 64 * hf;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (32 * c + e >= rem) x[c][e] = 0xFF800000u;  // -inf
@@ -401,11 +451,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       float m4[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        m4[c] = __uint_as_float(x[c][0]);
+        m4[c] = __uint_as_float(x[c >> 1][16 * (c & 1)]);
 #pragma unroll
-        for (int e = 1; e < 32; ++e) m4[c] = fmaxf(m4[c], __uint_as_float(x[c][e]));
+        for (int e = 1; e < 16; ++e) m4[c] = fmaxf(m4[c], __uint_as_float(x[c >> 1][16 * (c & 1) + e]));
       }
-      const float mn = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
+      const float mine = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      // the other half's maximum.  The next block's may overwrite it: its S is there only after
+      // both warps have handed over this block's P, and so have read this
+      *mx_own = mine;
+      asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+      const float mn = fmaxf(mine, *mx_other) * sl2;
       const bool resc = mn > ref + kRescaleLog2;  // the first block with a visible key always
       float alpha = 1.0f;
       if (resc) {
@@ -416,7 +471,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const float2 sc2 = make_float2(sl2, sl2), nb2 = make_float2(-base, -base);
       float2 sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -430,10 +485,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       l = fmaf(l, alpha, sum2.x + sum2.y);
       if (i > 0 && __any_sync(0xFFFFFFFFu, resc)) {
-        // a row's reference moved: scale its O, which holds all earlier P V (they were done
-        // before this S was)
+        // a row's reference moved: scale its O (half of it in each warp), which holds all
+        // earlier P V (they were done before this S was)
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D / 2; c += 32) {
           uint32_t o[32];
           tmem_ld_32x32b_x32(tO + c, o);
           tmem_ld_wait();
@@ -452,16 +507,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc_fence_after();
     }
     if (!ok) report_error(p.a.err, kErrWaitTimeout, &abort_flag);
-    bool have = ok && n > 0;  // O holds something
+    const bool have = ok && n > 0;  // O holds something
+    // the row's sum: both halves'
+    *mx_own = l;
+    asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+    l += *mx_other;
     float scale = 1.0f;
-    float4* xrow = reinterpret_cast<float4*>(sm + Sh::kOffRing + r * (D * 4 + 16));
+    float4* xrow = reinterpret_cast<float4*>(sm + Sh::kOffRing + r * (D * 4 + 16)) + (D / 8) * hf;
     if constexpr (!kTwo) {
       // join the two streams: references and sums first, then O through the ring, which both
       // streams' MMAs and copies have left
       if (nB > 0) {
-        float2* ml = reinterpret_cast<float2*>(sm + Sh::kOffMl);
-        ml[s * kRows + r] = make_float2(have ? ref : -INFINITY, have ? l : 0.0f);
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 9, 512;" ::: "memory");  // the maxima's places are free now
+        float2* ml = reinterpret_cast<float2*>(sm + Sh::kOffMax);
+        if (hf == 0) ml[s * kRows + r] = make_float2(have ? ref : -INFINITY, have ? l : 0.0f);
+        asm volatile("bar.sync 9, 512;" ::: "memory");
         const float2 other = ml[(s ^ 1) * kRows + r];
         const float top = fmaxf(ref, other.x);
         scale = ref == -INFINITY ? 0.0f : ex2(ref - top);
@@ -469,7 +529,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ref = top;
         if (s == 1) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
+          for (int c = 0; c < D / 2; c += 32) {
             uint32_t o[32];
             tmem_ld_32x32b_x32(tO + c, o);
             tmem_ld_wait();
@@ -479,20 +539,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                             __uint_as_float(o[4 * e + 2]) * scale, __uint_as_float(o[4 * e + 3]) * scale);
           }
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 9, 512;" ::: "memory");
       }
     }
     if (kTwo || s == 0) {
       const bool final_out = p.to_parts == 0;
       const int head = hk * p.G + (r - rt * p.G);
-      const float inv = final_out ? (l > 0.0f || l != l ? scale / l : 0.0f) : scale;
+      const float over = final_out ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
+      const float inv = scale * over;
       const int64_t row = tok * p.a.H + head;
-      uint16_t* orow = p.a.o + tok * p.a.st[6] + head * p.a.st[7];
-      float* prow = p.part_o + (static_cast<int64_t>(split) * p.a.Tq * p.a.H + row) * D;
-      if (!final_out && valid && cnt > 0)
+      uint16_t* orow = p.a.o + tok * p.a.st[6] + head * p.a.st[7] + (D / 2) * hf;
+      float* prow = p.part_o + (static_cast<int64_t>(split) * p.a.Tq * p.a.H + row) * D + (D / 2) * hf;
+      if (!final_out && valid && cnt > 0 && hf == 0)
         p.part_ml[static_cast<int64_t>(split) * p.a.Tq * p.a.H + row] = make_float2(ref, l);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < D / 2; c += 32) {
         uint32_t o[32];
         if (have) {
           tmem_ld_32x32b_x32(tO + c, o);
@@ -505,14 +566,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
         if (!kTwo && nB > 0) {
-          const float w = final_out ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 y = xrow[c / 4 + e];
-            f[4 * e] = fmaf(y.x, w, f[4 * e]);
-            f[4 * e + 1] = fmaf(y.y, w, f[4 * e + 1]);
-            f[4 * e + 2] = fmaf(y.z, w, f[4 * e + 2]);
-            f[4 * e + 3] = fmaf(y.w, w, f[4 * e + 3]);
+            f[4 * e] = fmaf(y.x, over, f[4 * e]);
+            f[4 * e + 1] = fmaf(y.y, over, f[4 * e + 1]);
+            f[4 * e + 2] = fmaf(y.z, over, f[4 * e + 2]);
+            f[4 * e + 3] = fmaf(y.w, over, f[4 * e + 3]);
           }
         }
         if (valid) {
@@ -534,7 +594,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tbase, 512);
+  if (warp == kSoftWarps + 1) tmem_dealloc(tbase, 512);
 }
 
 // ---- joining the splits of a row -----------------------------------------------------------
