@@ -25,6 +25,7 @@ this package fails.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -387,37 +388,50 @@ def q8_bsa_attention(q, k, v, row_ptr, col_idx, out_dtype=torch.float32, o=None,
 
 
 def _heads(name, t, dtype, shape, d):
-    """t: a CUDA tensor on the current device of this type and shape whose innermost dimension
-    (a head's d channels) is contiguous; its other strides are passed on."""
-    if t.dtype != dtype:
+    """The strides of t, a tensor on CUDA device d of this type and shape whose innermost
+    dimension (a head's channels) is contiguous."""
+    st = t.stride()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == d and (st[-1] == 1 or shape[-1] <= 1):
+        return st
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != d:
+    if t.get_device() != d:
         raise ValueError(f"{name}: must be a CUDA tensor on the current device (cuda:{d})")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    raise ValueError(f"{name}: the channels of a head must be contiguous")
 
 
-def _lengths(name, t, n, d):
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name}: expected torch.int32, got {t.dtype}")
+def _vector(name, t, dtype, n, d):
+    """The address of t, a contiguous vector of n elements on CUDA device d."""
+    if t.dtype is dtype and t.shape == (n,) and t.get_device() == d and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != (n,):
         raise ValueError(f"{name}: expected shape {(n,)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != d or not t.is_contiguous():
-        raise ValueError(f"{name}: must be a contiguous CUDA tensor on the current device (cuda:{d})")
+    raise ValueError(f"{name}: must be a contiguous CUDA tensor on the current device (cuda:{d})")
 
 
-_STRIDES8, _STRIDES14 = ctypes.c_int64 * 8, ctypes.c_int64 * 14
+def _dims(name, t, n):
+    if t.dim() != n:
+        raise ValueError(f"{name}: expected {n} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+_STRIDES8, _STRIDES14 = struct.Struct("8q").pack, struct.Struct("14q").pack
 
 
 def _workspace(workspace, need, device, d):
-    """(tensor or None, bytes): the caller's workspace, else one that torch allocates."""
+    """(tensor or None, address or None, bytes): the caller's workspace, else one from torch."""
     if workspace is None:
-        return (torch.empty(need, dtype=torch.uint8, device=device) if need else None), need
-    if not workspace.is_cuda or workspace.get_device() != d or not workspace.is_contiguous():
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
+    if workspace.get_device() != d or not workspace.is_contiguous():
         raise ValueError(f"workspace: must be a contiguous CUDA tensor on the current device (cuda:{d})")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def q8_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
@@ -427,37 +441,33 @@ def q8_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps
     positions int32 [T], inv_freq float64 [rot/2], weights float32 [d] or None (no norm)
     -> (q_out, k_out) bfloat16.  q_out=q, k_out=k work in place (bfloat16)."""
     dev = torch.cuda.current_device()
-    T, H, d = q.shape
-    Hkv = k.shape[1]
-    if q.dtype not in DTYPES:
-        raise TypeError(f"q: expected bfloat16 or float32, got {q.dtype}")
-    _heads("q", q, q.dtype, (T, H, d), dev)
-    _heads("k", k, q.dtype, (T, Hkv, d), dev)
+    T, H, d = _dims("q", q, 3)
+    Hkv = _dims("k", k, 3)[1]
+    dtype = q.dtype
+    if dtype not in DTYPES:
+        raise TypeError(f"q: expected bfloat16 or float32, got {dtype}")
+    sq, sk = _heads("q", q, dtype, (T, H, d), dev), _heads("k", k, dtype, (T, Hkv, d), dev)
     if q_out is None:
         q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+        sqo = (H * d, d, 1)
     else:
-        _heads("q_out", q_out, torch.bfloat16, (T, H, d), dev)
+        sqo = _heads("q_out", q_out, torch.bfloat16, (T, H, d), dev)
     if k_out is None:
         k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=q.device)
+        sko = (Hkv * d, d, 1)
     else:
-        _heads("k_out", k_out, torch.bfloat16, (T, Hkv, d), dev)
-    for name, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)):
-        if t.shape[1] > 1 and t.stride(1) != d:
-            raise ValueError(f"{name}: the heads of a token must be contiguous")
-    _lengths("positions", positions, T, dev)
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq: a 1-D float64 CUDA tensor")
-    _need(inv_freq, torch.float64, inv_freq.shape, "inv_freq")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _need(w, torch.float32, (d,), name)
-    _on_device(inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight)
-    many = T > 1
-    _check(_L.q8_qk_norm_rope(q.data_ptr(), k.data_ptr(), DTYPES[q.dtype], q.stride(0) if many else H * d,
-                              k.stride(0) if many else Hkv * d, _ptr(q_weight), _ptr(k_weight), float(eps),
-                              positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0],
-                              1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(),
-                              q_out.stride(0) if many else H * d, k_out.stride(0) if many else Hkv * d,
+        sko = _heads("k_out", k_out, torch.bfloat16, (T, Hkv, d), dev)
+    if (H > 1 and (sq[1] != d or sqo[1] != d)) or (Hkv > 1 and (sk[1] != d or sko[1] != d)):
+        raise ValueError("q, k, q_out, k_out: the heads of a token must be contiguous")
+    half = _dims("inv_freq", inv_freq, 1)[0]
+    if T <= 1:  # a single token: its stride says nothing
+        sq, sk, sqo, sko = (H * d,), (Hkv * d,), (H * d,), (Hkv * d,)
+    _check(_L.q8_qk_norm_rope(q.data_ptr(), k.data_ptr(), DTYPES[dtype], sq[0], sk[0],
+                              None if q_weight is None else _vector("q_weight", q_weight, torch.float32, d, dev),
+                              None if k_weight is None else _vector("k_weight", k_weight, torch.float32, d, dev),
+                              eps, _vector("positions", positions, torch.int32, T, dev),
+                              _vector("inv_freq", inv_freq, torch.float64, half, dev), 2 * half,
+                              1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), sqo[0], sko[0],
                               T, H, Hkv, d, _stream(stream)), "q8_qk_norm_rope")
     return q_out, k_out
 
@@ -473,28 +483,25 @@ def q8_prompt_attention(q, k, v, cu_q, cu_k=None, scale=None, o=None, workspace=
     -> o [Tq,H,d] bfloat16 (a new o is not initialised outside the sequences).  scale None:
     1/sqrt(d).  workspace None: allocated here with torch."""
     dev = torch.cuda.current_device()
-    Tq, H, d = q.shape
-    Tk, Hkv, _ = k.shape
-    _heads("q", q, torch.bfloat16, (Tq, H, d), dev)
-    _heads("k", k, torch.bfloat16, (Tk, Hkv, d), dev)
-    _heads("v", v, torch.bfloat16, (Tk, Hkv, d), dev)
-    if cu_k is None:
-        cu_k = cu_q
+    Tq, H, d = _dims("q", q, 3)
+    Tk, Hkv, _ = _dims("k", k, 3)
+    sq, sk, sv = (_heads("q", q, torch.bfloat16, (Tq, H, d), dev), _heads("k", k, torch.bfloat16, (Tk, Hkv, d), dev),
+                  _heads("v", v, torch.bfloat16, (Tk, Hkv, d), dev))
     n = cu_q.numel()
     if n < 1:
         raise ValueError("cu_q: expected at least one entry")
-    _lengths("cu_q", cu_q, n, dev)
-    _lengths("cu_k", cu_k, n, dev)
+    pq = _vector("cu_q", cu_q, torch.int32, n, dev)
+    pk = pq if cu_k is None else _vector("cu_k", cu_k, torch.int32, n, dev)
     if o is None:
         o = torch.empty((Tq, H, d), dtype=torch.bfloat16, device=q.device)
+        so = (H * d, d)
     else:
-        _heads("o", o, torch.bfloat16, (Tq, H, d), dev)
-    need = _L.q8_prompt_attention_workspace_size(n - 1, Tq, Tk, H, Hkv, d)
-    workspace, nbytes = _workspace(workspace, need, q.device, dev)
-    st = _STRIDES8(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2])
-    _check(_L.q8_prompt_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
-                                  o.data_ptr(), n - 1, Tq, Tk, H, Hkv, d,
-                                  d ** -0.5 if scale is None else float(scale), st, _ptr(workspace), nbytes,
+        so = _heads("o", o, torch.bfloat16, (Tq, H, d), dev)
+    workspace, pw, nbytes = _workspace(
+        workspace, _L.q8_prompt_attention_workspace_size(n - 1, Tq, Tk, H, Hkv, d), q.device, dev)
+    _check(_L.q8_prompt_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), pq, pk, o.data_ptr(), n - 1, Tq, Tk,
+                                  H, Hkv, d, (d or 1) ** -0.5 if scale is None else scale,
+                                  _STRIDES8(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1]), pw, nbytes,
                                   _stream(stream)), "q8_prompt_attention")
     return o
 
@@ -510,26 +517,26 @@ def q8_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, scale=None
     fine), own_len int32 [B] on the device: request b sees the prefix and its first own_len[b]
     own keys -> o [B,H,d] bfloat16.  scale None: 1/sqrt(d).  workspace None: allocated here."""
     dev = torch.cuda.current_device()
-    B, H, d = q.shape
-    P, Hkv, _ = k_prefix.shape
-    cap = k_own.shape[1]
-    _heads("q", q, torch.bfloat16, (B, H, d), dev)
-    _heads("k_prefix", k_prefix, torch.bfloat16, (P, Hkv, d), dev)
-    _heads("v_prefix", v_prefix, torch.bfloat16, (P, Hkv, d), dev)
-    _heads("k_own", k_own, torch.bfloat16, (B, cap, Hkv, d), dev)
-    _heads("v_own", v_own, torch.bfloat16, (B, cap, Hkv, d), dev)
-    _lengths("own_len", own_len, B, dev)
+    B, H, d = _dims("q", q, 3)
+    P, Hkv, _ = _dims("k_prefix", k_prefix, 3)
+    cap = _dims("k_own", k_own, 4)[1]
+    bf16, shared, own = torch.bfloat16, (P, Hkv, d), (B, cap, Hkv, d)
+    sq = _heads("q", q, bf16, (B, H, d), dev)
+    skp, svp = _heads("k_prefix", k_prefix, bf16, shared, dev), _heads("v_prefix", v_prefix, bf16, shared, dev)
+    sko, svo = _heads("k_own", k_own, bf16, own, dev), _heads("v_own", v_own, bf16, own, dev)
+    pn = _vector("own_len", own_len, torch.int32, B, dev)
     if o is None:
-        o = torch.empty((B, H, d), dtype=torch.bfloat16, device=q.device)
+        o = torch.empty((B, H, d), dtype=bf16, device=q.device)
+        so = (H * d, d)
     else:
-        _heads("o", o, torch.bfloat16, (B, H, d), dev)
-    need = _L.q8_prefix_attention_workspace_size(B, P, cap, H, Hkv, d)
-    workspace, nbytes = _workspace(workspace, need, q.device, dev)
-    st = _STRIDES14(*q.stride()[:2], *k_prefix.stride()[:2], *v_prefix.stride()[:2], *k_own.stride()[:3],
-                    *v_own.stride()[:3], *o.stride()[:2])
+        so = _heads("o", o, bf16, (B, H, d), dev)
+    workspace, pw, nbytes = _workspace(
+        workspace, _L.q8_prefix_attention_workspace_size(B, P, cap, H, Hkv, d), q.device, dev)
     _check(_L.q8_prefix_attention(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_own.data_ptr(),
-                                  v_own.data_ptr(), own_len.data_ptr(), o.data_ptr(), B, P, cap, H, Hkv, d,
-                                  d ** -0.5 if scale is None else float(scale), st, _ptr(workspace), nbytes,
+                                  v_own.data_ptr(), pn, o.data_ptr(), B, P, cap, H, Hkv, d,
+                                  (d or 1) ** -0.5 if scale is None else scale,
+                                  _STRIDES14(sq[0], sq[1], skp[0], skp[1], svp[0], svp[1], sko[0], sko[1], sko[2],
+                                             svo[0], svo[1], svo[2], so[0], so[1]), pw, nbytes,
                                   _stream(stream)), "q8_prefix_attention")
     return o
 

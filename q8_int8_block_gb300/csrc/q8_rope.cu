@@ -11,12 +11,13 @@
 //  - A team of d / 16 lanes (rounded up to a power of two) owns a head, each lane the two
 //    8-channel chunks whose channels pair up, so the rotation needs no exchange and every
 //    access is 16 bytes; the sum of squares is a shuffle tree in a fixed order.
-//  - A team walks several heads of one token, so that one set of 8 sines and cosines a lane
-//    serves them all; with few tokens every head gets a team of its own.
-//  - Angles: the fraction of a turn that one position advances is formed once a lane as a
-//    64-bit fixed-point number; position * step modulo 2^64 is then the exact fraction of a
-//    turn at any position, and only its top 32 bits become binary32.  Binary64 arithmetic
-//    would cost more than the memory traffic on this GPU.
+//  - A block takes a few tokens with all their heads.  Its threads form the tokens' sines and
+//    cosines once, in shared memory, while the first heads are on their way from memory; the
+//    teams then walk the heads, several loads ahead.
+//  - Angles: the fraction of a turn that one position advances is formed as a 64-bit
+//    fixed-point number; position * step modulo 2^64 is then the exact fraction of a turn at
+//    any position, and only its top 32 bits become binary32.  Binary64 arithmetic would cost
+//    more than the memory traffic on this GPU.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -41,7 +42,7 @@ struct RopeParams {
   float eps, inv_d;
   int64_t T;
   int d, rot;
-  int teams_per_token;     // a token's heads are dealt to this many teams in turn
+  int tokens;              // tokens of a block; its teams are dealt to them evenly
 };
 
 // inv_freq / (2 pi) as a fraction of a turn in units of 2^-64, modulo whole turns, from the
@@ -57,17 +58,31 @@ __device__ __forceinline__ uint64_t turn_step(double f) {
   return (bits >> 63) != 0 ? 0 - s : s;
 }
 
+// A chunk of 8 channels as it is loaded.
 template <bool kF32>
-__device__ __forceinline__ void load8(const void* x, int64_t at, float (&v)[8]) {
-  if constexpr (kF32) {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 a = f[0], b = f[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    bf16x8_to_f32(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at), v);
+struct Chunk {
+  uint4 v[kF32 ? 2 : 1];
+
+  __device__ __forceinline__ void load(const void* x, int64_t at) {
+    if constexpr (kF32) {
+      const uint4* f = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + at);
+      v[0] = f[0];
+      v[1] = f[1];
+    } else {
+      v[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
+    }
   }
-}
+  __device__ __forceinline__ void unpack(float (&f)[8]) const {
+    if constexpr (kF32) {
+      f[0] = __uint_as_float(v[0].x); f[1] = __uint_as_float(v[0].y);
+      f[2] = __uint_as_float(v[0].z); f[3] = __uint_as_float(v[0].w);
+      f[4] = __uint_as_float(v[1].x); f[5] = __uint_as_float(v[1].y);
+      f[6] = __uint_as_float(v[1].z); f[7] = __uint_as_float(v[1].w);
+    } else {
+      bf16x8_to_f32(v[0], f);
+    }
+  }
+};
 
 __device__ __forceinline__ void store8(uint16_t* out, const float (&v)[8]) {
   uint32_t u[4];
@@ -79,64 +94,91 @@ __device__ __forceinline__ void store8(uint16_t* out, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+__device__ __forceinline__ void read8(const float* s, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+constexpr int kMaxD = 256, kMaxTokens = 8;
+
 template <int kLanes, bool kF32, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeParams p) {
-  const int lane = threadIdx.x % kLanes;
-  const int64_t team = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
-  const int64_t nteams = static_cast<int64_t>(gridDim.x) * kThreads / kLanes;
-  const bool active = 16 * lane < p.d;
+__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const RopeParams p) {
+  constexpr int kTeams = kThreads / kLanes;
+  constexpr int kAhead = kF32 ? 2 : 4;  // heads of a team in flight: 32 registers
+  __shared__ __align__(16) float cos_s[kMaxTokens * kMaxD / 2], sin_s[kMaxTokens * kMaxD / 2];
+  __shared__ __align__(16) float w_s[2][kMaxD];
+  const int lane = threadIdx.x % kLanes, team = threadIdx.x / kLanes;
+  const unsigned mask = (kLanes == 32 ? 0xFFFFFFFFu : ((1u << kLanes) - 1u)) << (threadIdx.x & 31 & ~(kLanes - 1));
+  const int per_token = kTeams / p.tokens, mine = team / per_token, first = team - mine * per_token;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens, t = t0 + mine;
+  const bool active = 16 * lane < p.d && t < p.T;
   const bool turns = 16 * lane < p.rot;  // this lane's pairs are rotated
   // chunks (of 8 channels) a and b
   const int ca = !kInterleaved && turns ? lane : 2 * lane;
   const int cb = !kInterleaved && turns ? lane + p.rot / 16 : 2 * lane + 1;
-  uint64_t step[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) step[i] = turns ? turn_step(p.inv_freq[8 * lane + i]) : 0;
-  // the lane's weights of a query head and of a key head (1 where heads are not normalised)
-  float w[2][16];
-#pragma unroll
-  for (int part = 0; part < 2; ++part)
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      w[part][i] = p.w[part] != nullptr && active ? p.w[part][8 * (i < 8 ? ca : cb) + (i & 7)] : 1.0f;
-  const bool norm_q = p.w[0] != nullptr, norm_k = p.w[1] != nullptr;
   const int nh = p.heads[0] + p.heads[1];
-  const int64_t work = p.T * p.teams_per_token;
-  const int64_t rounds = (work + nteams - 1) / nteams;  // the same for every lane
-  for (int64_t it = 0; it < rounds; ++it) {
-    const int64_t item = it * nteams + team;
-    const bool on = active && item < work;
-    const int64_t t = item < work ? item / p.teams_per_token : 0;
-    const int first = static_cast<int>(item - t * p.teams_per_token);
-    float cs[8], sn[8];
-    const int64_t pos = on ? p.positions[t] : 0;
+
+  Chunk<kF32> xa[kAhead], xb[kAhead];
+  auto load = [&](int h0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int32_t frac = static_cast<int32_t>((static_cast<uint64_t>(pos) * step[i]) >> 32);
-      sincospif(static_cast<float>(frac) * 4.656612873077392578125e-10f, &sn[i], &cs[i]);  // 2^-31
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = h0 + u * per_token;
+      if (active && h < nh) {
+        const int part = h < p.heads[0] ? 0 : 1;
+        const int64_t at = t * p.x_stride[part] + static_cast<int64_t>(part == 0 ? h : h - p.heads[0]) * p.d;
+        xa[u].load(p.x[part], at + 8 * ca);
+        xb[u].load(p.x[part], at + 8 * cb);
+      }
     }
-    for (int h0 = 0; h0 < nh; h0 += p.teams_per_token) {
-      const int h = h0 + first;
-      const bool here = on && h < nh;
+  };
+  load(first);
+  const int half = p.rot / 2;
+  for (int i = threadIdx.x; i < p.tokens * half; i += kThreads) {
+    const int tok = i / half, f = i - tok * half;
+    if (t0 + tok < p.T) {
+      const int64_t pos = p.positions[t0 + tok];
+      const int32_t frac = static_cast<int32_t>((static_cast<uint64_t>(pos) * turn_step(p.inv_freq[f])) >> 32);
+      sincospif(static_cast<float>(frac) * 4.656612873077392578125e-10f, &sin_s[i], &cos_s[i]);  // 2^-31
+    }
+  }
+  for (int i = threadIdx.x; i < 2 * p.d; i += kThreads) {
+    const int part = i < p.d ? 0 : 1, c = i - part * p.d;
+    w_s[part][c] = p.w[part] != nullptr ? p.w[part][c] : 1.0f;  // 1 where heads are not normalised
+  }
+  __syncthreads();
+  float cs[8] = {}, sn[8] = {};
+  if (turns) {
+    read8(cos_s + mine * half + 8 * lane, cs);
+    read8(sin_s + mine * half + 8 * lane, sn);
+  }
+  const bool norm_q = p.w[0] != nullptr, norm_k = p.w[1] != nullptr;
+  for (int h0 = first; h0 < nh; h0 += kAhead * per_token) {
+    if (h0 != first) load(h0);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = h0 + u * per_token;
+      if (h >= nh) break;  // the same for the whole team
       const int part = h < p.heads[0] ? 0 : 1;
-      const int64_t hd = static_cast<int64_t>(part == 0 ? h : h - p.heads[0]) * p.d;
       float a[8] = {}, b[8] = {};
-      if (here) {
-        const int64_t row = t * p.x_stride[part] + hd;
-        load8<kF32>(p.x[part], row + 8 * ca, a);
-        load8<kF32>(p.x[part], row + 8 * cb, b);
+      if (active) {
+        xa[u].unpack(a);
+        xb[u].unpack(b);
       }
       float ss = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+      if (!active) continue;
       const float r = (part == 0 ? norm_q : norm_k) ? __frsqrt_rn(fmaf(ss, p.inv_d, p.eps)) : 1.0f;
+      float w[8];
+      read8(w_s[part] + 8 * ca, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] *= r * (part == 0 ? w[0][i] : w[1][i]);
-        b[i] *= r * (part == 0 ? w[0][8 + i] : w[1][8 + i]);
-      }
+      for (int i = 0; i < 8; ++i) a[i] *= r * w[i];
+      read8(w_s[part] + 8 * cb, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] *= r * w[i];
       if (turns) {
         if constexpr (kInterleaved) {  // pairs inside a chunk: a holds pairs 0-3, b pairs 4-7
 #pragma unroll
@@ -156,11 +198,9 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeParams
           }
         }
       }
-      if (here) {
-        uint16_t* o = p.out[part] + t * p.out_stride[part] + hd;
-        store8(o + 8 * ca, a);
-        store8(o + 8 * cb, b);
-      }
+      uint16_t* o = p.out[part] + t * p.out_stride[part] + static_cast<int64_t>(part == 0 ? h : h - p.heads[0]) * p.d;
+      store8(o + 8 * ca, a);
+      store8(o + 8 * cb, b);
     }
   }
 }
@@ -207,13 +247,22 @@ cudaError_t launch_qk_norm_rope(const void* q, const void* k, int xtype, int64_t
   p.d = d;
   p.rot = rot;
   const int lanes = d <= 16 ? 1 : d <= 32 ? 2 : d <= 64 ? 4 : d <= 128 ? 8 : 16;
-  const int64_t nh = H + Hkv, cap = static_cast<int64_t>(dev.sm_count) * 8;
-  // one head a team until the GPU is full, then up to eight
-  const int64_t full = cap * (kThreads / lanes);
-  const int64_t per = std::min<int64_t>(8, std::max<int64_t>(1, T * nh / full));
-  p.teams_per_token = static_cast<int>((nh + per - 1) / per);
-  const int64_t blocks = (T * p.teams_per_token * lanes + kThreads - 1) / kThreads;
-  const int grid = static_cast<int>(std::min(blocks, cap));
+  // Tokens of a block: the most that leave every SM a few blocks, among the counts that keep
+  // the teams of a token equally busy (8192 tokens of 40 heads of 128: 4 tokens, 5 heads a team)
+  const int64_t nh = H + Hkv, teams = kThreads / lanes;
+  p.tokens = 1;
+  double best = 0.0;
+  for (int n = 1; n <= kMaxTokens && n <= teams; n *= 2) {
+    if (n > 1 && T < static_cast<int64_t>(n) * dev.sm_count * 3) break;
+    const int64_t per = teams / n;
+    const double even = static_cast<double>(nh) / static_cast<double>((nh + per - 1) / per * per);
+    if (even >= best) {
+      best = even;
+      p.tokens = n;
+    }
+  }
+  const int64_t blocks = (T + p.tokens - 1) / p.tokens;
+  const int grid = static_cast<int>(blocks);
   const bool f32 = xtype == 0;
   switch (lanes) {
     case 1: return launch_lanes<1>(p, f32, interleaved, grid, stream);
