@@ -176,7 +176,7 @@ q8_status library_workspace(const DeviceInfo& dev, cudaStream_t stream, size_t b
 }
 
 // ---- checks of the attention layer's entry points --------------------------------------
-constexpr int64_t kSizeLimit = 0x7FFFFFFF;
+constexpr int64_t kSizeLimit = 0x7FFFFFFF - 1024;    // a count rounded up to whole tiles fits 32 bits
 constexpr double kRowLimit = 2147483647.0;           // query rows (tokens and sequences x heads)
 constexpr int64_t kStrideLimit = int64_t{1} << 38;   // elements: byte strides below 2^40 (TMA)
 

@@ -19,10 +19,13 @@ namespace {
 
 constexpr uint32_t kErrBadLength = 1u << 9;  // a sequence or cache length outside its array
 
+__device__ __forceinline__ bool bounds_ok(const PromptArgs& a, int64_t q0, int64_t q1, int64_t k0, int64_t k1) {
+  return 0 <= q0 && q0 <= q1 && q1 <= a.Tq && 0 <= k0 && k0 <= k1 && k1 <= a.Tk;
+}
+
 // whether sequence s lies inside the arrays
 __device__ __forceinline__ bool sequence_ok(const PromptArgs& a, int64_t s) {
-  const int64_t q0 = a.cu_q[s], q1 = a.cu_q[s + 1], k0 = a.cu_k[s], k1 = a.cu_k[s + 1];
-  return 0 <= q0 && q0 <= q1 && q1 <= a.Tq && 0 <= k0 && k0 <= k1 && k1 <= a.Tk;
+  return bounds_ok(a, a.cu_q[s], a.cu_q[s + 1], a.cu_k[s], a.cu_k[s + 1]);
 }
 
 __device__ __forceinline__ void pdl_launch_dependents() {
@@ -126,54 +129,70 @@ __device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, volati
   return true;
 }
 
-// Which queries and keys a CTA works on.
+// Which queries and keys a CTA works on (all counts fit 32 bits: see the entry points' limits).
 struct Item {
-  int64_t tok;      // first query token of stream A's tile
-  int64_t tok_end;  // behind the last query token of the sequence
-  int64_t key0;     // row of the sequence's first key
-  int64_t lk;       // its keys
-  int64_t off;      // query token t sees min(lk, t + off) keys (none if that is negative)
+  int tok;      // first query token of stream A's tile
+  int tok_end;  // behind the last query token of the sequence
+  int key0;     // row of the sequence's first key
+  int lk;       // its keys
 };
 
-__device__ __forceinline__ int64_t visible(const Item& it, int64_t t) {
-  const int64_t n = t + it.off;
-  return n < 0 ? 0 : n < it.lk ? n : it.lk;
+// Keys that query token t (below tok_end) sees: the last one all lk, each one before one less;
+// behind a prefix all of them.
+template <bool kPrefix>
+__device__ __forceinline__ int visible(const Item& it, int t) {
+  if (kPrefix) return it.lk;
+  const int n = it.lk - (it.tok_end - 1 - t);
+  return n < 0 ? 0 : n;
 }
 
 // Slots: sequence s owns the slots from cu_q[s] / n + s on, at least as many as it has groups
 // of n tokens, so a slot finds its sequence by a search over cu_q alone, without a plan.  All
-// lanes of a warp search together, 32 probes a round.
-__device__ __forceinline__ bool prompt_item(const PromptArgs& a, int64_t slot, int n, int lane, Item* it) {
-  auto first = [&](int64_t s) { return static_cast<int64_t>(a.cu_q[s]) / n + s; };
-  int64_t lo = 0, hi = a.B;
-  while (true) {
-    const int64_t step = (hi - lo + 31) / 32, s = lo + lane * step;
-    const unsigned ok = __ballot_sync(0xFFFFFFFFu, s < hi && first(s) <= slot);
+// lanes of a warp search together: 32 probes a round until 32 sequences are left, whose four
+// bounds are then read at once, so up to 32 sequences cost one memory latency.
+__device__ __forceinline__ bool prompt_item(const PromptArgs& a, int slot, int n, int lane, Item* it) {
+  auto first = [&](int s, int q) { return static_cast<int>(static_cast<unsigned>(q / n) + static_cast<unsigned>(s)); };
+  int lo = 0, hi = static_cast<int>(a.B);
+  while (hi - lo > 32) {
+    const int step = (hi - lo + 31) / 32, s = lo + lane * step;
+    const unsigned ok = __ballot_sync(0xFFFFFFFFu, s < hi && first(s, a.cu_q[s]) <= slot);
     if (ok == 0) return false;
     lo += (31 - __clz(ok)) * step;
     if (lo + step < hi) hi = lo + step;
-    if (step == 1) break;
   }
-  if (!sequence_ok(a, lo)) return false;
-  const int64_t q0 = a.cu_q[lo], q1 = a.cu_q[lo + 1], k0 = a.cu_k[lo], lk = a.cu_k[lo + 1] - k0;
-  const int64_t tile = slot - first(lo);
-  if (tile < 0 || q0 + tile * n >= q1) return false;
-  it->tok = q0 + tile * n;
+  const int mine = lo + lane;
+  int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+  if (mine < hi) {
+    q0 = a.cu_q[mine];
+    q1 = a.cu_q[mine + 1];
+    k0 = a.cu_k[mine];
+    k1 = a.cu_k[mine + 1];
+  }
+  const int begin = first(mine, q0);
+  const unsigned ok = __ballot_sync(0xFFFFFFFFu, mine < hi && begin <= slot);
+  if (ok == 0) return false;
+  const int from = 31 - __clz(ok);
+  q0 = __shfl_sync(0xFFFFFFFFu, q0, from);
+  q1 = __shfl_sync(0xFFFFFFFFu, q1, from);
+  k0 = __shfl_sync(0xFFFFFFFFu, k0, from);
+  k1 = __shfl_sync(0xFFFFFFFFu, k1, from);
+  const int tile = slot - __shfl_sync(0xFFFFFFFFu, begin, from);
+  const int64_t tok = q0 + static_cast<int64_t>(tile) * n;  // 64 bits: the bounds may be malformed
+  if (!bounds_ok(a, q0, q1, k0, k1) || tile < 0 || tok >= q1) return false;
+  it->tok = static_cast<int>(tok);
   it->tok_end = q1;
   it->key0 = k0;
-  it->lk = lk;
-  it->off = 1 - q0 + lk - (q1 - q0);
+  it->lk = k1 - k0;
   return true;
 }
 
 template <bool kPrefix>
-__device__ __forceinline__ bool find_item(const TileParams& p, int64_t slot, int n, int lane, Item* it) {
+__device__ __forceinline__ bool find_item(const TileParams& p, int slot, int n, int lane, Item* it) {
   if constexpr (kPrefix) {  // the requests are the tokens, all of them see all keys
     it->tok = slot * n;
-    it->tok_end = p.a.Tq;
+    it->tok_end = static_cast<int>(p.a.Tq);
     it->key0 = 0;
-    it->lk = p.a.Tk;
-    it->off = p.a.Tk;
+    it->lk = static_cast<int>(p.a.Tk);
     return it->tok < it->tok_end;
   } else {
     return prompt_item(p.a, slot, n, lane, it);
@@ -181,12 +200,14 @@ __device__ __forceinline__ bool find_item(const TileParams& p, int64_t slot, int
 }
 
 // Key blocks that the tile of n tokens from tok on needs, and the ones of a split.
-__device__ __forceinline__ int tile_blocks(const Item& it, int64_t tok, int n) {
+template <bool kPrefix>
+__device__ __forceinline__ int tile_blocks(const Item& it, int tok, int n) {
   if (tok >= it.tok_end) return 0;
-  const int64_t last = tok + n < it.tok_end ? tok + n - 1 : it.tok_end - 1;
-  return static_cast<int>((visible(it, last) + kKeys - 1) / kKeys);
+  return (visible<kPrefix>(it, min(tok + n, it.tok_end) - 1) + kKeys - 1) / kKeys;
 }
-__device__ __forceinline__ int blocks_per_split(int blocks, int splits) { return (blocks + splits - 1) / splits; }
+__device__ __forceinline__ int blocks_per_split(int blocks, int splits) {
+  return splits == 1 ? blocks : (blocks + splits - 1) / splits;
+}
 
 template <int D, bool kTwo, bool kPrefix>
 __global__ void __launch_bounds__(kTileThreads, 1)
@@ -198,33 +219,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   extern __shared__ __align__(1024) uint8_t sm[];
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = static_cast<int>(threadIdx.x & 31);
   const int hk = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.a.Hkv));
-  const int64_t slot = p.nslots - 1 - blockIdx.x / static_cast<unsigned>(p.a.Hkv);
+  const int slot = static_cast<int>(p.nslots) - 1 - static_cast<int>(blockIdx.x / static_cast<unsigned>(p.a.Hkv));
   const int split = static_cast<int>(blockIdx.y);
-  if constexpr (!kPrefix) {
-    if (blockIdx.x == 0 && split == 0)  // one CTA looks every sequence over
-      for (int64_t s = threadIdx.x; s < p.a.B; s += kTileThreads)
-        if (!sequence_ok(p.a, s)) atomicOr(p.a.err, kErrBadLength);
-  }
   if ((smem_u32(sm) & 1023u) != 0) {  // the whole CTA leaves before touching anything
     if (threadIdx.x == 0) atomicOr(p.a.err, kErrBadLaunch);
     return;
   }
   constexpr int kTiles = kTwo ? 2 : 1;
-  Item it;
-  if (!find_item<kPrefix>(p, slot, kTiles * p.nt, lane, &it)) return;  // the same for every warp
-  const int nbA = uniform(tile_blocks(it, it.tok, p.nt)), nbB = kTwo ? uniform(tile_blocks(it, it.tok + p.nt, p.nt)) : nbA;
-  const int nb = nbA > nbB ? nbA : nbB;
-  const int per = blocks_per_split(nb, p.splits);
-  const int b0 = split * per;
-  const int cnt = nb - b0 < per ? nb - b0 : per;  // blocks of this CTA (<= 0: none)
-  if (split > 0 && cnt <= 0) return;
-  // blocks of each stream: both tiles walk the same blocks, or one tile's are dealt in turn
-  auto clampn = [](int x, int hi) { return x < 0 ? 0 : x < hi ? x : hi; };
-  const int nA = kTwo ? clampn(nbA - b0, cnt) : (cnt + 1) / 2, nB = kTwo ? clampn(nbB - b0, cnt) : cnt / 2;
-  // rows of the last block behind the sequence's keys
-  const int tail = uniform(cnt > 0 && static_cast<int64_t>(b0 + cnt) * kKeys > it.lk
-                               ? static_cast<int>(it.lk - static_cast<int64_t>(b0 + cnt - 1) * kKeys) : kKeys);
-
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::kOffBar);
   uint64_t* q_full = bars;         // [1]
   uint64_t* tail_done = bars + 1;  // [1] the last V block's rows behind the keys are zero
@@ -237,7 +238,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(bars + 9 + 2 * NS);
   int& abort_flag = *reinterpret_cast<int*>(bars + 10 + 2 * NS);
   static_assert((11 + 2 * NS) * 8 <= 256, "barriers");
-  if (threadIdx.x == 0) {
+  // The start is latency: descriptors, barriers, TMEM and the search for the item go side by
+  // side, and the loads begin before the block has met for the first time.
+  if (warp == kSoftWarps && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
     mbar_init(q_full, 1);
     mbar_init(tail_done, 1);
     for (int i = 0; i < 2; ++i) {
@@ -253,9 +259,48 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     abort_flag = 0;
     fence_barrier_init();
   }
+  if constexpr (!kPrefix) {
+    if (blockIdx.x == 0 && split == 0)  // one CTA looks every sequence over
+      for (int64_t s = threadIdx.x; s < p.a.B; s += kTileThreads)
+        if (!sequence_ok(p.a, s)) atomicOr(p.a.err, kErrBadLength);
+  }
+  Item it = {};
+  const bool found = find_item<kPrefix>(p, slot, kTiles * p.nt, lane, &it);  // the same for every warp
+  const int nbA = uniform(found ? tile_blocks<kPrefix>(it, it.tok, p.nt) : 0);
+  const int nbB = kTwo ? uniform(found ? tile_blocks<kPrefix>(it, it.tok + p.nt, p.nt) : 0) : nbA;
+  const int nb = nbA > nbB ? nbA : nbB;
+  const int per = blocks_per_split(nb, p.splits);
+  const int b0 = split * per;
+  const int cnt = nb - b0 < per ? nb - b0 : per;  // blocks of this CTA (<= 0: none)
+  // blocks of each stream: both tiles walk the same blocks, or one tile's are dealt in turn
+  auto clampn = [](int x, int hi) { return x < 0 ? 0 : x < hi ? x : hi; };
+  const int nA = kTwo ? clampn(nbA - b0, cnt) : (cnt + 1) / 2, nB = kTwo ? clampn(nbB - b0, cnt) : cnt / 2;
+  // rows of the last block behind the sequence's keys
+  const int tail = uniform(cnt > 0 && (b0 + cnt) * kKeys > it.lk ? it.lk - (b0 + cnt - 1) * kKeys : kKeys);
+  // The ring holds the K and V blocks in the order of their use.  Two tiles: K0 V0 K1 V1 ...;
+  // one tile with two streams: K0 K1 V0 K2 V1 K3 V2 ...  (u: place in that order)
+  auto use_k = [&](int j) { return kTwo ? 2 * j : j < 2 ? j : 2 * j - 1; };
+  auto use_v = [&](int j) { return kTwo ? 2 * j + 1 : j + 2 <= cnt - 1 ? 2 * j + 2 : cnt + j; };
+  auto copy_block = [&](int u, bool isK, int j) {  // use u: block j of K or V
+    const int st = u % NS;
+    mbar_arrive_expect_tx(&full[st], Sh::kStage);
+    const int32_t row = it.key0 + (b0 + j) * kKeys;
+    for (int c = 0; c < D / 64; ++c)
+      tma_load_3d(sm + Sh::kOffRing + st * Sh::kStage + c * Sh::kHalf, isK ? &tmK : &tmV, &full[st], 64 * c,
+                  isK ? (p.k_head ? hk : 0) : (p.v_head ? hk : 0), row);
+  };
+  if (!found || (split > 0 && cnt <= 0)) return;  // nothing to do
   if (warp == kSoftWarps + 1) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
+  }
+  if (warp == kSoftWarps && lane == 0 && cnt > 0) {
+    mbar_arrive_expect_tx(q_full, kTiles * (D / 64) * 128u * static_cast<uint32_t>(p.G * p.nt));
+    for (int t = 0; t < kTiles; ++t)
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_3d(sm + t * Sh::kTile + c * Sh::kHalf, &tmQ, q_full, 64 * c, hk * p.G,
+                    it.tok + t * p.nt);
+    copy_block(0, true, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -263,43 +308,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t tbase = static_cast<uint32_t>(uniform(static_cast<int>(tmem_slot)));
   constexpr uint32_t kColO = 256;
 
-  // The ring holds the K and V blocks in the order of their use.  Two tiles: K0 V0 K1 V1 ...;
-  // one tile with two streams: K0 K1 V0 K2 V1 K3 V2 ...  (u: place in that order)
-  auto use_k = [&](int j) { return kTwo ? 2 * j : j < 2 ? j : 2 * j - 1; };
-  auto use_v = [&](int j) { return kTwo ? 2 * j + 1 : j + 2 <= cnt - 1 ? 2 * j + 2 : cnt + j; };
   if (warp == kSoftWarps) {
     // ---------------- loads ----------------
     bool ok = true;
     if (lane == 0 && cnt > 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-      const uint32_t box = 128u * static_cast<uint32_t>(p.G * p.nt);
-      mbar_arrive_expect_tx(q_full, kTiles * (D / 64) * box);
-      for (int t = 0; t < kTiles; ++t)
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(sm + t * Sh::kTile + c * Sh::kHalf, &tmQ, q_full, 64 * c, hk * p.G,
-                      static_cast<int32_t>(it.tok + t * p.nt));
-      int issued = 0;
+      int issued = 1;  // the first block of K is under way
       auto load = [&](int u, bool isK, int j) {
         const int st = u % NS, turn = u / NS;
         if (ok && turn > 0) ok = mbar_wait_sleep(&empty[st], static_cast<uint32_t>(turn - 1) & 1, &abort_flag);
         if (!ok) return;
         issued = u + 1;
-        mbar_arrive_expect_tx(&full[st], Sh::kStage);
-        const int32_t row = static_cast<int32_t>(it.key0 + static_cast<int64_t>(b0 + j) * kKeys);
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(sm + Sh::kOffRing + st * Sh::kStage + c * Sh::kHalf, isK ? &tmK : &tmV, &full[st], 64 * c,
-                      isK ? (p.k_head ? hk : 0) : (p.v_head ? hk : 0), row);
+        copy_block(u, isK, j);
       };
       if constexpr (kTwo) {
         for (int j = 0; j < cnt; ++j) {
-          load(2 * j, true, j);
+          if (j > 0) load(2 * j, true, j);
           load(2 * j + 1, false, j);
         }
       } else {
-        int u = 0;
-        load(u++, true, 0);
+        int u = 1;
         if (cnt > 1) load(u++, true, 1);
         for (int j = 0; j < cnt; ++j) {
           load(u++, false, j);
@@ -421,14 +448,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float* mx_own = reinterpret_cast<float*>(sm + Sh::kOffMax) + (2 * s + hf) * kRows + r;
     float* mx_other = reinterpret_cast<float*>(sm + Sh::kOffMax) + (2 * s + (hf ^ 1)) * kRows + r;
     const int rt = r / p.G;
-    const int64_t tok = it.tok + (kTwo ? s * p.nt : 0) + rt;
+    const int tok = it.tok + (kTwo ? s * p.nt : 0) + rt;
     const bool valid = rt < p.nt && tok < it.tok_end;
     const int n = s == 0 ? nA : nB;
     const float sl2 = p.scale_log2;
     // keys this row sees, counted from the CTA's first block
-    const int64_t seen = (valid ? visible(it, tok) : 0) - static_cast<int64_t>(b0) * kKeys;
-    const int lim = seen < 0 ? 0 : seen > 0x7FFFFF00 ? 0x7FFFFF00 : static_cast<int>(seen);
-    const int whole = __reduce_min_sync(0xFFFFFFFFu, valid ? lim : 0x7FFFFF00);  // the warp's rows see all keys below
+    const int lim = max(0, (valid ? visible<kPrefix>(it, tok) : 0) - b0 * kKeys);
+    const int whole = __reduce_min_sync(0xFFFFFFFFu, valid ? lim : 0x7FFFFFFF);  // the warp's rows see all keys below
     float ref = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int i = 0; i < n; ++i) {
@@ -502,8 +528,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[s]);
     }
-    if (ok && n > 0) {
-      ok = warp_wait(&o_full[s], 0, &abort_flag);
+    // the stream's products are done; without any, its Q tile (used below) has still to land
+    if (ok && cnt > 0) {
+      ok = warp_wait(n > 0 ? &o_full[s] : q_full, 0, &abort_flag);
       tc_fence_after();
     }
     if (!ok) report_error(p.a.err, kErrWaitTimeout, &abort_flag);
@@ -547,11 +574,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int head = hk * p.G + (r - rt * p.G);
       const float over = final_out ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
       const float inv = scale * over;
-      const int64_t row = tok * p.a.H + head;
+      const int64_t row = static_cast<int64_t>(tok) * p.a.H + head;
       uint16_t* orow = p.a.o + tok * p.a.st[6] + head * p.a.st[7] + (D / 2) * hf;
       float* prow = p.part_o + (static_cast<int64_t>(split) * p.a.Tq * p.a.H + row) * D + (D / 2) * hf;
       if (!final_out && valid && cnt > 0 && hf == 0)
         p.part_ml[static_cast<int64_t>(split) * p.a.Tq * p.a.H + row] = make_float2(ref, l);
+      // Through shared memory (the stream's own Q tile, which its S products have left), so that
+      // the warp writes whole 128-byte lines: one row a lane would take a store 32 lines.
+      // A lane stages kLine bytes of its row in 16-byte pieces, swizzled as the tile was.
+      constexpr int kLine = D, kPieces = kLine / 16;
+      uint8_t* stage = sm + s * Sh::kTile + (D == 128 ? hf * Sh::kHalf : 0) + 32 * qd * 128;
+      auto piece = [&](int row, int q) {
+        return reinterpret_cast<uint4*>(stage + row * 128 + (((D == 128 ? q : kPieces * hf + q) ^ (row & 7)) << 4));
+      };
+      const unsigned rows = __ballot_sync(0xFFFFFFFFu, valid);
+      auto flush = [&](uint8_t* dst) {  // dst: where this lane's row goes (kLine bytes)
+        __syncwarp();
+        const uint64_t at = reinterpret_cast<uint64_t>(dst);
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e) {
+          const int row = (32 / kPieces) * e + lane / kPieces, q = lane % kPieces;
+          const uint64_t to = __shfl_sync(0xFFFFFFFFu, at, row);
+          if ((rows >> row) & 1u) *reinterpret_cast<uint4*>(to + 16 * q) = *piece(row, q);
+        }
+        __syncwarp();
+      };
 #pragma unroll 1
       for (int c = 0; c < D / 2; c += 32) {
         uint32_t o[32];
@@ -575,17 +622,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             f[4 * e + 3] = fmaf(y.w, over, f[4 * e + 3]);
           }
         }
-        if (valid) {
-          if (final_out) {
+        if (final_out) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              reinterpret_cast<uint4*>(orow + c)[e] =
-                  make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
-                             pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
-          } else if (cnt > 0) {
+          for (int e = 0; e < 4; ++e)
+            *piece(lane, c / 8 + e) = make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
+                                                 pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+          if (c + 32 == D / 2) flush(reinterpret_cast<uint8_t*>(orow));
+        } else if (cnt > 0) {
+          constexpr int kFloats = kLine / 4;  // of a row, staged at a time
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<float4*>(prow + c)[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+          for (int g = 0; g < 32; g += kFloats) {
+#pragma unroll
+            for (int e = 0; e < kPieces; ++e)
+              *piece(lane, e) = make_uint4(__float_as_uint(f[g + 4 * e]), __float_as_uint(f[g + 4 * e + 1]),
+                                           __float_as_uint(f[g + 4 * e + 2]), __float_as_uint(f[g + 4 * e + 3]));
+            flush(reinterpret_cast<uint8_t*>(prow + c + g));
           }
         }
       }
@@ -599,16 +650,50 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // ---- joining the splits of a row -----------------------------------------------------------
 // o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, one warp a row.
+// `place` gives the row of a split.  A warp takes the splits from, from + step, ...: their
+// references and sums are read by the lanes, their rows four at a time.
+template <int D, typename F>
+__device__ __forceinline__ void join_parts(int used, int from, int step, int lane, const float2* ml, const float* o,
+                                           F place, float& l, float (&acc)[D / 32]) {
+  constexpr int E = D / 32;
+  float top = -INFINITY;  // of all splits
+  for (int s = lane; s < used; s += 32) top = fmaxf(top, ml[place(s)].x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+  l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+  for (int s0 = from; s0 < used; s0 += 32 * step) {
+    float w = 0.0f, sum = 0.0f;  // this lane's split
+    if (s0 + lane * step < used) {
+      const float2 v = ml[place(s0 + lane * step)];
+      w = v.x == -INFINITY && v.y == 0.0f ? 0.0f : ex2(v.x - top);
+      sum = v.y * w;
+    }
+    const int n = min(32, (used - s0 + step - 1) / step);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float ws = __shfl_sync(0xFFFFFFFFu, w, s);
+      const float* src = o + place(s0 + s * step) * D + E * lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(src[e], ws, acc[e]);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+    l += sum;
+  }
+}
+
 template <int D, bool kTwo>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ TileParams p) {
   constexpr int E = D / 32;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int hk = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.a.Hkv));
-  const int64_t slot = p.nslots - 1 - blockIdx.x / static_cast<unsigned>(p.a.Hkv);
+  const int slot = static_cast<int>(p.nslots) - 1 - static_cast<int>(blockIdx.x / static_cast<unsigned>(p.a.Hkv));
   const int ntok = (kTwo ? 2 : 1) * p.nt;
   Item it;
   if (!prompt_item(p.a, slot, ntok, lane, &it)) return;
-  const int nbA = tile_blocks(it, it.tok, p.nt), nbB = kTwo ? tile_blocks(it, it.tok + p.nt, p.nt) : 0;
+  const int nbA = tile_blocks<false>(it, it.tok, p.nt), nbB = kTwo ? tile_blocks<false>(it, it.tok + p.nt, p.nt) : 0;
   const int nb = nbA > nbB ? nbA : nbB;
   const int per = blocks_per_split(nb, p.splits), used = per > 0 ? (nb + per - 1) / per : 0;
   const int64_t rows = p.a.Tq * p.a.H;
@@ -616,19 +701,8 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
     const int64_t tok = it.tok + r / p.G;
     if (tok >= it.tok_end) break;
     const int64_t head = hk * p.G + r % p.G, row = tok * p.a.H + head;
-    float top = -INFINITY;
-    for (int s = lane; s < used; s += 32) top = fmaxf(top, p.part_ml[s * rows + row].x);
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    float l = 0.0f, acc[E] = {};
-    if (top != -INFINITY)
-      for (int s = 0; s < used; ++s) {
-        const float2 ml = p.part_ml[s * rows + row];
-        const float w = ex2(ml.x - top);
-        l = fmaf(ml.y, w, l);
-        const float* src = p.part_o + (s * rows + row) * D + E * lane;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(src[e], w, acc[e]);
-      }
+    float l, acc[E];
+    join_parts<D>(used, 0, 1, lane, p.part_ml, p.part_o, [&](int s) { return s * rows + row; }, l, acc);
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.a.o + tok * p.a.st[6] + head * p.a.st[7] + E * lane);
 #pragma unroll
@@ -644,13 +718,16 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
 // three CTAs on an SM keep 192 KB in flight.  The products run on mma.sync: 16 rows are all
 // there is, and the tensor pipe is not what bounds this.  Rows behind the request's keys are
 // not read (zeros are filled in).
+// kAlone: no other kernel works on this call.  The prefix, short or of one request only, is
+// walked here in front of the own keys, and the CTAs that share a row's keys are a cluster
+// that joins them through its shared memory: one launch and no workspace.
 constexpr int kOwnWarps = 4, kOwnKeys = 16, kOwnStages = 2, kOwnRows = 16;
 
 struct OwnParams {
   PrefixArgs a;
   int G, chunks;   // heads of a group; 16-head chunks of it
-  int splits;      // at most so many CTAs share a request's keys
-  int prefix_splits, prefix_used;  // partial results of the prefix: allocated, written
+  int splits;      // at most so many CTAs share a request's keys (alone: a cluster of exactly so many)
+  int prefix_splits;  // partial results of the prefix
   float scale_log2;
   float* part_o;    // [prefix_splits + splits][B * H][D]
   float2* part_ml;
@@ -695,35 +772,49 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <int D>
+// The block cluster: a barrier of all its threads, and a value in the shared memory of CTA `rank`.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float peer_load(const float* own, int rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(own)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+template <int D, bool kAlone>
 __global__ void __launch_bounds__(32 * kOwnWarps, 3) attn_own_kernel(const __grid_constant__ OwnParams p) {
   using Sh = OwnShape<D>;
   constexpr int KS = D / 16, C16 = D / 8;  // k steps of a score; 16-byte chunks of a row
-  pdl_launch_dependents();
+  if constexpr (!kAlone) pdl_launch_dependents();
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ float2 ml_s[kOwnWarps][kOwnRows];
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int g = lane >> 2, t = lane & 3;
   const PrefixArgs& a = p.a;
-  const int64_t per_b = a.Hkv * p.chunks;
+  const unsigned per_b = static_cast<unsigned>(a.Hkv) * static_cast<unsigned>(p.chunks);
   const int64_t b = blockIdx.x / per_b;
-  const int rem = static_cast<int>(blockIdx.x - b * per_b);
+  const int rem = static_cast<int>(blockIdx.x - static_cast<unsigned>(b) * per_b);
   const int hk = rem / p.chunks, chunk = rem - hk * p.chunks, split = static_cast<int>(blockIdx.y);
-  const int64_t n = own_length(a, b), per = own_per_split(n, p.splits);
-  if (threadIdx.x == 0 && rem == 0 && split == 0 && n != a.own_len[b]) atomicOr(a.err, kErrBadLength);
+  const int64_t shared = kAlone ? a.P : 0;  // keys of the prefix, in front
+  const int64_t own = own_length(a, b), n = shared + own, per = own_per_split(n, p.splits);
+  if (threadIdx.x == 0 && rem == 0 && split == 0 && own != a.own_len[b]) atomicOr(a.err, kErrBadLength);
   const int64_t k0 = split * per, k1 = k0 + per < n ? k0 + per : n;
-  const bool direct = p.splits == 1 && p.prefix_splits == 0;  // nothing to join: o is written here
-  if (k0 >= k1 && !(direct && split == 0)) {
+  if (!kAlone && k0 >= k1) {
     pdl_wait();
     return;
   }
   const int nrows = p.G - chunk * kOwnRows < kOwnRows ? p.G - chunk * kOwnRows : kOwnRows;
   const int64_t head0 = static_cast<int64_t>(hk) * p.G + chunk * kOwnRows;
-  const int npieces = static_cast<int>((k1 - k0 + kOwnKeys - 1) / kOwnKeys);
+  const int npieces = k1 > k0 ? static_cast<int>((k1 - k0 + kOwnKeys - 1) / kOwnKeys) : 0;
   const int mine = npieces > warp ? (npieces - warp + kOwnWarps - 1) / kOwnWarps : 0;
   uint8_t* ring = sm + warp * Sh::kWarp;
   const uint16_t* kbase = a.ko + b * a.st[6] + hk * a.st[8];
   const uint16_t* vbase = a.vo + b * a.st[9] + hk * a.st[11];
+  const uint16_t* kshared = a.kp + hk * a.st[3];
+  const uint16_t* vshared = a.vp + hk * a.st[5];
   auto load = [&](int i) {  // the warp's i-th piece
     if (i < mine) {
       uint8_t* dst = ring + (i % kOwnStages) * 2 * Sh::kPiece;
@@ -732,10 +823,18 @@ __global__ void __launch_bounds__(32 * kOwnWarps, 3) attn_own_kernel(const __gri
       for (int c = lane; c < kOwnKeys * C16; c += 32) {
         const int row = c / C16, col = c % C16;
         const bool on = key + row < k1;
-        const int64_t at = on ? key + row : k0;
+        const int64_t at = on ? key + row : k0;  // a key of this range stands in where none is read
         const int off = row * D * 2 + ((col ^ (row & 7)) << 4);
-        cp_async16(dst + off, kbase + at * a.st[7] + 8 * col, on);
-        cp_async16(dst + Sh::kPiece + off, vbase + at * a.st[10] + 8 * col, on);
+        const uint16_t *ks, *vs;
+        if (kAlone && at < shared) {
+          ks = kshared + at * a.st[2];
+          vs = vshared + at * a.st[4];
+        } else {
+          ks = kbase + (at - shared) * a.st[7];
+          vs = vbase + (at - shared) * a.st[10];
+        }
+        cp_async16(dst + off, ks + 8 * col, on);
+        cp_async16(dst + Sh::kPiece + off, vs + 8 * col, on);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -837,70 +936,98 @@ __global__ void __launch_bounds__(32 * kOwnWarps, 3) attn_own_kernel(const __gri
         *reinterpret_cast<float2*>(mineo + (g + 8 * h) * Sh::kPad + 8 * c + 2 * t) = make_float2(o[c][2 * h], o[c][2 * h + 1]);
     }
   }
-  __syncthreads();
   constexpr int E = D / 32;
-  for (int r = warp; r < nrows; r += kOwnWarps) {
-    float top = -INFINITY;
+  // (reference, sum, the lane's channels) of a row from the four warps of a CTA
+  auto join_warps = [&](int r, float& top, float& sum, float (&acc)[E]) {
+    top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kOwnWarps; ++w) top = fmaxf(top, ml_s[w][r].x);
-    float sum = 0.0f, acc[E] = {};
+    sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
 #pragma unroll
     for (int w = 0; w < kOwnWarps; ++w) {
       const float2 ml = ml_s[w][r];
-      const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
-      if (f == 0.0f && ml.y == 0.0f) continue;  // a warp without a piece
+      if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // a warp without a piece
+      const float f = ex2(ml.x - top);
       sum = fmaf(ml.y, f, sum);
       const float* src = reinterpret_cast<const float*>(sm + w * Sh::kWarp) + r * Sh::kPad + E * lane;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = fmaf(src[e], f, acc[e]);
     }
-    const int64_t head = head0 + r, row = b * a.H + head;
-    if (direct) {
+  };
+  __syncthreads();
+  if constexpr (kAlone) {
+    // each CTA joins its warps into warp 0's place, then the cluster's CTAs share the rows
+    for (int r = warp; r < nrows; r += kOwnWarps) {
+      float top, sum, acc[E];
+      join_warps(r, top, sum, acc);
+      __syncwarp();  // every lane has read the row before it is overwritten
+      float* dst = reinterpret_cast<float*>(sm) + r * Sh::kPad + E * lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) dst[e] = acc[e];
+      if (lane == 0) ml_s[0][r] = make_float2(top, sum);
+    }
+    cluster_sync();
+    for (int r = split * kOwnWarps + warp; r < nrows; r += p.splits * kOwnWarps) {
+      float top = -INFINITY, sum = 0.0f, acc[E] = {};
+      for (int x = 0; x < p.splits; ++x) top = fmaxf(top, peer_load(&ml_s[0][r].x, x));
+      for (int x = 0; x < p.splits; ++x) {
+        const float m = peer_load(&ml_s[0][r].x, x), l1 = peer_load(&ml_s[0][r].y, x);
+        if (m == -INFINITY && l1 == 0.0f) continue;  // a CTA without keys
+        const float f = ex2(m - top);
+        sum = fmaf(l1, f, sum);
+        const float* src = reinterpret_cast<const float*>(sm) + r * Sh::kPad + E * lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(peer_load(src + e, x), f, acc[e]);
+      }
       const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + b * a.st[12] + head * a.st[13] + E * lane);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + b * a.st[12] + (head0 + r) * a.st[13] + E * lane);
 #pragma unroll
       for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-    } else {
-      const int64_t at = static_cast<int64_t>(p.prefix_splits + split) * a.B * a.H + row;
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+  } else {
+    for (int r = warp; r < nrows; r += kOwnWarps) {
+      float top, sum, acc[E];
+      join_warps(r, top, sum, acc);
+      const int64_t at = static_cast<int64_t>(p.prefix_splits + split) * a.B * a.H + b * a.H + head0 + r;
       if (lane == 0) p.part_ml[at] = make_float2(top, sum);
 #pragma unroll
       for (int e = 0; e < E; e += 2)
         *reinterpret_cast<float2*>(p.part_o + at * D + E * lane + e) = make_float2(acc[e], acc[e + 1]);
     }
+    pdl_wait();  // the join waits for this kernel only: it has to end after the prefix's
   }
-  pdl_wait();  // the join waits for this kernel only: it has to end after the prefix's
 }
 
-// A row's partial results: the splits of the prefix, then those of the request's own keys.
+// A row's partial results: the splits of the prefix, then those of the request's own keys.  A
+// block a row, its four warps a quarter of the splits each.
 template <int D>
 __global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant__ OwnParams p) {
   constexpr int E = D / 32;
-  const int lane = static_cast<int>(threadIdx.x & 31);
+  __shared__ float acc_s[4][D];
+  __shared__ float l_s[4];
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const PrefixArgs& a = p.a;
-  const int64_t rows = a.B * a.H, row = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) / 32;
-  if (row >= rows) return;
+  const int64_t rows = a.B * a.H, row = blockIdx.x;
   const int64_t b = row / a.H, head = row - b * a.H;
   const int64_t n = own_length(a, b), per = own_per_split(n, p.splits);
-  const int own = per > 0 ? static_cast<int>((n + per - 1) / per) : 0, used = p.prefix_used + own;
-  auto place = [&](int s) { return (s < p.prefix_used ? s : p.prefix_splits + s - p.prefix_used) * rows + row; };
+  const int own = per > 0 ? static_cast<int>((n + per - 1) / per) : 0, used = p.prefix_splits + own;
   pdl_wait();
-  float top = -INFINITY;
-  for (int s = lane; s < used; s += 32) top = fmaxf(top, p.part_ml[place(s)].x);
+  float l, acc[E];
+  join_parts<D>(used, warp, 4, lane, p.part_ml, p.part_o, [&](int s) { return s * rows + row; }, l, acc);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  float l = 0.0f, acc[E] = {};
-  for (int s = 0; s < used; ++s) {
-    const int64_t at = place(s);
-    const float2 ml = p.part_ml[at];
-    const float w = ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : ex2(ml.x - top);
-    l = fmaf(ml.y, w, l);
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(p.part_o[at * D + E * lane + e], w, acc[e]);
+  for (int e = 0; e < E; ++e) acc_s[warp][E * lane + e] = acc[e];
+  if (lane == 0) l_s[warp] = l;
+  __syncthreads();
+  if (threadIdx.x < D / 2) {
+    const int c = 2 * static_cast<int>(threadIdx.x);
+    const float sum = (l_s[0] + l_s[1]) + (l_s[2] + l_s[3]), inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+    const float x = (acc_s[0][c] + acc_s[1][c]) + (acc_s[2][c] + acc_s[3][c]);
+    const float y = (acc_s[0][c + 1] + acc_s[1][c + 1]) + (acc_s[2][c + 1] + acc_s[3][c + 1]);
+    *reinterpret_cast<uint32_t*>(a.o + b * a.st[12] + head * a.st[13] + c) = pack_bf16(x * inv, y * inv);
   }
-  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + b * a.st[12] + head * a.st[13] + E * lane);
-#pragma unroll
-  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
 }
 
 // ---- host ----------------------------------------------------------------------------------
@@ -1000,9 +1127,9 @@ cudaError_t prompt_attention(const PromptArgs& a, const DeviceInfo& dev, cudaStr
 struct PrefixPlan {
   bool two;                   // two tiles of requests a block
   int64_t nslots;
-  int prefix_splits, prefix_used, own_splits, chunks;
-  bool direct() const { return prefix_splits == 0 && own_splits == 1; }
-  size_t partials() const { return direct() ? 0 : static_cast<size_t>(prefix_splits + own_splits); }
+  int prefix_splits, own_splits, chunks;
+  bool alone;                 // the own kernel walks the prefix too
+  size_t partials() const { return alone ? 0 : static_cast<size_t>(prefix_splits + own_splits); }
 };
 PrefixPlan prefix_plan(int64_t B, int64_t P, int64_t cap, int64_t H, int64_t Hkv, const DeviceInfo& dev) {
   const int64_t G = H / Hkv, nt = kRows / G;
@@ -1010,32 +1137,48 @@ PrefixPlan prefix_plan(int64_t B, int64_t P, int64_t cap, int64_t H, int64_t Hkv
   pl.two = B > nt;
   const int64_t n = pl.two ? 2 * nt : nt, blocks = (P + kKeys - 1) / kKeys;
   pl.nslots = (B + n - 1) / n;
-  pl.prefix_splits = 0;
-  pl.prefix_used = 0;
-  if (P > 0) {
-    const int64_t s = std::max<int64_t>(1, std::min(dev.sm_count / (pl.nslots * Hkv), blocks / 2));
-    const int64_t per = (blocks + s - 1) / s;
-    pl.prefix_splits = pl.prefix_used = static_cast<int>((blocks + per - 1) / per);
-  }
   pl.chunks = static_cast<int>((G + kOwnRows - 1) / kOwnRows);
   const int64_t busy = B * Hkv * pl.chunks;
-  pl.own_splits = static_cast<int>(std::max<int64_t>(1, std::min(3 * dev.sm_count / busy, cap / 256)));
+  // Alone: few shared keys are read again for every request, which costs less than a second
+  // and a third launch (1 request behind 1000 keys: 27 us a call with three, 21 with one), and
+  // clusters of eight fill the GPU or have little to do.
+  pl.alone = B * P <= 4096 && (8 * busy >= 2 * dev.sm_count || P + cap <= 2048);
+  if (pl.alone) {
+    pl.prefix_splits = 0;
+    const int64_t s = std::min(3 * dev.sm_count / busy, (P + cap + 127) / 128);
+    pl.own_splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, s)));
+    return pl;
+  }
+  const int64_t s = std::max<int64_t>(1, std::min(dev.sm_count / (pl.nslots * Hkv), blocks / 2));
+  const int64_t per = (blocks + s - 1) / s;
+  pl.prefix_splits = P > 0 ? static_cast<int>((blocks + per - 1) / per) : 0;
+  // Three blocks an SM, or more where lengths differ: a long request is then no block's alone
+  pl.own_splits = static_cast<int>(std::max<int64_t>(1, std::min(std::max<int64_t>(4, 3 * dev.sm_count / busy), cap / 128)));
   return pl;
 }
 
+// A launch that may begin before the kernel in front of it has ended (dependent), or whose
+// `cluster` blocks of the same grid column form a cluster.
 template <typename K, typename... A>
-cudaError_t launch_dependent(K kernel, dim3 grid, unsigned threads, size_t smem, bool dependent, cudaStream_t stream,
-                             const A&... args) {
+cudaError_t launch_with(K kernel, dim3 grid, unsigned threads, size_t smem, bool dependent, int cluster,
+                        cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = dependent ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (dependent) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = 1;
+    attr[cfg.numAttrs].val.clusterDim.y = static_cast<unsigned>(cluster);
+    attr[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -1047,7 +1190,8 @@ cudaError_t prefix_attention(const PrefixArgs& a, const DeviceInfo& dev, cudaStr
   const float scale_log2 = a.scale * 1.4426950408889634f;
   const int G = static_cast<int>(a.H / a.Hkv);
   cudaError_t e;
-  if (a.P > 0) {
+  const bool tiles = pl.prefix_splits > 0;
+  if (tiles) {
     TileParams t = {};
     t.a.q = a.q;
     t.a.k = a.kp;
@@ -1077,18 +1221,20 @@ cudaError_t prefix_attention(const PrefixArgs& a, const DeviceInfo& dev, cudaStr
   p.chunks = pl.chunks;
   p.splits = pl.own_splits;
   p.prefix_splits = pl.prefix_splits;
-  p.prefix_used = pl.prefix_used;
   p.scale_log2 = scale_log2;
   p.part_o = part_o;
   p.part_ml = part_ml;
   constexpr int smem = OwnShape<D>::kSmem;
-  e = ensure_smem(reinterpret_cast<const void*>(attn_own_kernel<D>), smem, dev.device);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(attn_own_kernel<D>,
-                       dim3(static_cast<unsigned>(a.B * a.Hkv * pl.chunks), static_cast<unsigned>(pl.own_splits)),
-                       32 * kOwnWarps, smem, a.P > 0, stream, p);
-  if (e != cudaSuccess || pl.direct()) return e;
-  return launch_dependent(prefix_join_kernel<D>, dim3(static_cast<unsigned>((a.B * a.H + 3) / 4)), 128, 0, true, stream, p);
+  const dim3 grid(static_cast<unsigned>(a.B * a.Hkv * pl.chunks), static_cast<unsigned>(pl.own_splits));
+  if (pl.alone) {
+    const auto kernel = attn_own_kernel<D, true>;
+    if ((e = ensure_smem(reinterpret_cast<const void*>(kernel), smem, dev.device)) != cudaSuccess) return e;
+    return launch_with(kernel, grid, 32 * kOwnWarps, smem, false, pl.own_splits, stream, p);
+  }
+  const auto kernel = attn_own_kernel<D, false>;
+  if ((e = ensure_smem(reinterpret_cast<const void*>(kernel), smem, dev.device)) != cudaSuccess) return e;
+  if ((e = launch_with(kernel, grid, 32 * kOwnWarps, smem, tiles, 1, stream, p)) != cudaSuccess) return e;
+  return launch_with(prefix_join_kernel<D>, dim3(static_cast<unsigned>(a.B * a.H)), 128, 0, true, 1, stream, p);
 }
 
 }  // namespace

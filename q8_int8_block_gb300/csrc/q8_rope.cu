@@ -103,9 +103,9 @@ __device__ __forceinline__ void read8(const float* s, float (&v)[8]) {
 constexpr int kMaxD = 256, kMaxTokens = 8;
 
 template <int kLanes, bool kF32, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const RopeParams p) {
   constexpr int kTeams = kThreads / kLanes;
-  constexpr int kAhead = kF32 ? 2 : 4;  // heads of a team in flight: 32 registers
+  constexpr int kAhead = kF32 ? 1 : 2;  // heads of a team in flight: 16 registers
   __shared__ __align__(16) float cos_s[kMaxTokens * kMaxD / 2], sin_s[kMaxTokens * kMaxD / 2];
   __shared__ __align__(16) float w_s[2][kMaxD];
   const int lane = threadIdx.x % kLanes, team = threadIdx.x / kLanes;
@@ -253,7 +253,7 @@ cudaError_t launch_qk_norm_rope(const void* q, const void* k, int xtype, int64_t
   p.tokens = 1;
   double best = 0.0;
   for (int n = 1; n <= kMaxTokens && n <= teams; n *= 2) {
-    if (n > 1 && T < static_cast<int64_t>(n) * dev.sm_count * 3) break;
+    if (n > 1 && T < static_cast<int64_t>(n) * dev.sm_count * 4) break;
     const int64_t per = teams / n;
     const double even = static_cast<double>(nh) / static_cast<double>((nh + per - 1) / per * per);
     if (even >= best) {
