@@ -55,11 +55,21 @@ struct TileShape {
   static constexpr uint32_t kOffRing = (kTwo ? 2 : 1) * kTile;
   static constexpr uint32_t kOffMax = kOffRing + kStages * kStage;  // float [2 streams][2 halves][rows]
   static constexpr uint32_t kOffBar = kOffMax + 4 * kRows * 4;
-  static constexpr uint32_t kSmem = kOffBar + 256;
+  static constexpr int kBars = 22 + 2 * kStages;
+  static constexpr uint32_t kOffWork = kOffBar + kBars * 8;
+  static constexpr uint32_t kSmem = kOffWork + 2 * 64 + 16 + 16;  // two items, the next grid index, TMEM address and flag
+  static_assert(kOffWork % 16 == 0, "alignment");
   static_assert(kSmem <= 227 * 1024, "shared memory of a block");
-  // the one-tile form joins its two streams through the ring
-  static_assert(kTwo || kStages * kStage >= kRows * (D * 4 + 16), "exchange buffer");
 };
+
+// What the load warp tells the others about an item.
+struct Work {
+  int tok, tok_end, lk;  // Item
+  int hk, split, b0;     // key/value head, split, its first block
+  int cnt, nA, nB;       // blocks (-1: no more items), and each stream's
+  int tail;              // rows of the last block that are the sequence's (kKeys: all)
+};
+static_assert(sizeof(Work) <= 64, "an item's place");
 
 struct TileParams {
   PromptArgs a;            // strides of q, k, v, o; for the prefix B, Tq are the requests and Tk is P
@@ -120,13 +130,58 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// warp_wait that polls (bounded as mbar_wait)
-__device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
+// One thread's wait that polls (bounded as mbar_wait).
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_test(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!__all_sync(0xFFFFFFFFu, mbar_test(bar, parity)))
-    if (__any_sync(0xFFFFFFFFu, *abort_flag != 0 || clock64() - t0 > kWaitBudgetCycles)) return false;
+  while (!mbar_test(bar, parity))
+    if (*abort_flag != 0 || clock64() - t0 > kWaitBudgetCycles) return false;
   return true;
+}
+
+// Work stealing: a block asks for the index of one that has not been launched yet, which then
+// never is.  The answer (16 bytes) lands in shared memory and completes on the barrier.
+__device__ __forceinline__ void ask_next(void* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ bool read_next(const void* answer, uint32_t* x, uint32_t* y) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+      "ld.shared.b128 h, [%3];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "mov.u32 %2, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, _, _}, h;\n\t}"
+      : "=r"(ok), "=r"(*x), "=r"(*y)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return ok != 0;
+}
+
+// Transposes 16-byte pieces among groups of kN neighbouring lanes: lane b of a group gives its
+// pieces 0 .. kN - 1 and gets piece b of each of the group's lanes.
+template <int kN>
+__device__ __forceinline__ void transpose_pieces(uint4 (&v)[kN], int lane) {
+#pragma unroll
+  for (int m = 1; m < kN; m <<= 1) {
+    const bool up = (lane & m) != 0;
+#pragma unroll
+    for (int q = 0; q < kN; ++q)
+      if ((q & m) == 0) {
+        uint4 x = up ? v[q] : v[q | m];
+        x.x = __shfl_xor_sync(0xFFFFFFFFu, x.x, m);
+        x.y = __shfl_xor_sync(0xFFFFFFFFu, x.y, m);
+        x.z = __shfl_xor_sync(0xFFFFFFFFu, x.z, m);
+        x.w = __shfl_xor_sync(0xFFFFFFFFu, x.w, m);
+        if (up) v[q] = x;
+        else v[q | m] = x;
+      }
+  }
 }
 
 // Which queries and keys a CTA works on (all counts fit 32 bits: see the entry points' limits).
@@ -215,228 +270,317 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TileParams p) {
   using Sh = TileShape<D, kTwo>;
   constexpr int NS = Sh::kStages;
+  constexpr bool kSteal = !kPrefix;
   if constexpr (kPrefix) pdl_launch_dependents();  // the requests' own keys may start
   extern __shared__ __align__(1024) uint8_t sm[];
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = static_cast<int>(threadIdx.x & 31);
-  const int hk = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.a.Hkv));
-  const int slot = static_cast<int>(p.nslots) - 1 - static_cast<int>(blockIdx.x / static_cast<unsigned>(p.a.Hkv));
-  const int split = static_cast<int>(blockIdx.y);
   if ((smem_u32(sm) & 1023u) != 0) {  // the whole CTA leaves before touching anything
     if (threadIdx.x == 0) atomicOr(p.a.err, kErrBadLaunch);
     return;
   }
   constexpr int kTiles = kTwo ? 2 : 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::kOffBar);
-  uint64_t* q_full = bars;         // [1]
-  uint64_t* tail_done = bars + 1;  // [1] the last V block's rows behind the keys are zero
-  uint64_t* s_full = bars + 2;     // [2] S of a stream computed (and its earlier P V done)
-  uint64_t* p_full = bars + 4;     // [2] P written, O rescaled: an arrival of each warp
-  uint64_t* o_full = bars + 6;     // [2] a stream's last P V done
-  uint64_t* full = bars + 8;       // [NS]
-  uint64_t* empty = bars + 8 + NS; // [NS]
-  uint64_t* end_bar = bars + 8 + 2 * NS;
-  uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(bars + 9 + 2 * NS);
-  int& abort_flag = *reinterpret_cast<int*>(bars + 10 + 2 * NS);
-  static_assert((11 + 2 * NS) * 8 <= 256, "barriers");
-  // The start is latency: descriptors, barriers, TMEM and the search for the item go side by
-  // side, and the loads begin before the block has met for the first time.
+  uint64_t* q_full = bars;           // [1] an item's Q landed
+  uint64_t* q_empty = bars + 1;      // [1] its last S is done
+  uint64_t* tail_done = bars + 2;    // [2] (by item) the last V block's rows behind the keys are zero
+  uint64_t* s_full = bars + 4;       // [2] S of a stream computed (and its earlier P V done)
+  uint64_t* p_full = bars + 6;       // [2] P written, O rescaled: an arrival of each warp
+  uint64_t* o_full = bars + 8;       // [2] a stream's last P V of an item done
+  uint64_t* o_empty = bars + 10;     // [2] an item's O has been read
+  uint64_t* work_full = bars + 12;   // [2] an item's place written
+  uint64_t* work_empty = bars + 14;  // [2] the softmax and MMA warps are done with the item
+  uint64_t* next_bar = bars + 16;    // [1] the next grid index
+  uint64_t* end_bar = bars + 17;     // [1]
+  uint64_t* full = bars + 18;        // [NS]
+  uint64_t* empty = full + NS;       // [NS]
+  auto work_at = [&](int w) { return reinterpret_cast<Work*>(sm + Sh::kOffWork + 64 * w); };
+  void* next_index = sm + Sh::kOffWork + 128;
+  uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(sm + Sh::kOffWork + 144);
+  int& abort_flag = *reinterpret_cast<int*>(sm + Sh::kOffWork + 148);
   if (warp == kSoftWarps && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
     mbar_init(q_full, 1);
-    mbar_init(tail_done, 1);
+    mbar_init(q_empty, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&tail_done[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], kSoftWarps / 2);
       mbar_init(&o_full[i], 1);
+      mbar_init(&o_empty[i], kSoftWarps / 2);
+      mbar_init(&work_full[i], 1);
+      mbar_init(&work_empty[i], kSoftWarps + 1);
     }
+    mbar_init(next_bar, 1);
+    mbar_init(end_bar, 1);
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(end_bar, 1);
     abort_flag = 0;
     fence_barrier_init();
   }
-  if constexpr (!kPrefix) {
-    if (blockIdx.x == 0 && split == 0)  // one CTA looks every sequence over
-      for (int64_t s = threadIdx.x; s < p.a.B; s += kTileThreads)
-        if (!sequence_ok(p.a, s)) atomicOr(p.a.err, kErrBadLength);
-  }
-  Item it = {};
-  const bool found = find_item<kPrefix>(p, slot, kTiles * p.nt, lane, &it);  // the same for every warp
-  const int nbA = uniform(found ? tile_blocks<kPrefix>(it, it.tok, p.nt) : 0);
-  const int nbB = kTwo ? uniform(found ? tile_blocks<kPrefix>(it, it.tok + p.nt, p.nt) : 0) : nbA;
-  const int nb = nbA > nbB ? nbA : nbB;
-  const int per = blocks_per_split(nb, p.splits);
-  const int b0 = split * per;
-  const int cnt = nb - b0 < per ? nb - b0 : per;  // blocks of this CTA (<= 0: none)
-  // blocks of each stream: both tiles walk the same blocks, or one tile's are dealt in turn
-  auto clampn = [](int x, int hi) { return x < 0 ? 0 : x < hi ? x : hi; };
-  const int nA = kTwo ? clampn(nbA - b0, cnt) : (cnt + 1) / 2, nB = kTwo ? clampn(nbB - b0, cnt) : cnt / 2;
-  // rows of the last block behind the sequence's keys
-  const int tail = uniform(cnt > 0 && (b0 + cnt) * kKeys > it.lk ? it.lk - (b0 + cnt - 1) * kKeys : kKeys);
-  // The ring holds the K and V blocks in the order of their use.  Two tiles: K0 V0 K1 V1 ...;
-  // one tile with two streams: K0 K1 V0 K2 V1 K3 V2 ...  (u: place in that order)
-  auto use_k = [&](int j) { return kTwo ? 2 * j : j < 2 ? j : 2 * j - 1; };
-  auto use_v = [&](int j) { return kTwo ? 2 * j + 1 : j + 2 <= cnt - 1 ? 2 * j + 2 : cnt + j; };
-  auto copy_block = [&](int u, bool isK, int j) {  // use u: block j of K or V
-    const int st = u % NS;
-    mbar_arrive_expect_tx(&full[st], Sh::kStage);
-    const int32_t row = it.key0 + (b0 + j) * kKeys;
-    for (int c = 0; c < D / 64; ++c)
-      tma_load_3d(sm + Sh::kOffRing + st * Sh::kStage + c * Sh::kHalf, isK ? &tmK : &tmV, &full[st], 64 * c,
-                  isK ? (p.k_head ? hk : 0) : (p.v_head ? hk : 0), row);
-  };
-  if (!found || (split > 0 && cnt <= 0)) return;  // nothing to do
   if (warp == kSoftWarps + 1) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
-  }
-  if (warp == kSoftWarps && lane == 0 && cnt > 0) {
-    mbar_arrive_expect_tx(q_full, kTiles * (D / 64) * 128u * static_cast<uint32_t>(p.G * p.nt));
-    for (int t = 0; t < kTiles; ++t)
-      for (int c = 0; c < D / 64; ++c)
-        tma_load_3d(sm + t * Sh::kTile + c * Sh::kHalf, &tmQ, q_full, 64 * c, hk * p.G,
-                    it.tok + t * p.nt);
-    copy_block(0, true, 0);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = static_cast<uint32_t>(uniform(static_cast<int>(tmem_slot)));
   constexpr uint32_t kColO = 256;
+  // The ring holds the K and V blocks in the order of their use, item behind item.  Two tiles:
+  // K0 V0 K1 V1 ...; one tile with two streams: K0 K1 V0 K2 V1 K3 V2 ...  Loads and MMAs walk it
+  // with a cursor each.
+  struct Cursor {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void step() {
+      ph = st + 1 == NS ? ph ^ 1 : ph;
+      st = st + 1 == NS ? 0 : st + 1;
+    }
+  };
 
   if (warp == kSoftWarps) {
-    // ---------------- loads ----------------
+    // ---------------- items and loads ----------------
     bool ok = true;
-    if (lane == 0 && cnt > 0) {
-      int issued = 1;  // the first block of K is under way
-      auto load = [&](int u, bool isK, int j) {
-        const int st = u % NS, turn = u / NS;
-        if (ok && turn > 0) ok = mbar_wait_sleep(&empty[st], static_cast<uint32_t>(turn - 1) & 1, &abort_flag);
-        if (!ok) return;
-        issued = u + 1;
-        copy_block(u, isK, j);
-      };
-      if constexpr (kTwo) {
-        for (int j = 0; j < cnt; ++j) {
-          if (j > 0) load(2 * j, true, j);
-          load(2 * j + 1, false, j);
+    int items = 0, loaded = 0;       // items handed over; those with blocks
+    unsigned issued = 0;             // copies under way or done
+    Cursor at, last;                 // the next one's place, the last one's
+    uint32_t x = blockIdx.x, y = blockIdx.y, asked = 0;
+    if constexpr (!kPrefix) {
+      if (x == 0 && y == 0)  // one warp looks every sequence over
+        for (int64_t s = lane; s < p.a.B; s += 32)
+          if (!sequence_ok(p.a, s)) atomicOr(p.a.err, kErrBadLength);
+    }
+    while (true) {
+      const int hk = static_cast<int>(x % static_cast<unsigned>(p.a.Hkv)), split = static_cast<int>(y);
+      const int slot = static_cast<int>(p.nslots) - 1 - static_cast<int>(x / static_cast<unsigned>(p.a.Hkv));
+      Item it = {};
+      const bool found = find_item<kPrefix>(p, slot, kTiles * p.nt, lane, &it);
+      const int nbA = found ? tile_blocks<kPrefix>(it, it.tok, p.nt) : 0;
+      const int nbB = kTwo ? (found ? tile_blocks<kPrefix>(it, it.tok + p.nt, p.nt) : 0) : nbA;
+      const int nb = nbA > nbB ? nbA : nbB;
+      const int per = blocks_per_split(nb, p.splits);
+      const int b0 = split * per;
+      const int cnt = nb - b0 < per ? nb - b0 : per;  // blocks of this split (<= 0: none)
+      if (found && (split == 0 || cnt > 0)) {
+        const int w = items & 1;
+        // rows of the last block that are the sequence's
+        const int tail = cnt > 0 && (b0 + cnt) * kKeys > it.lk ? it.lk - (b0 + cnt - 1) * kKeys : kKeys;
+        if (lane == 0) {
+          if (items >= 2) ok = mbar_wait_sleep(&work_empty[w], static_cast<uint32_t>((items >> 1) - 1) & 1, &abort_flag);
+          if (ok) {
+            // blocks of each stream: both tiles walk the same blocks, or one tile's are dealt in turn
+            auto clampn = [](int v, int hi) { return v < 0 ? 0 : v < hi ? v : hi; };
+            Work o;
+            o.tok = it.tok;
+            o.tok_end = it.tok_end;
+            o.lk = it.lk;
+            o.hk = hk;
+            o.split = split;
+            o.b0 = b0;
+            o.cnt = cnt;
+            o.nA = kTwo ? clampn(nbA - b0, cnt) : (cnt + 1) / 2;
+            o.nB = kTwo ? clampn(nbB - b0, cnt) : cnt / 2;
+            o.tail = tail;
+            *work_at(w) = o;
+            mbar_arrive(&work_full[w]);
+          }
+          if (ok && cnt > 0) {
+            auto load = [&](bool isK, int j) {
+              // the place's last copy but this one has been read (the phase before the copy's own)
+              if (ok && issued >= NS) ok = mbar_wait_sleep(&empty[at.st], at.ph ^ 1, &abort_flag);
+              if (!ok) return;
+              mbar_arrive_expect_tx(&full[at.st], Sh::kStage);
+              const int32_t row = it.key0 + (b0 + j) * kKeys;
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(sm + Sh::kOffRing + at.st * Sh::kStage + c * Sh::kHalf, isK ? &tmK : &tmV, &full[at.st],
+                            64 * c, isK ? (p.k_head ? hk : 0) : (p.v_head ? hk : 0), row);
+              last = at;
+              at.step();
+              ++issued;
+            };
+            load(true, 0);
+            if (ok && loaded > 0) ok = mbar_wait_sleep(q_empty, static_cast<uint32_t>(loaded - 1) & 1, &abort_flag);
+            if (ok) {
+              mbar_arrive_expect_tx(q_full, kTiles * (D / 64) * 128u * static_cast<uint32_t>(p.G * p.nt));
+              for (int t = 0; t < kTiles; ++t)
+                for (int c = 0; c < D / 64; ++c)
+                  tma_load_3d(sm + t * Sh::kTile + c * Sh::kHalf, &tmQ, q_full, 64 * c, hk * p.G, it.tok + t * p.nt);
+              ++loaded;
+            }
+            constexpr int kLead = kTwo ? 1 : 2;  // S of so many blocks comes before the first P V
+            if (!kTwo && cnt > 1) load(true, 1);
+            for (int j = 0; j < cnt; ++j) {
+              load(false, j);
+              if (j + kLead < cnt) load(true, j + kLead);
+            }
+          }
         }
-      } else {
-        int u = 1;
-        if (cnt > 1) load(u++, true, 1);
-        for (int j = 0; j < cnt; ++j) {
-          load(u++, false, j);
-          if (j + 2 < cnt) load(u++, true, j + 2);
+        ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+        if (ok && tail < kKeys) {
+          // a weight of 0 does not silence a NaN behind the sequence: those rows of V become 0
+          const int st = __shfl_sync(0xFFFFFFFFu, last.st, 0);  // the item's last copy
+          ok = warp_wait(&full[st], __shfl_sync(0xFFFFFFFFu, last.ph, 0), &abort_flag);
+          uint8_t* v = sm + Sh::kOffRing + st * Sh::kStage;
+          if (ok) {
+            for (int c = 0; c < D / 64; ++c)
+              for (int i = tail * 8 + lane; i < kKeys * 8; i += 32)
+                reinterpret_cast<uint4*>(v + c * Sh::kHalf)[i] = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tail_done[w]);
+          }
+        }
+        ++items;
+      }
+      if (!kSteal) break;
+      // asked for as late as the ring's lead allows: what others may take is not held back here
+      if (lane == 0) {
+        mbar_arrive_expect_tx(next_bar, 16);
+        ask_next(next_index, next_bar);
+      }
+      __syncwarp();
+      ok = warp_wait(next_bar, asked & 1, nullptr) && ok;  // the answer lands in any case
+      if (!ok) break;
+      ++asked;
+      const bool more = read_next(next_index, &x, &y);
+      fence_proxy_async_smem();  // the answer has been read before the next one may land
+      __syncwarp();
+      if (!more) break;
+    }
+    if (lane == 0) {
+      if (ok) {  // no more items
+        const int w = items & 1;
+        if (items >= 2) ok = mbar_wait_sleep(&work_empty[w], static_cast<uint32_t>((items >> 1) - 1) & 1, &abort_flag);
+        if (ok) {
+          work_at(w)->cnt = -1;
+          mbar_arrive(&work_full[w]);
         }
       }
       if (!ok) report_error(p.a.err, kErrWaitTimeout, &abort_flag);
       // no copy may still be landing in shared memory when the CTA ends
-      mbar_wait(q_full, 0, nullptr);
-      for (int u = issued > NS ? issued - NS : 0; u < issued; ++u)
-        mbar_wait(&full[u % NS], static_cast<uint32_t>(u / NS) & 1, nullptr);
-    }
-    ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
-    if (tail < kKeys && ok) {
-      // a weight of 0 does not silence a NaN behind the sequence: those rows of V become 0
-      const int st = use_v(cnt - 1) % NS;
-      uint8_t* v = sm + Sh::kOffRing + st * Sh::kStage;
-      for (int c = 0; c < D / 64; ++c)
-        for (int i = tail * 8 + lane; i < kKeys * 8; i += 32)
-          reinterpret_cast<uint4*>(v + c * Sh::kHalf)[i] = make_uint4(0u, 0u, 0u, 0u);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tail_done);
+      if (loaded > 0) mbar_wait(q_full, static_cast<uint32_t>(loaded - 1) & 1, nullptr);
+      for (int i = 0; i < NS && issued >= static_cast<unsigned>(NS); ++i, at.step()) mbar_wait(&full[at.st], at.ph ^ 1, nullptr);
+      for (int i = 0; i < at.st && issued < static_cast<unsigned>(NS); ++i) mbar_wait(&full[i], 0, nullptr);
     }
   } else if (warp == kSoftWarps + 1) {
     // ---------------- MMAs ----------------
-    // the whole warp walks the loop, so that descriptors stay in uniform registers; one lane issues
-    if (cnt > 0) {
-      const bool leader = elect_one();
-      constexpr uint32_t idS = idesc_bf16(kRows, kKeys, 0, 0), idO = idesc_bf16(kRows, D, 0, 1);
-      const uint64_t dQ = sdesc_k_sw128(smem_u32(sm)), dK = sdesc_k_sw128(smem_u32(sm + Sh::kOffRing));
-      const uint64_t dV = sdesc_mn_sw128(smem_u32(sm + Sh::kOffRing), Sh::kHalf, 1024);
-      bool ok = warp_wait(q_full, 0, &abort_flag);
-      auto landed = [&](int u) { ok = ok && warp_poll(&full[u % NS], static_cast<uint32_t>(u / NS) & 1, &abort_flag); };
-      // several at once: one latency where all are there, which is the rule for loads
-      auto all_there = [&](int u0, int u1, int s, int i) {
-        const bool there = mbar_test(&full[u0 % NS], static_cast<uint32_t>(u0 / NS) & 1) &
-                           mbar_test(&full[u1 % NS], static_cast<uint32_t>(u1 / NS) & 1) &
-                           mbar_test(&p_full[s], static_cast<uint32_t>(i) & 1);
-        if (__all_sync(0xFFFFFFFFu, there)) return;
-        landed(u0);
-        landed(u1);
-        ok = ok && warp_poll(&p_full[s], static_cast<uint32_t>(i) & 1, &abort_flag);
-      };
-      auto issue_s = [&](int s, int j) {  // stream s, block j, whose K has landed
-        const uint64_t a = dQ + static_cast<uint64_t>(((kTwo ? s : 0) * Sh::kTile) >> 4);
-        const uint64_t b = dK + static_cast<uint64_t>(((use_k(j) % NS) * Sh::kStage) >> 4);
+    // One elected thread walks the loop.  elect.sync tells the compiler that it is alone: behind a
+    // plain lane == 0 every MMA is issued by a loop over the lanes that might be active.
+    if (elect_one()) {
+    constexpr uint32_t idS = idesc_bf16(kRows, kKeys, 0, 0), idO = idesc_bf16(kRows, D, 0, 1);
+    const uint64_t dQ = sdesc_k_sw128(smem_u32(sm)), dK = sdesc_k_sw128(smem_u32(sm + Sh::kOffRing));
+    const uint64_t dV = sdesc_mn_sw128(smem_u32(sm + Sh::kOffRing), Sh::kHalf, 1024);
+    bool ok = true;
+    int loaded = 0, tails = 0;   // items with blocks; bit w: parity of the tails of place w
+    Cursor at;
+    int doneA = 0, doneB = 0;    // blocks of each stream in earlier items
+    for (int items = 0; ok; ++items) {
+      const int w = items & 1;
+      ok = mbar_poll(&work_full[w], static_cast<uint32_t>(items >> 1) & 1, &abort_flag);
+      if (!ok) break;
+      const Work* o = work_at(w);
+      const int cnt = o->cnt, nA = o->nA, nB = o->nB, tail = o->tail;
+      if (cnt < 0) break;
+      if (cnt > 0) {
+        auto landed = [&](const Cursor& c) { ok = ok && mbar_poll(&full[c.st], c.ph, &abort_flag); };
+        int left = nA + nB;  // S still to come
+        auto issue_s = [&](int s, const Cursor& c) {  // stream s with a block of K, which has landed
+          const uint64_t a = dQ + static_cast<uint64_t>(((kTwo ? s : 0) * Sh::kTile) >> 4);
+          const uint64_t b = dK + static_cast<uint64_t>((c.st * Sh::kStage) >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t o = static_cast<uint64_t>(((k >> 2) * Sh::kHalf + (k & 3) * 32) >> 4);
-          mma_f16_ss(tbase + s * kKeys, a + o, b + o, idS, k > 0 ? 1u : 0u);
-        }
-        mma_commit(&s_full[s]);
-      };
-      auto issue_pv = [&](int s, int j, bool first) {  // 16 keys a step: 8 columns of P, 16 rows of V
-        const uint64_t b = dV + static_cast<uint64_t>(((use_v(j) % NS) * Sh::kStage) >> 4);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = static_cast<uint64_t>(((k >> 2) * Sh::kHalf + (k & 3) * 32) >> 4);
+            mma_f16_ss(tbase + s * kKeys, a + off, b + off, idS, k > 0 ? 1u : 0u);
+          }
+          mma_commit(&s_full[s]);
+        };
+        auto issue_pv = [&](int s, const Cursor& c, bool first) {  // 16 keys a step: 8 columns of P, 16 rows of V
+          const uint64_t b = dV + static_cast<uint64_t>((c.st * Sh::kStage) >> 4);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)  // the second 64 keys' P begins at column 64
-          mma_f16_ts(tbase + kColO + s * D, tbase + s * kKeys + 8 * k + (k >= 4 ? 32 : 0),
-                     b + static_cast<uint64_t>(k * (2048 >> 4)), idO, k > 0 || !first ? 1u : 0u);
-      };
-      // P V of block j (the stream's i-th) and, in the same go, S of the stream's next block
-      auto turn = [&](int s, int j, int i, int next, bool more, bool release_v, bool release_k) {
-        all_there(use_v(j), more ? use_k(next) : use_v(j), s, i);
-        if (!ok) return;
-        tc_fence_after();
-        if (leader) {
-          issue_pv(s, j, i == 0);
+          for (int k = 0; k < kKeys / 16; ++k)  // the second 64 keys' P begins at column 64
+            mma_f16_ts(tbase + kColO + s * D, tbase + s * kKeys + 8 * k + (k >= 4 ? 32 : 0),
+                       b + static_cast<uint64_t>(k * (2048 >> 4)), idO, k > 0 || !first ? 1u : 0u);
+        };
+        // P V of the stream's i-th block and, in the same go, S of its next one
+        auto turn = [&](int s, int i, const Cursor& v, const Cursor& k, bool more, bool release_v, bool release_k) {
+          const uint32_t ph = static_cast<uint32_t>((s == 0 ? doneA : doneB) + i) & 1;
+          // several at once: one latency where all are there, which is the rule for loads
+          const bool there = mbar_test(&full[v.st], v.ph) & (!more || mbar_test(&full[k.st], k.ph)) & mbar_test(&p_full[s], ph);
+          if (!there) {
+            landed(v);
+            if (more) landed(k);
+            ok = ok && mbar_poll(&p_full[s], ph, &abort_flag);
+          }
+          // the item before has to be out of the accumulator
+          if (i == 0 && items > 0) ok = ok && mbar_poll(&o_empty[s], static_cast<uint32_t>(items - 1) & 1, &abort_flag);
+          if (!ok) return;
+          tc_fence_after();
+          if (more) --left;
+          issue_pv(s, v, i == 0);
           if (!more) mma_commit(&o_full[s]);
-          if (release_v) mma_commit(&empty[use_v(j) % NS]);
+          if (release_v) mma_commit(&empty[v.st]);
           if (more) {
-            issue_s(s, next);
-            if (release_k) mma_commit(&empty[use_k(next) % NS]);
+            issue_s(s, k);
+            if (release_k) mma_commit(&empty[k.st]);
+            if (left == 0) mma_commit(q_empty);
+          }
+        };
+        ok = mbar_poll(q_full, static_cast<uint32_t>(loaded) & 1, &abort_flag);
+        ++loaded;
+        const Cursor k0 = at;
+        at.step();
+        const Cursor k1 = at;
+        landed(k0);
+        if (!kTwo && cnt > 1) {
+          at.step();
+          landed(k1);
+        }
+        tc_fence_after();
+        left -= kTwo ? (nA > 0) + (nB > 0) : (cnt > 1 ? 2 : 1);
+        if (ok) {
+          if constexpr (kTwo) {
+            if (nA > 0) issue_s(0, k0);
+            if (nB > 0) issue_s(1, k0);
+            mma_commit(&empty[k0.st]);
+          } else {
+            issue_s(0, k0);
+            mma_commit(&empty[k0.st]);
+            if (cnt > 1) {
+              issue_s(1, k1);
+              mma_commit(&empty[k1.st]);
+            }
+          }
+          if (left == 0) mma_commit(q_empty);
+        }
+        for (int j = 0; ok && j < cnt; ++j) {
+          if (j == cnt - 1 && tail < kKeys) {
+            ok = mbar_poll(&tail_done[w], static_cast<uint32_t>(tails >> w) & 1, &abort_flag);
+            tails ^= 1 << w;
+          }
+          const Cursor v = at;
+          at.step();
+          const Cursor k = at;
+          if (j + (kTwo ? 1 : 2) < cnt) at.step();
+          if constexpr (kTwo) {  // the last stream that walks a block releases it
+            if (ok && j < nA) turn(0, j, v, k, j + 1 < nA, j >= nB, j + 1 >= nB);
+            if (ok && j < nB) turn(1, j, v, k, j + 1 < nB, true, true);
+          } else {
+            if (ok) turn(j & 1, j >> 1, v, k, j + 2 < cnt, true, true);
           }
         }
-        __syncwarp();
-      };
-      landed(use_k(0));
-      if (!kTwo && cnt > 1) landed(use_k(1));
-      tc_fence_after();
-      if (ok && leader) {
-        if constexpr (kTwo) {
-          if (nA > 0) issue_s(0, 0);
-          if (nB > 0) issue_s(1, 0);
-          mma_commit(&empty[use_k(0) % NS]);
-        } else {
-          issue_s(0, 0);
-          mma_commit(&empty[use_k(0) % NS]);
-          if (cnt > 1) {
-            issue_s(1, 1);
-            mma_commit(&empty[use_k(1) % NS]);
-          }
-        }
+        doneA += nA;
+        doneB += nB;
       }
-      __syncwarp();
-      for (int j = 0; ok && j < cnt; ++j) {
-        if constexpr (kTwo) {
-          // the last stream that walks a block releases it
-          if (j == cnt - 1 && tail < kKeys) ok = ok && warp_wait(tail_done, 0, &abort_flag);
-          if (j < nA) turn(0, j, j, j + 1, j + 1 < nA, j >= nB, j + 1 >= nB);
-          if (j < nB) turn(1, j, j, j + 1, j + 1 < nB, true, true);
-        } else {
-          if (j == cnt - 1 && tail < kKeys) ok = ok && warp_wait(tail_done, 0, &abort_flag);
-          turn(j & 1, j, j >> 1, j + 2, j + 2 < cnt, true, true);
-        }
-      }
-      if (!ok && leader) report_error(p.a.err, kErrWaitTimeout, &abort_flag);
-      // every MMA issued has finished before the CTA frees TMEM and shared memory
-      if (leader) mma_commit(end_bar);
-      mbar_wait(end_bar, 0, nullptr);
+      mbar_arrive(&work_empty[w]);
+    }
+    if (!ok) report_error(p.a.err, kErrWaitTimeout, &abort_flag);
+    // every MMA issued has finished before the CTA frees TMEM and shared memory
+    mma_commit(end_bar);
+    mbar_wait(end_bar, 0, nullptr);
     }
   } else {
     // ---------------- softmax, half a row a thread ----------------
@@ -448,199 +592,214 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float* mx_own = reinterpret_cast<float*>(sm + Sh::kOffMax) + (2 * s + hf) * kRows + r;
     float* mx_other = reinterpret_cast<float*>(sm + Sh::kOffMax) + (2 * s + (hf ^ 1)) * kRows + r;
     const int rt = r / p.G;
-    const int tok = it.tok + (kTwo ? s * p.nt : 0) + rt;
-    const bool valid = rt < p.nt && tok < it.tok_end;
-    const int n = s == 0 ? nA : nB;
     const float sl2 = p.scale_log2;
-    // keys this row sees, counted from the CTA's first block
-    const int lim = max(0, (valid ? visible<kPrefix>(it, tok) : 0) - b0 * kKeys);
-    const int whole = __reduce_min_sync(0xFFFFFFFFu, valid ? lim : 0x7FFFFFFF);  // the warp's rows see all keys below
-    float ref = -INFINITY, l = 0.0f;
     bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const int j = kTwo ? i : 2 * i + s;  // block, counted from b0
-      // a wait that gave up is met by all warps of a stream: each goes on to the pair's barrier
-      ok = ok && warp_wait(&s_full[s], static_cast<uint32_t>(i) & 1, &abort_flag);
-      tc_fence_after();
-      uint32_t x[2][32];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32(tS + 32 * c, x[c]);
-      tmem_ld_wait();
-      if ((j + 1) * kKeys > whole) {
-        const int rem = lim - j * kKeys - 64 * hf;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (32 * c + e >= rem) x[c][e] = 0xFF800000u;  // -inf
+    int done = 0, outs = 0;  // blocks of earlier items; earlier items with blocks
+    for (int items = 0;; ++items) {
+      const int w = items & 1;
+      ok = ok && warp_wait(&work_full[w], static_cast<uint32_t>(items >> 1) & 1, &abort_flag);
+      // the warps that meet at barriers below go on together or leave together
+      if (kTwo ? wg_barrier_any<256>(9 + s, !ok) : wg_barrier_any<512>(9, !ok)) {
+        ok = false;
+        break;
       }
-      float m4[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        m4[c] = __uint_as_float(x[c >> 1][16 * (c & 1)]);
-#pragma unroll
-        for (int e = 1; e < 16; ++e) m4[c] = fmaxf(m4[c], __uint_as_float(x[c >> 1][16 * (c & 1) + e]));
+      const Work* o = work_at(w);
+      const int cnt = o->cnt, n = s == 0 ? o->nA : o->nB;
+      if (cnt < 0) break;
+      int lim, whole;
+      {
+        Item it;
+        it.tok_end = o->tok_end;
+        it.lk = o->lk;
+        const int tok = o->tok + (kTwo ? s * p.nt : 0) + rt;
+        const bool valid = rt < p.nt && tok < it.tok_end;
+        // keys this row sees, counted from the split's first block
+        lim = max(0, (valid ? visible<kPrefix>(it, tok) : 0) - o->b0 * kKeys);
+        whole = __reduce_min_sync(0xFFFFFFFFu, valid ? lim : 0x7FFFFFFF);  // the warp's rows see all keys below
       }
-      const float mine = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      // the other half's maximum.  The next block's may overwrite it: its S is there only after
-      // both warps have handed over this block's P, and so have read this
-      *mx_own = mine;
-      asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-      const float mn = fmaxf(mine, *mx_other) * sl2;
-      const bool resc = mn > ref + kRescaleLog2;  // the first block with a visible key always
-      float alpha = 1.0f;
-      if (resc) {
-        alpha = ex2(ref - mn);  // 0 on the first
-        ref = mn;
-      }
-      const float base = ref == -INFINITY ? 0.0f : ref;  // no key seen so far: every weight is 2^-inf = 0
-      const float2 sc2 = make_float2(sl2, sl2), nb2 = make_float2(-base, -base);
-      float2 sum2 = make_float2(0.0f, 0.0f);
+      float ref = -INFINITY, l = 0.0f;
+      for (int i = 0; i < n; ++i) {
+        const int j = kTwo ? i : 2 * i + s;  // block, counted from b0
+        // a wait that gave up is met by all warps of a stream: each goes on to the pair's barrier
+        ok = ok && warp_wait(&s_full[s], static_cast<uint32_t>(done + i) & 1, &abort_flag);
+        tc_fence_after();
+        uint32_t x[2][32];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t pk[16];
+        for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32(tS + 32 * c, x[c]);
+        tmem_ld_wait();
+        if ((j + 1) * kKeys > whole) {
+          const int rem = lim - j * kKeys - 64 * hf;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2 t = __ffma2_rn(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sc2, nb2);
-          t.x = ex2(t.x);
-          t.y = ex2(t.y);
-          sum2 = __fadd2_rn(sum2, t);
-          pk[e] = pack_bf16(t.x, t.y);
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e >= rem) x[c][e] = 0xFF800000u;  // -inf
         }
-        tmem_st_32x32b_x16(tS + 16 * c, pk);
-      }
-      l = fmaf(l, alpha, sum2.x + sum2.y);
-      if (i > 0 && __any_sync(0xFFFFFFFFu, resc)) {
-        // a row's reference moved: scale its O (half of it in each warp), which holds all
-        // earlier P V (they were done before this S was)
-#pragma unroll 1
-        for (int c = 0; c < D / 2; c += 32) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(tO + c, o);
-          tmem_ld_wait();
+        float m4[4];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st_32x32b_x32(tO + c, o);
+        for (int c = 0; c < 4; ++c) {
+          m4[c] = __uint_as_float(x[c >> 1][16 * (c & 1)]);
+#pragma unroll
+          for (int e = 1; e < 16; ++e) m4[c] = fmaxf(m4[c], __uint_as_float(x[c >> 1][16 * (c & 1) + e]));
         }
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[s]);
-    }
-    // the stream's products are done; without any, its Q tile (used below) has still to land
-    if (ok && cnt > 0) {
-      ok = warp_wait(n > 0 ? &o_full[s] : q_full, 0, &abort_flag);
-      tc_fence_after();
-    }
-    if (!ok) report_error(p.a.err, kErrWaitTimeout, &abort_flag);
-    const bool have = ok && n > 0;  // O holds something
-    // the row's sum: both halves'
-    *mx_own = l;
-    asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-    l += *mx_other;
-    float scale = 1.0f;
-    float4* xrow = reinterpret_cast<float4*>(sm + Sh::kOffRing + r * (D * 4 + 16)) + (D / 8) * hf;
-    if constexpr (!kTwo) {
-      // join the two streams: references and sums first, then O through the ring, which both
-      // streams' MMAs and copies have left
-      if (nB > 0) {
-        asm volatile("bar.sync 9, 512;" ::: "memory");  // the maxima's places are free now
-        float2* ml = reinterpret_cast<float2*>(sm + Sh::kOffMax);
-        if (hf == 0) ml[s * kRows + r] = make_float2(have ? ref : -INFINITY, have ? l : 0.0f);
-        asm volatile("bar.sync 9, 512;" ::: "memory");
-        const float2 other = ml[(s ^ 1) * kRows + r];
-        const float top = fmaxf(ref, other.x);
-        scale = ref == -INFINITY ? 0.0f : ex2(ref - top);
-        l = l * scale + (other.x == -INFINITY ? 0.0f : other.y * ex2(other.x - top));
-        ref = top;
-        if (s == 1) {
+        const float mine = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        // Nearly always the reference of the earlier blocks serves: no row of either half is more
+        // than 2^8 above it.  Only where one is do the halves exchange their maxima.  (The next
+        // block's may overwrite them: its S is there only after both warps have handed over this
+        // block's P, and so have read these.)
+        float alpha = 1.0f;
+        const bool any = wg_barrier_any<64>(pair_bar, mine * sl2 > ref + kRescaleLog2);
+        if (any) {
+          *mx_own = mine;
+          asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+          const float mn = fmaxf(mine, *mx_other) * sl2;
+          if (mn > ref + kRescaleLog2) {  // the first block with a visible key always
+            alpha = ex2(ref - mn);        // 0 on the first
+            ref = mn;
+          }
+        }
+        const float base = ref == -INFINITY ? 0.0f : ref;  // no key seen so far: every weight is 2^-inf = 0
+        const float2 sc2 = make_float2(sl2, sl2), nb2 = make_float2(-base, -base);
+        float2 sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 t = __ffma2_rn(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sc2, nb2);
+            t.x = ex2(t.x);
+            t.y = ex2(t.y);
+            sum2 = __fadd2_rn(sum2, t);
+            pk[e] = pack_bf16(t.x, t.y);
+          }
+          tmem_st_32x32b_x16(tS + 16 * c, pk);
+        }
+        l = fmaf(l, alpha, sum2.x + sum2.y);
+        if (any && i > 0) {
+          // a row's reference moved: scale its O (half of it in each warp), which holds all
+          // earlier P V (they were done before this S was)
 #pragma unroll 1
           for (int c = 0; c < D / 2; c += 32) {
             uint32_t o[32];
             tmem_ld_32x32b_x32(tO + c, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              xrow[c / 4 + e] = make_float4(__uint_as_float(o[4 * e]) * scale, __uint_as_float(o[4 * e + 1]) * scale,
-                                            __uint_as_float(o[4 * e + 2]) * scale, __uint_as_float(o[4 * e + 3]) * scale);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st_32x32b_x32(tO + c, o);
           }
         }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[s]);
+      }
+      done += n;
+      if (ok && n > 0) {  // the stream's products are done
+        ok = warp_wait(&o_full[s], static_cast<uint32_t>(outs) & 1, &abort_flag);
+        tc_fence_after();
+      }
+      outs += n > 0 ? 1 : 0;
+      // the row's sum: both halves'
+      *mx_own = l;
+      asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+      l += *mx_other;
+      asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+      float scale = 1.0f, other_scale = 0.0f;
+      const bool both = !kTwo && o->nB > 0;  // the other stream has an O of these rows too
+      if constexpr (!kTwo) {
+        // the two streams' references and sums; stream A then reads both accumulators
+        float2* ml = reinterpret_cast<float2*>(sm + Sh::kOffMax);
+        asm volatile("bar.sync 9, 512;" ::: "memory");  // the sums' places are free now
+        if (hf == 0) ml[s * kRows + r] = make_float2(n > 0 ? ref : -INFINITY, n > 0 ? l : 0.0f);
         asm volatile("bar.sync 9, 512;" ::: "memory");
+        const float2 other = ml[(s ^ 1) * kRows + r];
+        const float top = fmaxf(ref, other.x);
+        scale = ref == -INFINITY ? 0.0f : ex2(ref - top);
+        other_scale = other.x == -INFINITY ? 0.0f : ex2(other.x - top);
+        l = l * scale + other.y * other_scale;
+        ref = top;
+        asm volatile("bar.sync 9, 512;" ::: "memory");  // read before the next item's maxima come
       }
-    }
-    if (kTwo || s == 0) {
-      const bool final_out = p.to_parts == 0;
-      const int head = hk * p.G + (r - rt * p.G);
-      const float over = final_out ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
-      const float inv = scale * over;
-      const int64_t row = static_cast<int64_t>(tok) * p.a.H + head;
-      uint16_t* orow = p.a.o + tok * p.a.st[6] + head * p.a.st[7] + (D / 2) * hf;
-      float* prow = p.part_o + (static_cast<int64_t>(split) * p.a.Tq * p.a.H + row) * D + (D / 2) * hf;
-      if (!final_out && valid && cnt > 0 && hf == 0)
-        p.part_ml[static_cast<int64_t>(split) * p.a.Tq * p.a.H + row] = make_float2(ref, l);
-      // Through shared memory (the stream's own Q tile, which its S products have left), so that
-      // the warp writes whole 128-byte lines: one row a lane would take a store 32 lines.
-      // A lane stages kLine bytes of its row in 16-byte pieces, swizzled as the tile was.
-      constexpr int kLine = D, kPieces = kLine / 16;
-      uint8_t* stage = sm + s * Sh::kTile + (D == 128 ? hf * Sh::kHalf : 0) + 32 * qd * 128;
-      auto piece = [&](int row, int q) {
-        return reinterpret_cast<uint4*>(stage + row * 128 + (((D == 128 ? q : kPieces * hf + q) ^ (row & 7)) << 4));
-      };
-      const unsigned rows = __ballot_sync(0xFFFFFFFFu, valid);
-      auto flush = [&](uint8_t* dst) {  // dst: where this lane's row goes (kLine bytes)
-        __syncwarp();
-        const uint64_t at = reinterpret_cast<uint64_t>(dst);
+      if (kTwo || s == 0) {
+        const int tok = o->tok + (kTwo ? s * p.nt : 0) + rt;
+        const bool valid = rt < p.nt && tok < o->tok_end;
+        const int head = o->hk * p.G + (r - rt * p.G);
+        const bool final_out = p.to_parts == 0;
+        const float over = final_out ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
+        const float inv = scale * over, inv_other = other_scale * over;
+        const int64_t row = static_cast<int64_t>(o->split) * p.a.Tq * p.a.H + static_cast<int64_t>(tok) * p.a.H + head;
+        if (!final_out && valid && cnt > 0 && hf == 0) p.part_ml[row] = make_float2(ref, l);
+        // where this lane's half row goes
+        const uint64_t at = final_out ? reinterpret_cast<uint64_t>(p.a.o + tok * p.a.st[6] + head * p.a.st[7] + (D / 2) * hf)
+                                      : reinterpret_cast<uint64_t>(p.part_o + row * D + (D / 2) * hf);
+        const unsigned rows = __ballot_sync(0xFFFFFFFFu, valid && (final_out || cnt > 0));
+        // kN pieces of 16 bytes of every row, from byte `from` on: transposed among kN lanes, so
+        // that a store covers whole lines (one row a lane would take a store 32 lines)
+        auto put = [&](auto& v, int from) {
+          constexpr int kN = sizeof(v) / 16;
+          transpose_pieces<kN>(v, lane);
 #pragma unroll
-        for (int e = 0; e < kPieces; ++e) {
-          const int row = (32 / kPieces) * e + lane / kPieces, q = lane % kPieces;
-          const uint64_t to = __shfl_sync(0xFFFFFFFFu, at, row);
-          if ((rows >> row) & 1u) *reinterpret_cast<uint4*>(to + 16 * q) = *piece(row, q);
-        }
-        __syncwarp();
-      };
-#pragma unroll 1
-      for (int c = 0; c < D / 2; c += 32) {
-        uint32_t o[32];
-        if (have) {
-          tmem_ld_32x32b_x32(tO + c, o);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;  // no key: 0
-        }
-        float f[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
-        if (!kTwo && nB > 0) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 y = xrow[c / 4 + e];
-            f[4 * e] = fmaf(y.x, over, f[4 * e]);
-            f[4 * e + 1] = fmaf(y.y, over, f[4 * e + 1]);
-            f[4 * e + 2] = fmaf(y.z, over, f[4 * e + 2]);
-            f[4 * e + 3] = fmaf(y.w, over, f[4 * e + 3]);
+          for (int e = 0; e < kN; ++e) {
+            const int from_lane = (lane & ~(kN - 1)) + e;  // whose row this piece belongs to
+            const uint64_t to = __shfl_sync(0xFFFFFFFFu, at, from_lane) + static_cast<uint64_t>(from + 16 * (lane & (kN - 1)));
+            if ((rows >> from_lane) & 1u) *reinterpret_cast<uint4*>(to) = v[e];
           }
-        }
+        };
+        auto channels = [&](int c, float (&f)[32]) {  // 32 of this lane's, from c on
+          if (ok && n > 0) {
+            uint32_t t[32];
+            tmem_ld_32x32b_x32(tO + c, t);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(t[e]) * inv;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = 0.0f;  // no key: 0
+          }
+          if (both && ok) {
+            uint32_t t[32];
+            tmem_ld_32x32b_x32(tO + D + c, t);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(t[e]), inv_other, f[e]);
+          }
+        };
         if (final_out) {
+          uint4 v[D / 16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *piece(lane, c / 8 + e) = make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
-                                                 pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
-          if (c + 32 == D / 2) flush(reinterpret_cast<uint8_t*>(orow));
+          for (int c = 0; c < D / 2; c += 32) {
+            float f[32];
+            channels(c, f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[c / 8 + e] = make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
+                                        pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+          }
+          put(v, 0);
         } else if (cnt > 0) {
-          constexpr int kFloats = kLine / 4;  // of a row, staged at a time
+#pragma unroll 1
+          for (int c = 0; c < D / 2; c += 32) {
+            float f[32];
+            channels(c, f);
+            uint4 v[8];
 #pragma unroll
-          for (int g = 0; g < 32; g += kFloats) {
-#pragma unroll
-            for (int e = 0; e < kPieces; ++e)
-              *piece(lane, e) = make_uint4(__float_as_uint(f[g + 4 * e]), __float_as_uint(f[g + 4 * e + 1]),
-                                           __float_as_uint(f[g + 4 * e + 2]), __float_as_uint(f[g + 4 * e + 3]));
-            flush(reinterpret_cast<uint8_t*>(prow + c + g));
+            for (int e = 0; e < 8; ++e)
+              v[e] = make_uint4(__float_as_uint(f[4 * e]), __float_as_uint(f[4 * e + 1]), __float_as_uint(f[4 * e + 2]),
+                                __float_as_uint(f[4 * e + 3]));
+            put(v, 4 * c);
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&o_empty[s]);
+          if (!kTwo) mbar_arrive(&o_empty[1]);
+        }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&work_empty[w]);
     }
+    if (!ok) report_error(p.a.err, kErrWaitTimeout, &abort_flag);
   }
   tc_fence_before();
   __syncthreads();
