@@ -144,6 +144,13 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _stream_on(stream, d):
+    """_stream for a caller that has looked the current device d up already."""
+    if stream is None and _RAW_STREAM is not None:
+        return _RAW_STREAM(d)
+    return _stream(stream)
+
+
 def _key(table, key, name):
     """table[key], or a ValueError naming the accepted keys."""
     if key not in table:
@@ -413,12 +420,6 @@ def _vector(name, t, dtype, n, d):
     raise ValueError(f"{name}: must be a contiguous CUDA tensor on the current device (cuda:{d})")
 
 
-def _dims(name, t, n):
-    if t.dim() != n:
-        raise ValueError(f"{name}: expected {n} dimensions, got shape {tuple(t.shape)}")
-    return t.shape
-
-
 _STRIDES8, _STRIDES14 = struct.Struct("8q").pack, struct.Struct("14q").pack
 
 
@@ -441,34 +442,33 @@ def q8_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps
     positions int32 [T], inv_freq float64 [rot/2], weights float32 [d] or None (no norm)
     -> (q_out, k_out) bfloat16.  q_out=q, k_out=k work in place (bfloat16)."""
     dev = torch.cuda.current_device()
-    T, H, d = _dims("q", q, 3)
-    Hkv = _dims("k", k, 3)[1]
-    dtype = q.dtype
-    if dtype not in DTYPES:
+    (T, H, d), (_, Hkv, _), (half,) = q.shape, k.shape, inv_freq.shape
+    dtype, bf16, f32 = q.dtype, torch.bfloat16, torch.float32
+    xtype = DTYPES.get(dtype)
+    if xtype is None:
         raise TypeError(f"q: expected bfloat16 or float32, got {dtype}")
     sq, sk = _heads("q", q, dtype, (T, H, d), dev), _heads("k", k, dtype, (T, Hkv, d), dev)
     if q_out is None:
-        q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
-        sqo = (H * d, d, 1)
+        q_out, sqo = torch.empty((T, H, d), dtype=bf16, device=q.device), (H * d, d)
     else:
-        sqo = _heads("q_out", q_out, torch.bfloat16, (T, H, d), dev)
+        sqo = _heads("q_out", q_out, bf16, (T, H, d), dev)
     if k_out is None:
-        k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=q.device)
-        sko = (Hkv * d, d, 1)
+        k_out, sko = torch.empty((T, Hkv, d), dtype=bf16, device=q.device), (Hkv * d, d)
     else:
-        sko = _heads("k_out", k_out, torch.bfloat16, (T, Hkv, d), dev)
+        sko = _heads("k_out", k_out, bf16, (T, Hkv, d), dev)
     if (H > 1 and (sq[1] != d or sqo[1] != d)) or (Hkv > 1 and (sk[1] != d or sko[1] != d)):
         raise ValueError("q, k, q_out, k_out: the heads of a token must be contiguous")
-    half = _dims("inv_freq", inv_freq, 1)[0]
     if T <= 1:  # a single token: its stride says nothing
         sq, sk, sqo, sko = (H * d,), (Hkv * d,), (H * d,), (Hkv * d,)
-    _check(_L.q8_qk_norm_rope(q.data_ptr(), k.data_ptr(), DTYPES[dtype], sq[0], sk[0],
-                              None if q_weight is None else _vector("q_weight", q_weight, torch.float32, d, dev),
-                              None if k_weight is None else _vector("k_weight", k_weight, torch.float32, d, dev),
-                              eps, _vector("positions", positions, torch.int32, T, dev),
-                              _vector("inv_freq", inv_freq, torch.float64, half, dev), 2 * half,
-                              1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), sqo[0], sko[0],
-                              T, H, Hkv, d, _stream(stream)), "q8_qk_norm_rope")
+    status = _L.q8_qk_norm_rope(
+        q.data_ptr(), k.data_ptr(), xtype, sq[0], sk[0],
+        None if q_weight is None else _vector("q_weight", q_weight, f32, d, dev),
+        None if k_weight is None else _vector("k_weight", k_weight, f32, d, dev), eps,
+        _vector("positions", positions, torch.int32, T, dev), _vector("inv_freq", inv_freq, torch.float64, half, dev),
+        2 * half, 1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), sqo[0], sko[0], T, H, Hkv, d,
+        _stream_on(stream, dev))
+    if status:
+        raise Q8Error(status, "q8_qk_norm_rope")
     return q_out, k_out
 
 
@@ -483,8 +483,7 @@ def q8_prompt_attention(q, k, v, cu_q, cu_k=None, scale=None, o=None, workspace=
     -> o [Tq,H,d] bfloat16 (a new o is not initialised outside the sequences).  scale None:
     1/sqrt(d).  workspace None: allocated here with torch."""
     dev = torch.cuda.current_device()
-    Tq, H, d = _dims("q", q, 3)
-    Tk, Hkv, _ = _dims("k", k, 3)
+    (Tq, H, d), (Tk, Hkv, _) = q.shape, k.shape
     sq, sk, sv = (_heads("q", q, torch.bfloat16, (Tq, H, d), dev), _heads("k", k, torch.bfloat16, (Tk, Hkv, d), dev),
                   _heads("v", v, torch.bfloat16, (Tk, Hkv, d), dev))
     n = cu_q.numel()
@@ -499,10 +498,12 @@ def q8_prompt_attention(q, k, v, cu_q, cu_k=None, scale=None, o=None, workspace=
         so = _heads("o", o, torch.bfloat16, (Tq, H, d), dev)
     workspace, pw, nbytes = _workspace(
         workspace, _L.q8_prompt_attention_workspace_size(n - 1, Tq, Tk, H, Hkv, d), q.device, dev)
-    _check(_L.q8_prompt_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), pq, pk, o.data_ptr(), n - 1, Tq, Tk,
-                                  H, Hkv, d, (d or 1) ** -0.5 if scale is None else scale,
-                                  _STRIDES8(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1]), pw, nbytes,
-                                  _stream(stream)), "q8_prompt_attention")
+    status = _L.q8_prompt_attention(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), pq, pk, o.data_ptr(), n - 1, Tq, Tk, H, Hkv, d,
+        (d or 1) ** -0.5 if scale is None else scale,
+        _STRIDES8(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1]), pw, nbytes, _stream_on(stream, dev))
+    if status:
+        raise Q8Error(status, "q8_prompt_attention")
     return o
 
 
@@ -517,9 +518,7 @@ def q8_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, scale=None
     fine), own_len int32 [B] on the device: request b sees the prefix and its first own_len[b]
     own keys -> o [B,H,d] bfloat16.  scale None: 1/sqrt(d).  workspace None: allocated here."""
     dev = torch.cuda.current_device()
-    B, H, d = _dims("q", q, 3)
-    P, Hkv, _ = _dims("k_prefix", k_prefix, 3)
-    cap = _dims("k_own", k_own, 4)[1]
+    (B, H, d), (P, Hkv, _), (_, cap, _, _) = q.shape, k_prefix.shape, k_own.shape
     bf16, shared, own = torch.bfloat16, (P, Hkv, d), (B, cap, Hkv, d)
     sq = _heads("q", q, bf16, (B, H, d), dev)
     skp, svp = _heads("k_prefix", k_prefix, bf16, shared, dev), _heads("v_prefix", v_prefix, bf16, shared, dev)
@@ -532,12 +531,13 @@ def q8_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, scale=None
         so = _heads("o", o, bf16, (B, H, d), dev)
     workspace, pw, nbytes = _workspace(
         workspace, _L.q8_prefix_attention_workspace_size(B, P, cap, H, Hkv, d), q.device, dev)
-    _check(_L.q8_prefix_attention(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_own.data_ptr(),
-                                  v_own.data_ptr(), pn, o.data_ptr(), B, P, cap, H, Hkv, d,
-                                  (d or 1) ** -0.5 if scale is None else scale,
-                                  _STRIDES14(sq[0], sq[1], skp[0], skp[1], svp[0], svp[1], sko[0], sko[1], sko[2],
-                                             svo[0], svo[1], svo[2], so[0], so[1]), pw, nbytes,
-                                  _stream(stream)), "q8_prefix_attention")
+    status = _L.q8_prefix_attention(
+        q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_own.data_ptr(), v_own.data_ptr(), pn, o.data_ptr(),
+        B, P, cap, H, Hkv, d, (d or 1) ** -0.5 if scale is None else scale,
+        _STRIDES14(sq[0], sq[1], skp[0], skp[1], svp[0], svp[1], sko[0], sko[1], sko[2], svo[0], svo[1], svo[2],
+                   so[0], so[1]), pw, nbytes, _stream_on(stream, dev))
+    if status:
+        raise Q8Error(status, "q8_prefix_attention")
     return o
 
 
