@@ -1293,15 +1293,18 @@ struct PrefixPlan {
 PrefixPlan prefix_plan(int64_t B, int64_t P, int64_t cap, int64_t H, int64_t Hkv, const DeviceInfo& dev) {
   const int64_t G = H / Hkv, nt = kRows / G;
   PrefixPlan pl;
-  pl.two = B > nt;
+  // Two tiles a block only where one already fills the GPU twice: with one, half as many partial
+  // results are written (64 requests behind 8192 keys: 31 us a call against 33)
+  pl.two = (B + nt - 1) / nt * Hkv >= 2 * dev.sm_count;
   const int64_t n = pl.two ? 2 * nt : nt, blocks = (P + kKeys - 1) / kKeys;
   pl.nslots = (B + n - 1) / n;
   pl.chunks = static_cast<int>((G + kOwnRows - 1) / kOwnRows);
   const int64_t busy = B * Hkv * pl.chunks;
   // Alone: few shared keys are read again for every request, which costs less than a second
-  // and a third launch (1 request behind 1000 keys: 27 us a call with three, 21 with one), and
-  // clusters of eight fill the GPU or have little to do.
-  pl.alone = B * P <= 4096 && (8 * busy >= 2 * dev.sm_count || P + cap <= 2048);
+  // and a third launch, where no request has so many keys that its few blocks end last (device
+  // time, 1 request behind 1000 keys: 10.5 us against 13.6 with three launches; 64 requests
+  // with up to 2000 keys: 44 us alone; 16 behind 1000: 18 against 13.7)
+  pl.alone = B * P <= 4096 && P + cap <= (busy > 3 * dev.sm_count ? 1024 : 2048);
   if (pl.alone) {
     pl.prefix_splits = 0;
     const int64_t s = std::min(3 * dev.sm_count / busy, (P + cap + 127) / 128);
@@ -1311,8 +1314,11 @@ PrefixPlan prefix_plan(int64_t B, int64_t P, int64_t cap, int64_t H, int64_t Hkv
   const int64_t s = std::max<int64_t>(1, std::min(dev.sm_count / (pl.nslots * Hkv), blocks / 2));
   const int64_t per = (blocks + s - 1) / s;
   pl.prefix_splits = P > 0 ? static_cast<int>((blocks + per - 1) / per) : 0;
-  // Three blocks an SM, or more where lengths differ: a long request is then no block's alone
-  pl.own_splits = static_cast<int>(std::max<int64_t>(1, std::min(std::max<int64_t>(4, 3 * dev.sm_count / busy), cap / 128)));
+  // Three blocks an SM, or, as lengths differ, up to 32 an SM of 256 keys of the longest each:
+  // those of shorter requests end at once (64 requests with up to 4000 keys behind 8192: 51 us
+  // against 59; 512 keys: 30 us with two a request, 31 with four)
+  const int64_t few = 3 * dev.sm_count / busy, many = std::min(cap / 256, 32 * dev.sm_count / busy);
+  pl.own_splits = static_cast<int>(std::max<int64_t>(1, std::min(std::max(few, many), cap / 128)));
   return pl;
 }
 
