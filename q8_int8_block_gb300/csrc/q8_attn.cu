@@ -1314,11 +1314,14 @@ PrefixPlan prefix_plan(int64_t B, int64_t P, int64_t cap, int64_t H, int64_t Hkv
   const int64_t s = std::max<int64_t>(1, std::min(dev.sm_count / (pl.nslots * Hkv), blocks / 2));
   const int64_t per = (blocks + s - 1) / s;
   pl.prefix_splits = P > 0 ? static_cast<int>((blocks + per - 1) / per) : 0;
-  // Three blocks an SM, or, as lengths differ, up to 32 an SM of 256 keys of the longest each:
-  // those of shorter requests end at once (64 requests with up to 4000 keys behind 8192: 51 us
-  // against 59; 512 keys: 30 us with two a request, 31 with four)
-  const int64_t few = 3 * dev.sm_count / busy, many = std::min(cap / 256, 32 * dev.sm_count / busy);
-  pl.own_splits = static_cast<int>(std::max<int64_t>(1, std::min(std::max(few, many), cap / 128)));
+  // One wave of three blocks an SM; with more than a few requests, whose lengths differ, more and
+  // smaller ones (256 keys of the longest each, 32 an SM, 64 results to join at most): those of
+  // shorter requests end at once (64 requests with up to 4000 keys behind 8192: 51 us against 59
+  // with one wave; 512 keys: 30 us with two a request, 31 with four; 1 request with 131072 keys:
+  // 92 us with one wave, 109 with 64 splits)
+  const int64_t few = 3 * dev.sm_count / busy;
+  const int64_t many = std::min<int64_t>({cap / 256, 32 * dev.sm_count / busy, 64});
+  pl.own_splits = static_cast<int>(std::max<int64_t>(1, std::min(few < 16 ? std::max(few, many) : few, cap / 128)));
   return pl;
 }
 
