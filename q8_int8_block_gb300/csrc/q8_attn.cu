@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   using Sh = TileShape<D, kTwo>;
   constexpr int NS = Sh::kStages;
   constexpr bool kSteal = !kPrefix;
-  if constexpr (kPrefix) pdl_launch_dependents();  // the requests' own keys may start
+  if (kPrefix || p.to_parts != 0) pdl_launch_dependents();  // the requests' own keys, or the join, may start
   extern __shared__ __align__(1024) uint8_t sm[];
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = static_cast<int>(threadIdx.x & 31);
   if ((smem_u32(sm) & 1023u) != 0) {  // the whole CTA leaves before touching anything
@@ -856,6 +856,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
   const int nb = nbA > nbB ? nbA : nbB;
   const int per = blocks_per_split(nb, p.splits), used = per > 0 ? (nb + per - 1) / per : 0;
   const int64_t rows = p.a.Tq * p.a.H;
+  pdl_wait();
   for (int r = blockIdx.y * 8 + warp; r < ntok * p.G; r += 8 * gridDim.y) {
     const int64_t tok = it.tok + r / p.G;
     if (tok >= it.tok_end) break;
@@ -1224,6 +1225,31 @@ bool encode_rows(CUtensorMap* map, const void* ptr, int64_t d, int64_t heads, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch that may begin before the kernel in front of it has ended (dependent), or whose
+// `cluster` blocks of the same grid column form a cluster.
+template <typename K, typename... A>
+cudaError_t launch_with(K kernel, dim3 grid, unsigned threads, size_t smem, bool dependent, int cluster,
+                        cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (dependent) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = 1;
+    attr[cfg.numAttrs].val.clusterDim.y = static_cast<unsigned>(cluster);
+    attr[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int D, bool kTwo, bool kPrefix>
 cudaError_t launch_tiles(TileParams& p, const DeviceInfo& dev, cudaStream_t stream) {
   const PromptArgs& a = p.a;
@@ -1256,7 +1282,9 @@ PromptPlan prompt_plan(int64_t B, int64_t Tq, int64_t Tk, int64_t H, int64_t Hkv
   pl.two = (Tq / (2 * nt) + 1) * Hkv >= dev.sm_count;
   const int64_t n = pl.two ? 2 * nt : nt;
   pl.nslots = Tq / n + B;
-  const int64_t busy = (Tq / n + 1) * Hkv, blocks = (Tk + kKeys - 1) / kKeys;
+  // Keys are split where the blocks in work (a sequence has one at least) leave SMs without any,
+  // eight key blocks a split: with fewer the join costs what the split saves
+  const int64_t busy = (Tq / n + std::min(B, Tq)) * Hkv, blocks = (Tk + kKeys - 1) / kKeys;
   pl.splits = static_cast<int>(std::max<int64_t>(1, std::min(dev.sm_count / busy, blocks / 8)));
   return pl;
 }
@@ -1277,9 +1305,8 @@ cudaError_t prompt_attention(const PromptArgs& a, const DeviceInfo& dev, cudaStr
   cudaError_t e = pl.two ? launch_tiles<D, true, false>(p, dev, stream) : launch_tiles<D, false, false>(p, dev, stream);
   if (e != cudaSuccess || pl.splits == 1) return e;
   const dim3 grid(static_cast<unsigned>(pl.nslots * a.Hkv), 4);
-  if (pl.two) prompt_join_kernel<D, true><<<grid, 256, 0, stream>>>(p);
-  else prompt_join_kernel<D, false><<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return pl.two ? launch_with(prompt_join_kernel<D, true>, grid, 256, 0, true, 1, stream, p)
+                : launch_with(prompt_join_kernel<D, false>, grid, 256, 0, true, 1, stream, p);
 }
 
 // How a prefix call is cut up.
@@ -1323,31 +1350,6 @@ PrefixPlan prefix_plan(int64_t B, int64_t P, int64_t cap, int64_t H, int64_t Hkv
   const int64_t many = std::min<int64_t>({cap / 256, 32 * dev.sm_count / busy, 64});
   pl.own_splits = static_cast<int>(std::max<int64_t>(1, std::min(few < 16 ? std::max(few, many) : few, cap / 128)));
   return pl;
-}
-
-// A launch that may begin before the kernel in front of it has ended (dependent), or whose
-// `cluster` blocks of the same grid column form a cluster.
-template <typename K, typename... A>
-cudaError_t launch_with(K kernel, dim3 grid, unsigned threads, size_t smem, bool dependent, int cluster,
-                        cudaStream_t stream, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  cfg.attrs = attr;
-  if (dependent) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster > 1) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attr[cfg.numAttrs].val.clusterDim.x = 1;
-    attr[cfg.numAttrs].val.clusterDim.y = static_cast<unsigned>(cluster);
-    attr[cfg.numAttrs++].val.clusterDim.z = 1;
-  }
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int D>
