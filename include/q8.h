@@ -266,11 +266,13 @@ q8_status q8_qk_norm_rope(const void* q, const void* k, q8_dtype xtype, int64_t 
  *     the context (lk > lq: the earlier keys were cached before).  A query that sees no key
  *     gets 0.  Rows of o outside every sequence are left as they are, and nothing outside a
  *     sequence's own keys reaches its outputs.  A sequence that is not inside [0, Tq] x
- *     [0, Tk] or has a negative length is skipped and sets bit 9 of the device error word;
+ *     [0, Tk] or has a negative length is skipped and sets bit 9 of the device error word (the
+ *     ones beside it are then found only where cu_q still rises);
  *   o = sum_j p_j v_j / sum_j p_j, p_j = exp(scale * (q . k_j) - max); scale finite and > 0
  *     (else Q8_ERR_VALUE).
  * Scores, maxima, sums and o are binary32; the weights p enter the product with v rounded to
- * bfloat16 (as in q8_bsa_attention), and o is rounded to bfloat16 once.
+ * bfloat16 (as in q8_bsa_attention), and o is rounded to bfloat16 once.  o may not share
+ * memory with an input.
  * workspace: at least q8_prompt_attention_workspace_size() bytes, 16-byte aligned (partial
  * results where the keys are split among several blocks; NULL where that size is 0).  Calls
  * that overlap in time need one each.  Never allocates.

@@ -423,12 +423,20 @@ def _vector(name, t, dtype, n, d):
 _STRIDES8, _STRIDES14 = struct.Struct("8q").pack, struct.Struct("14q").pack
 
 
-def _workspace(workspace, need, device, d):
+def _empty(shape, dtype, device, stream):
+    """A new tensor for work on `stream`: torch hands its memory on in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(workspace, need, device, d, stream):
     """(tensor or None, address or None, bytes): the caller's workspace, else one from torch."""
     if workspace is None:
         if need == 0:
             return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _empty(need, torch.uint8, device, stream)
         return workspace, workspace.data_ptr(), need
     if workspace.get_device() != d or not workspace.is_contiguous():
         raise ValueError(f"workspace: must be a contiguous CUDA tensor on the current device (cuda:{d})")
@@ -449,11 +457,11 @@ def q8_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps
         raise TypeError(f"q: expected bfloat16 or float32, got {dtype}")
     sq, sk = _heads("q", q, dtype, (T, H, d), dev), _heads("k", k, dtype, (T, Hkv, d), dev)
     if q_out is None:
-        q_out, sqo = torch.empty((T, H, d), dtype=bf16, device=q.device), (H * d, d)
+        q_out, sqo = _empty((T, H, d), bf16, q.device, stream), (H * d, d)
     else:
         sqo = _heads("q_out", q_out, bf16, (T, H, d), dev)
     if k_out is None:
-        k_out, sko = torch.empty((T, Hkv, d), dtype=bf16, device=q.device), (Hkv * d, d)
+        k_out, sko = _empty((T, Hkv, d), bf16, q.device, stream), (Hkv * d, d)
     else:
         sko = _heads("k_out", k_out, bf16, (T, Hkv, d), dev)
     if (H > 1 and (sq[1] != d or sqo[1] != d)) or (Hkv > 1 and (sk[1] != d or sko[1] != d)):
@@ -481,7 +489,7 @@ def q8_prompt_attention(q, k, v, cu_q, cu_k=None, scale=None, o=None, workspace=
     128; strided views are fine), cu_q and cu_k int32 [B+1] on the device: sequence s holds the
     queries cu_q[s]:cu_q[s+1], the last ones of its keys cu_k[s]:cu_k[s+1] (None: cu_q)
     -> o [Tq,H,d] bfloat16 (a new o is not initialised outside the sequences).  scale None:
-    1/sqrt(d).  workspace None: allocated here with torch."""
+    1/sqrt(d).  workspace None: allocated here with torch (as a new o, on `stream`)."""
     dev = torch.cuda.current_device()
     (Tq, H, d), (Tk, Hkv, _) = q.shape, k.shape
     sq, sk, sv = (_heads("q", q, torch.bfloat16, (Tq, H, d), dev), _heads("k", k, torch.bfloat16, (Tk, Hkv, d), dev),
@@ -492,12 +500,12 @@ def q8_prompt_attention(q, k, v, cu_q, cu_k=None, scale=None, o=None, workspace=
     pq = _vector("cu_q", cu_q, torch.int32, n, dev)
     pk = pq if cu_k is None else _vector("cu_k", cu_k, torch.int32, n, dev)
     if o is None:
-        o = torch.empty((Tq, H, d), dtype=torch.bfloat16, device=q.device)
+        o = _empty((Tq, H, d), torch.bfloat16, q.device, stream)
         so = (H * d, d)
     else:
         so = _heads("o", o, torch.bfloat16, (Tq, H, d), dev)
     workspace, pw, nbytes = _workspace(
-        workspace, _L.q8_prompt_attention_workspace_size(n - 1, Tq, Tk, H, Hkv, d), q.device, dev)
+        workspace, _L.q8_prompt_attention_workspace_size(n - 1, Tq, Tk, H, Hkv, d), q.device, dev, stream)
     status = _L.q8_prompt_attention(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), pq, pk, o.data_ptr(), n - 1, Tq, Tk, H, Hkv, d,
         (d or 1) ** -0.5 if scale is None else scale,
@@ -516,7 +524,8 @@ def q8_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, scale=None
     """One query for each of B requests behind a shared prefix: q [B,H,d], k_prefix and
     v_prefix [P,Hkv,d], k_own and v_own [B,cap,Hkv,d] bfloat16 (d 64 or 128; strided views are
     fine), own_len int32 [B] on the device: request b sees the prefix and its first own_len[b]
-    own keys -> o [B,H,d] bfloat16.  scale None: 1/sqrt(d).  workspace None: allocated here."""
+    own keys -> o [B,H,d] bfloat16.  scale None: 1/sqrt(d).  workspace None: allocated here with
+    torch (as a new o, on `stream`)."""
     dev = torch.cuda.current_device()
     (B, H, d), (P, Hkv, _), (_, cap, _, _) = q.shape, k_prefix.shape, k_own.shape
     bf16, shared, own = torch.bfloat16, (P, Hkv, d), (B, cap, Hkv, d)
@@ -525,12 +534,12 @@ def q8_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, scale=None
     sko, svo = _heads("k_own", k_own, bf16, own, dev), _heads("v_own", v_own, bf16, own, dev)
     pn = _vector("own_len", own_len, torch.int32, B, dev)
     if o is None:
-        o = torch.empty((B, H, d), dtype=bf16, device=q.device)
+        o = _empty((B, H, d), bf16, q.device, stream)
         so = (H * d, d)
     else:
         so = _heads("o", o, bf16, (B, H, d), dev)
     workspace, pw, nbytes = _workspace(
-        workspace, _L.q8_prefix_attention_workspace_size(B, P, cap, H, Hkv, d), q.device, dev)
+        workspace, _L.q8_prefix_attention_workspace_size(B, P, cap, H, Hkv, d), q.device, dev, stream)
     status = _L.q8_prefix_attention(
         q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_own.data_ptr(), v_own.data_ptr(), pn, o.data_ptr(),
         B, P, cap, H, Hkv, d, (d or 1) ** -0.5 if scale is None else scale,

@@ -786,7 +786,7 @@ std::map<std::pair<const void*, int>, int> g_regs;
 
 int device_info(DeviceInfo* out) { return static_cast<int>(current_device(out)); }
 
-cudaError_t ensure_smem(const void* fn, size_t bytes, int device) {
+cudaError_t ensure_smem(const void* fn, size_t bytes, int device) try {
   std::lock_guard<std::mutex> lock(g_attr_mu);
   size_t& cur = g_smem_set[{fn, device}];
   if (cur >= bytes) return cudaSuccess;
@@ -794,6 +794,8 @@ cudaError_t ensure_smem(const void* fn, size_t bytes, int device) {
       cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
   if (e == cudaSuccess) cur = bytes;
   return e;
+} catch (...) {  // no exception may leave a C entry point
+  return cudaErrorMemoryAllocation;
 }
 
 void forget_kernel_attributes() {

@@ -4,6 +4,18 @@
 // Qwen3.5/3.6 hybrid models on mining cards (CMP 100-210)" (news.hada.io topic 29953) runs:
 // o = softmax(scale q . k) v over the keys a query sees, H query heads over Hkv key/value
 // heads.
+//
+// Both entry points walk the keys once with a running reference m and sum l per row (online
+// softmax; Milakov and Gimelshein, 2018): for a block of scores s, w = 2^(s' - m) with
+// s' = s scale log2(e);  l += sum w;  O += w V;  where a row's maximum has left m behind, l and
+// O are first scaled by 2^(m - m').  Parts of a row that different blocks walked are joined by
+// o = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p, M = max m_p, in a fixed order.
+// Scores, m, l and O are binary32; w is rounded to bfloat16 for the product with V only (l sums
+// the unrounded weights), o once at the end.
+//
+//  attn_tile_kernel    whole prompts, and a batch's queries over its shared prefix: tensor work
+//  attn_own_kernel     a request's own keys, which no other reads: the bytes of its cache
+//  *_join_kernel       the splits of a row
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -34,6 +46,31 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- the tile kernel ---------------------------------------------------------------------
+// The rows of a tile are the G heads of 128 / G neighbouring tokens: the heads that share a
+// key/value head are rows of the same products, so K and V are read once for all of them and
+// a causal tile of few tokens wastes little of its diagonal block.
+//
+// Bound: the tensor pipe.  A block of 128 keys takes d / 16 + 8 MMAs of 64 cycles (S = Q K^T, and
+// O += P V): 1024 cycles at d = 128.  Its softmax takes about 1500 from the S committed to the
+// P handed over, so one stream of blocks would leave the pipe idle most of the time.  Hence
+// two streams, A and B, each with its S (128 columns of TMEM) and O (d columns): while one is in its
+// softmax the pipe works on the other.
+//  - kTwo: the streams are two tiles behind one another in the sequence that walk the same
+//    blocks of K and V (each is loaded once for 256 rows).
+//  - else: one tile, whose even and odd blocks are the streams; their O are joined at the end.
+// P takes the place of S in TMEM, as the A operand of P V.  Softmax: sixteen warps, eight a
+// stream, two for 32 rows, each thread half a row (64 scores in registers, no shuffles); with
+// four warps a stream, a row a thread, 8192 tokens took 480 us instead of 372.  One warp finds the items and
+// loads (TMA, a ring of 5 to 8 K or V blocks that runs over from item to item), one elected
+// thread issues the MMAs.
+// The reference moves only when a row's maximum gains more than 2^8 (weights stay below 2^8, far
+// from the ends of binary32 and of bfloat16's equal range): rescaling O is rare.
+// The blocks are persistent: the next item (tile, head, split) is asked for while the current
+// one is in work, the last ones of a sequence, which see the most keys, first.
+//
+// 32 query heads, 8 key/value heads of 128: 8192 tokens in 345 us (1.59 PFLOP/s counted over the
+// causal half, 0.84 of the measured dense rate), 16384 tokens at 1.85 PFLOP/s.  What is left
+// there is the clock under load, and the ends: the first S and the last O of a block's items.
 constexpr int kRows = 128;     // query rows of a tile: 128 / G tokens x G heads
 constexpr int kKeys = 128;     // keys of a block
 constexpr int kSoftWarps = 16;  // softmax: 8 warps a stream, two (a half of the keys each) for 32 rows
@@ -111,9 +148,8 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
-// A value that is the same on all lanes, told to the compiler as such: the MMA warp's loop and
-// its descriptors then stay in uniform registers.  Without it each MMA took ~90 cycles to issue
-// next to the softmax warps, with it the tensor pipe's 64.
+// A value that is the same on all lanes, told to the compiler as such (loop counts and branches
+// on it then need no reconvergence; 5 % of a long prompt).
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // A test of a barrier's phase that does not suspend: polling with it sees a phase complete about
@@ -202,7 +238,8 @@ __device__ __forceinline__ int visible(const Item& it, int t) {
 }
 
 // Slots: sequence s owns the slots from cu_q[s] / n + s on, at least as many as it has groups
-// of n tokens, so a slot finds its sequence by a search over cu_q alone, without a plan.  All
+// of n tokens (there are Tq / n + B in all), so a slot finds its sequence by a search over cu_q
+// alone: no plan is made in front of the launch.  All
 // lanes of a warp search together: 32 probes a round until 32 sequences are left, whose four
 // bounds are then read at once, so up to 32 sequences cost one memory latency.
 __device__ __forceinline__ bool prompt_item(const PromptArgs& a, int slot, int n, int lane, Item* it) {
@@ -271,7 +308,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   using Sh = TileShape<D, kTwo>;
   constexpr int NS = Sh::kStages;
   constexpr bool kSteal = !kPrefix;
-  if (kPrefix || p.to_parts != 0) pdl_launch_dependents();  // the requests' own keys, or the join, may start
+  // the requests' own keys, or the join, may start (one token behind 2000 keys: 16.5 us, 18.5 without)
+  if (kPrefix || p.to_parts != 0) pdl_launch_dependents();
   extern __shared__ __align__(1024) uint8_t sm[];
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = static_cast<int>(threadIdx.x & 31);
   if ((smem_u32(sm) & 1023u) != 0) {  // the whole CTA leaves before touching anything
@@ -469,7 +507,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else if (warp == kSoftWarps + 1) {
     // ---------------- MMAs ----------------
     // One elected thread walks the loop.  elect.sync tells the compiler that it is alone: behind a
-    // plain lane == 0 every MMA is issued by a loop over the lanes that might be active.
+    // plain lane == 0 every MMA is issued by a loop over the lanes that might be active (250
+    // cycles an MMA next to the softmax warps, against the pipe's 64).
     if (elect_one()) {
     constexpr uint32_t idS = idesc_bf16(kRows, kKeys, 0, 0), idO = idesc_bf16(kRows, D, 0, 1);
     const uint64_t dQ = sdesc_k_sw128(smem_u32(sm)), dK = sdesc_k_sw128(smem_u32(sm + Sh::kOffRing));
@@ -843,21 +882,21 @@ __device__ __forceinline__ void join_parts(int used, int from, int step, int lan
   }
 }
 
-template <int D, bool kTwo>
+// The splits of a prompt's rows (one tile a block: two are only taken where nothing is split).
+template <int D>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ TileParams p) {
   constexpr int E = D / 32;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int hk = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.a.Hkv));
   const int slot = static_cast<int>(p.nslots) - 1 - static_cast<int>(blockIdx.x / static_cast<unsigned>(p.a.Hkv));
-  const int ntok = (kTwo ? 2 : 1) * p.nt;
   Item it;
-  if (!prompt_item(p.a, slot, ntok, lane, &it)) return;
-  const int nbA = tile_blocks<false>(it, it.tok, p.nt), nbB = kTwo ? tile_blocks<false>(it, it.tok + p.nt, p.nt) : 0;
-  const int nb = nbA > nbB ? nbA : nbB;
+  const bool found = prompt_item(p.a, slot, p.nt, lane, &it);
+  pdl_wait();  // in every block: what follows on the stream has to find the tiles done
+  if (!found) return;
+  const int nb = tile_blocks<false>(it, it.tok, p.nt);
   const int per = blocks_per_split(nb, p.splits), used = per > 0 ? (nb + per - 1) / per : 0;
   const int64_t rows = p.a.Tq * p.a.H;
-  pdl_wait();
-  for (int r = blockIdx.y * 8 + warp; r < ntok * p.G; r += 8 * gridDim.y) {
+  for (int r = blockIdx.y * 8 + warp; r < p.nt * p.G; r += 8 * gridDim.y) {
     const int64_t tok = it.tok + r / p.G;
     if (tok >= it.tok_end) break;
     const int64_t head = hk * p.G + r % p.G, row = tok * p.a.H + head;
@@ -1040,24 +1079,25 @@ __global__ void __launch_bounds__(32 * kOwnWarps, 3) attn_own_kernel(const __gri
         for (int e = 0; e < 4; ++e)
           if (8 * x + 2 * t + (e & 1) >= left) s[x][e] = -INFINITY;
     }
-    float alpha[2];
+    float alpha[2], base[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float m = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)) * sl2;
       alpha[h] = 1.0f;
-      if (m > ref[h]) {  // a piece holds a visible key, so the reference is finite from the first on
+      if (m > ref[h]) {
         alpha[h] = ex2(ref[h] - m);
         ref[h] = m;
       }
+      base[h] = ref[h] == -INFINITY ? 0.0f : ref[h];  // scores of -inf only: every weight is 0
     }
     uint32_t pa[4];
     float w[2][4];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[x][e] = ex2(fmaf(s[x][e], sl2, -ref[e >> 1]));
+      for (int e = 0; e < 4; ++e) w[x][e] = ex2(fmaf(s[x][e], sl2, -base[e >> 1]));
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       l[h] = fmaf(l[h], alpha[h], (w[0][2 * h] + w[0][2 * h + 1]) + (w[1][2 * h] + w[1][2 * h + 1]));
@@ -1279,11 +1319,16 @@ struct PromptPlan {
 PromptPlan prompt_plan(int64_t B, int64_t Tq, int64_t Tk, int64_t H, int64_t Hkv, const DeviceInfo& dev) {
   const int64_t nt = kRows / (H / Hkv);
   PromptPlan pl;
+  // Two tiles a block where that still gives every SM one: K and V are then loaded once for 256
+  // rows, and no O is joined (4 prompts of up to 1531 tokens, 16 heads of 64: 26 us, 28.7 with one
+  // tile; 512 tokens behind 8192, whose blocks are too few: 107 us with one tile and the keys in
+  // two splits, 114 with two tiles and four)
   pl.two = (Tq / (2 * nt) + 1) * Hkv >= dev.sm_count;
   const int64_t n = pl.two ? 2 * nt : nt;
   pl.nslots = Tq / n + B;
-  // Keys are split where the blocks in work (a sequence has one at least) leave SMs without any,
-  // eight key blocks a split: with fewer the join costs what the split saves
+  // Keys are split where the blocks in work leave SMs without any (a sequence counts as one block at
+  // least: 64 single tokens of 2048 keys take 86 us so, 114 in two splits), eight key blocks a
+  // split at least: with four, 128 tokens behind 1000 take 17 us instead of 14.5
   const int64_t busy = (Tq / n + std::min(B, Tq)) * Hkv, blocks = (Tk + kKeys - 1) / kKeys;
   pl.splits = static_cast<int>(std::max<int64_t>(1, std::min(dev.sm_count / busy, blocks / 8)));
   return pl;
@@ -1305,8 +1350,7 @@ cudaError_t prompt_attention(const PromptArgs& a, const DeviceInfo& dev, cudaStr
   cudaError_t e = pl.two ? launch_tiles<D, true, false>(p, dev, stream) : launch_tiles<D, false, false>(p, dev, stream);
   if (e != cudaSuccess || pl.splits == 1) return e;
   const dim3 grid(static_cast<unsigned>(pl.nslots * a.Hkv), 4);
-  return pl.two ? launch_with(prompt_join_kernel<D, true>, grid, 256, 0, true, 1, stream, p)
-                : launch_with(prompt_join_kernel<D, false>, grid, 256, 0, true, 1, stream, p);
+  return launch_with(prompt_join_kernel<D>, grid, 256, 0, true, 1, stream, p);
 }
 
 // How a prefix call is cut up.

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 8) qk_norm_rope_kernel(const RopePar
   __shared__ __align__(16) float cos_s[kMaxTokens * kMaxD / 2], sin_s[kMaxTokens * kMaxD / 2];
   __shared__ __align__(16) float w_s[2][kMaxD];
   const int lane = threadIdx.x % kLanes, team = threadIdx.x / kLanes;
-  const unsigned mask = (kLanes == 32 ? 0xFFFFFFFFu : ((1u << kLanes) - 1u)) << (threadIdx.x & 31 & ~(kLanes - 1));
+  const unsigned mask = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
   const int per_token = kTeams / p.tokens, mine = team / per_token, first = team - mine * per_token;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens, t = t0 + mine;
   const bool active = 16 * lane < p.d && t < p.T;

@@ -252,6 +252,92 @@ def test_keys_behind_4_gigabytes(q8):
     R.assert_within(o, *R.prefix(q[:2], k, v, *own, [65, 33]))
 
 
+@pytest.mark.parametrize("H,Hkv,d", [(2, 2, 64), (4, 1, 128), (16, 16, 64)])
+@pytest.mark.parametrize("B,longest", [(33, 9), (1025, 3), (1500, 70)])
+def test_many_sequences(q8, B, longest, H, Hkv, d):
+    """More sequences than one round of the search tells apart, empty ones among them, and far
+    more work items than the GPU has SMs."""
+    _prompt(q8, [(i * 7) % (longest + 1) for i in range(B)], [(i * 7) % (longest + 1) for i in range(B)], H, Hkv, d,
+            seed=B)
+
+
+def test_few_new_tokens_among_many_empty_sequences(q8):
+    """Split keys with more items than SMs: most of them belong to sequences without a query."""
+    nq, nk = [0] * 700, [0] * 700
+    nq[3], nk[3], nq[350], nk[350], nq[699], nk[699] = 1, 9000, 5, 4000, 2, 20000
+    nk[5] = 77
+    _prompt(q8, nq, nk, 8, 2, 128, seed=8)
+    _prompt(q8, nq, nk, 4, 4, 64, seed=8)
+
+
+def test_every_shape_again_and_again(q8):
+    """Calls of different cuts behind one another on one stream, each as it is alone."""
+    calls = []
+    for s, (nq, nk, H, Hkv, d) in enumerate([([900, 70], [900, 70], 32, 8, 128), ([1], [9000], 8, 2, 128),
+                                             ([40] * 30, [40] * 30, 16, 16, 64), ([3, 2], [4000, 10], 8, 1, 64)]):
+        q, k, v, tq, tk, o = _prompt(q8, nq, nk, H, Hkv, d, seed=s)
+        calls.append((q8.q8_prompt_attention, (q, k, v, tq, tk), o))
+    for B, P, cap in ((1, 300, 60), (20, 3000, 100), (5, 9000, 3000), (70, 0, 40)):
+        a = _prefix(q8, B, P, cap, [(i * 29 + cap) % (cap + 1) for i in range(B)], 8, 2, 128, seed=B)
+        calls.append((q8.q8_prefix_attention, a[:6], a[6]))
+    for i in range(40):
+        got = [f(*a) for f, a, _ in calls]
+        for j, (x, (_, _, want)) in enumerate(zip(got, calls)):
+            assert torch.equal(x, want), (i, j)
+    assert q8.q8_device_error() == 0
+
+
+@pytest.mark.parametrize("n", [300, 5000])
+def test_scores_of_minus_infinity_weigh_nothing(q8, n):
+    """Visible keys whose score is below binary32: the others carry the softmax."""
+    H, Hkv, d = 4, 2, 128
+    q, k, v = _rand(1, 3, H, d), _rand(2, n, Hkv, d), _rand(3, n, Hkv, d)
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[:160], bad[200:203] = True, True
+    q[..., 0], k[..., 0] = 2.0 ** 100, 0.0
+    good_k, good_v = k[~bad], v[~bad]
+    k[bad, :, 0] = -2.0 ** 100
+    ln = torch.tensor([n] * 3, dtype=torch.int32, device="cuda")
+    z = k[:0]
+    m = good_k.shape[0]
+    q0, one = q.clone(), lambda x: x[None].expand(3, *x.shape)
+    q0[..., 0] = 0  # the same scores over the good keys: their first channel is 0
+    want = R.prefix(q0, z, z, one(good_k), one(good_v), [m] * 3)
+    R.assert_within(q8.q8_prefix_attention(q, z, z, one(k), one(v), ln), *want, "own keys")
+    R.assert_within(q8.q8_prefix_attention(q, k, v, one(z), one(z), ln * 0), *want, "shared keys")
+    for i in range(3):
+        got = q8.q8_prompt_attention(q[i:i + 1], k, v, torch.tensor([0, 1], dtype=torch.int32, device="cuda"),
+                                     torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+        R.assert_within(got, want[0][i:i + 1], want[1][i:i + 1], "prompt")
+
+
+def test_work_on_a_stream_that_is_not_current(q8):
+    """New outputs and workspaces belong to the stream of the call: what the current stream does
+    with freed memory does not reach them, nor they it."""
+    (cq, tq), (ck, tk) = _cum([1]), _cum([50000])
+    a = _rand(1, 1, 8, 128), _rand(2, 50000, 2, 128), _rand(3, 50000, 2, 128), tq, tk
+    want = q8.q8_prompt_attention(*a)
+    need = q8.q8_prompt_attention_workspace_size(1, 1, 50000, 8, 2, 128)
+    assert need > 0
+    side = torch.cuda.Stream()
+    x = torch.empty_like(want)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(10_000_000)  # the current stream still writes x when the side stream is done
+    x.fill_(NAN)
+    del x
+    got = q8.q8_prompt_attention(*a, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    o = torch.empty_like(want)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(10_000_000)  # the workspace is written when the call is long over
+    q8.q8_prompt_attention(*a, o=o, stream=side)
+    y = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and (y == 0).all()
+
+
 def test_empty_prompts(q8):
     z = torch.empty(0, 4, 64, dtype=BF16, device="cuda")
     t = lambda c: torch.tensor(c, dtype=torch.int32, device="cuda")  # noqa: E731
@@ -304,6 +390,13 @@ def test_long_prefix_and_large_batches(q8):
     _prefix(q8, 2, 70001, 300, [300, 1], 8, 2, 128)
     _prefix(q8, 300, 1000, 40, [i % 41 for i in range(300)], 4, 1, 128)
     _prefix(q8, 1, 60, 30011, [30011], 8, 2, 128)
+
+
+@pytest.mark.parametrize("B,P,cap", [(1, 1024, 1024), (1, 1025, 1024), (4, 1024, 200), (4, 1025, 200), (70, 58, 900),
+                                     (70, 0, 1030), (300, 0, 70), (2, 1, 2047), (2, 1, 2048)])
+@pytest.mark.parametrize("H,Hkv,d", [(8, 8, 64), (20, 1, 128)])
+def test_both_sides_of_the_single_launch(q8, B, P, cap, H, Hkv, d):
+    _prefix(q8, B, P, cap, [(i * 131 + cap) % (cap + 1) for i in range(B)], H, Hkv, d, seed=B)
 
 
 @pytest.mark.parametrize("gain", [0.0, 8.0, 40.0])
