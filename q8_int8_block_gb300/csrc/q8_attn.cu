@@ -1321,8 +1321,8 @@ PromptPlan prompt_plan(int64_t B, int64_t Tq, int64_t Tk, int64_t H, int64_t Hkv
   PromptPlan pl;
   // Two tiles a block where that still gives every SM one: K and V are then loaded once for 256
   // rows, and no O is joined (4 prompts of up to 1531 tokens, 16 heads of 64: 26 us, 28.7 with one
-  // tile; 512 tokens behind 8192, whose blocks are too few: 107 us with one tile and the keys in
-  // two splits, 114 with two tiles and four)
+  // tile; 2 x 512 tokens behind 16384 cached ones, which make too few: 107 us with one tile, 114
+  // with two and split keys)
   pl.two = (Tq / (2 * nt) + 1) * Hkv >= dev.sm_count;
   const int64_t n = pl.two ? 2 * nt : nt;
   pl.nslots = Tq / n + B;
