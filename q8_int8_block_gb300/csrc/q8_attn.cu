@@ -24,7 +24,7 @@
 #include <mutex>
 
 #include "q8_internal.h"
-#include "q8_ptx.cuh"
+#include "q8_attn_ptx.cuh"
 
 namespace q8 {
 namespace {
