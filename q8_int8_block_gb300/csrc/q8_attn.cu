@@ -387,11 +387,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     unsigned issued = 0;             // copies under way or done
     Cursor at, last;                 // the next one's place, the last one's
     uint32_t x = blockIdx.x, y = blockIdx.y, asked = 0;
-    if constexpr (!kPrefix) {
-      if (x == 0 && y == 0)  // one warp looks every sequence over
-        for (int64_t s = lane; s < p.a.B; s += 32)
-          if (!sequence_ok(p.a, s)) atomicOr(p.a.err, kErrBadLength);
-    }
     while (true) {
       const int hk = static_cast<int>(x % static_cast<unsigned>(p.a.Hkv)), split = static_cast<int>(y);
       const int slot = static_cast<int>(p.nslots) - 1 - static_cast<int>(x / static_cast<unsigned>(p.a.Hkv));
@@ -632,6 +627,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float* mx_other = reinterpret_cast<float*>(sm + Sh::kOffMax) + (2 * s + (hf ^ 1)) * kRows + r;
     const int rt = r / p.G;
     const float sl2 = p.scale_log2;
+    if constexpr (!kPrefix) {
+      if (blockIdx.x == 0 && blockIdx.y == 0) {  // one block looks every sequence over, while its first loads run
+        bool bad = false;
+#pragma unroll 4
+        for (int64_t i = threadIdx.x; i < p.a.B; i += 32 * kSoftWarps) bad |= !sequence_ok(p.a, i);
+        if (bad) atomicOr(p.a.err, kErrBadLength);
+      }
+    }
     bool ok = true;
     int done = 0, outs = 0;  // blocks of earlier items; earlier items with blocks
     for (int items = 0;; ++items) {

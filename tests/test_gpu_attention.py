@@ -182,6 +182,20 @@ def test_malformed_sequences_are_skipped_and_reported(q8, cq, ck):
     assert q8.q8_device_error() == 0
 
 
+@pytest.mark.parametrize("at", [0, 511, 512, 2999])
+def test_a_malformed_sequence_among_many_is_reported(q8, at):
+    B, d = 3000, 64
+    q = _rand(1, B, 1, d)
+    t = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    ck = t.clone()
+    o = q8.q8_prompt_attention(q, q, q, t, ck)
+    assert q8.q8_device_error() == 0
+    assert torch.equal(o, q)  # one key each: its value
+    ck[at] = ck[at + 1] + 1
+    q8.q8_prompt_attention(q, q, q, t, ck)
+    assert q8.q8_device_error() == 512
+
+
 def test_two_calls_and_two_graphs_at_once(q8):
     """The same shapes on two streams together, then two captured graphs replayed together:
     each call has its own workspace."""
