@@ -58,7 +58,9 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 //  - kTwo: the streams are two tiles behind one another in the sequence that walk the same
 //    blocks of K and V (each is loaded once for 256 rows).
 //  - else: one tile, whose even and odd blocks are the streams; their O are joined at the end.
-// P takes the place of S in TMEM, as the A operand of P V.  Softmax: sixteen warps, eight a
+// P takes the place of S in TMEM, as the A operand of P V; with d = 64 there is room for it beside
+// S, and the stream's next S is computed during the softmax (8192 tokens of 32 heads of 64: 246 us,
+// 259 with P over S).  Softmax: sixteen warps, eight a
 // stream, two for 32 rows, each thread half a row (64 scores in registers, no shuffles); with
 // four warps a stream, a row a thread, 8192 tokens took 480 us instead of 372.  One warp finds the items and
 // loads (TMA, a ring of 5 to 8 K or V blocks that runs over from item to item), one elected
@@ -88,11 +90,14 @@ struct TileShape {
   static constexpr uint32_t kTile = kRows * D * 2;           // a Q tile
   static constexpr uint32_t kStage = kKeys * D * 2;          // a K or V block
   static constexpr uint32_t kHalf = kKeys * 128;             // 64 channels of 128 rows
+  // P beside S in TMEM (128 channels leave no room for it)
+  static constexpr bool kApart = D == 64;
+  static constexpr int kLead = (kTwo ? 1 : 2) + (kApart ? 1 : 0);  // K blocks in front of the first V block
   static constexpr int kStages = D == 128 ? (kTwo ? 5 : 6) : 8;
   static constexpr uint32_t kOffRing = (kTwo ? 2 : 1) * kTile;
   static constexpr uint32_t kOffMax = kOffRing + kStages * kStage;  // float [2 streams][2 halves][rows]
   static constexpr uint32_t kOffBar = kOffMax + 4 * kRows * 4;
-  static constexpr int kBars = 22 + 2 * kStages;
+  static constexpr int kBars = 24 + 2 * kStages;
   static constexpr uint32_t kOffWork = kOffBar + kBars * 8;
   static constexpr uint32_t kSmem = kOffWork + 2 * 64 + 16 + 16;  // two items, the next grid index, TMEM address and flag
   static_assert(kOffWork % 16 == 0, "alignment");
@@ -307,7 +312,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TileParams p) {
   using Sh = TileShape<D, kTwo>;
   constexpr int NS = Sh::kStages;
-  constexpr bool kSteal = !kPrefix;
+  constexpr bool kSteal = !kPrefix, kApart = Sh::kApart;
+  constexpr int kLead = Sh::kLead;
   // the requests' own keys, or the join, may start (one token behind 2000 keys: 16.5 us, 18.5 without)
   if (kPrefix || p.to_parts != 0) pdl_launch_dependents();
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -323,13 +329,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t* tail_done = bars + 2;    // [2] (by item) the last V block's rows behind the keys are zero
   uint64_t* s_full = bars + 4;       // [2] S of a stream computed (and its earlier P V done)
   uint64_t* p_full = bars + 6;       // [2] P written, O rescaled: an arrival of each warp
-  uint64_t* o_full = bars + 8;       // [2] a stream's last P V of an item done
+  uint64_t* o_full = bars + 8;       // [2] a stream's last P V of an item done (kApart: each P V)
   uint64_t* o_empty = bars + 10;     // [2] an item's O has been read
   uint64_t* work_full = bars + 12;   // [2] an item's place written
   uint64_t* work_empty = bars + 14;  // [2] the softmax and MMA warps are done with the item
   uint64_t* next_bar = bars + 16;    // [1] the next grid index
   uint64_t* end_bar = bars + 17;     // [1]
-  uint64_t* full = bars + 18;        // [NS]
+  uint64_t* s_read = bars + 18;      // [2] kApart: S is in the softmax warps' registers
+  uint64_t* full = bars + 20;        // [NS]
   uint64_t* empty = full + NS;       // [NS]
   auto work_at = [&](int w) { return reinterpret_cast<Work*>(sm + Sh::kOffWork + 64 * w); };
   void* next_index = sm + Sh::kOffWork + 128;
@@ -346,6 +353,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], kSoftWarps / 2);
       mbar_init(&o_full[i], 1);
+      mbar_init(&s_read[i], kSoftWarps / 2);
       mbar_init(&o_empty[i], kSoftWarps / 2);
       mbar_init(&work_full[i], 1);
       mbar_init(&work_empty[i], kSoftWarps + 1);
@@ -367,10 +375,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = static_cast<uint32_t>(uniform(static_cast<int>(tmem_slot)));
-  constexpr uint32_t kColO = 256;
+  // columns: S of the streams, then O, then P where it does not take the place of S
+  constexpr uint32_t kColO = 256, kColP = kApart ? kColO + 2 * D : 0, kStepP = kApart ? 64 : kKeys;
+  // where the second 64 keys' P begins: over S behind it, so that half a row's warp overwrites
+  // what it has read itself
+  constexpr uint32_t kHalfP = kApart ? 32 : 64;
   // The ring holds the K and V blocks in the order of their use, item behind item.  Two tiles:
-  // K0 V0 K1 V1 ...; one tile with two streams: K0 K1 V0 K2 V1 K3 V2 ...  Loads and MMAs walk it
-  // with a cursor each.
+  // K0 V0 K1 V1 ...; one tile with two streams: K0 K1 V0 K2 V1 K3 V2 ...; one K block more in front
+  // where the next S does not wait for P V.  Loads and MMAs walk it with a cursor each.
   struct Cursor {
     int st = 0;
     uint32_t ph = 0;
@@ -444,8 +456,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                   tma_load_3d(sm + t * Sh::kTile + c * Sh::kHalf, &tmQ, q_full, 64 * c, hk * p.G, it.tok + t * p.nt);
               ++loaded;
             }
-            constexpr int kLead = kTwo ? 1 : 2;  // S of so many blocks comes before the first P V
-            if (!kTwo && cnt > 1) load(true, 1);
+#pragma unroll
+            for (int j = 1; j < kLead; ++j)
+              if (cnt > j) load(true, j);
             for (int j = 0; j < cnt; ++j) {
               load(false, j);
               if (j + kLead < cnt) load(true, j + kLead);
@@ -535,8 +548,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         auto issue_pv = [&](int s, const Cursor& c, bool first) {  // 16 keys a step: 8 columns of P, 16 rows of V
           const uint64_t b = dV + static_cast<uint64_t>((c.st * Sh::kStage) >> 4);
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)  // the second 64 keys' P begins at column 64
-            mma_f16_ts(tbase + kColO + s * D, tbase + s * kKeys + 8 * k + (k >= 4 ? 32 : 0),
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_f16_ts(tbase + kColO + s * D, tbase + kColP + s * kStepP + 8 * k + (k >= 4 ? kHalfP - 32 : 0),
                        b + static_cast<uint64_t>(k * (2048 >> 4)), idO, k > 0 || !first ? 1u : 0u);
         };
         // P V of the stream's i-th block and, in the same go, S of its next one
@@ -563,16 +576,39 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (left == 0) mma_commit(q_empty);
           }
         };
+        // kApart: S of the stream's block behind the i-th one, once that one's S has been read
+        auto next_s = [&](int s, int i, const Cursor& k, bool release) {
+          landed(k);
+          ok = ok && mbar_poll(&s_read[s], static_cast<uint32_t>((s == 0 ? doneA : doneB) + i) & 1, &abort_flag);
+          if (!ok) return;
+          tc_fence_after();
+          issue_s(s, k);
+          if (release) mma_commit(&empty[k.st]);
+          if (--left == 0) mma_commit(q_empty);
+        };
+        auto pv = [&](int s, int i, const Cursor& v, bool release) {
+          landed(v);
+          ok = ok && mbar_poll(&p_full[s], static_cast<uint32_t>((s == 0 ? doneA : doneB) + i) & 1, &abort_flag);
+          // the item before has to be out of the accumulator
+          if (i == 0 && items > 0) ok = ok && mbar_poll(&o_empty[s], static_cast<uint32_t>(items - 1) & 1, &abort_flag);
+          if (!ok) return;
+          tc_fence_after();
+          issue_pv(s, v, i == 0);
+          mma_commit(&o_full[s]);
+          if (release) mma_commit(&empty[v.st]);
+        };
         ok = mbar_poll(q_full, static_cast<uint32_t>(loaded) & 1, &abort_flag);
         ++loaded;
         const Cursor k0 = at;
         at.step();
         const Cursor k1 = at;
         landed(k0);
-        if (!kTwo && cnt > 1) {
+        if (kLead > 1 && cnt > 1) {
           at.step();
-          landed(k1);
+          if (!kTwo) landed(k1);
         }
+        Cursor kn = kTwo ? k1 : at;  // kApart: the block of K for the next S
+        if (kLead > 2 && cnt > 2) at.step();
         tc_fence_after();
         left -= kTwo ? (nA > 0) + (nB > 0) : (cnt > 1 ? 2 : 1);
         if (ok) {
@@ -598,8 +634,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const Cursor v = at;
           at.step();
           const Cursor k = at;
-          if (j + (kTwo ? 1 : 2) < cnt) at.step();
-          if constexpr (kTwo) {  // the last stream that walks a block releases it
+          if (j + kLead < cnt) at.step();
+          if constexpr (kApart) {
+            constexpr int kStep = kTwo ? 1 : 2;
+            if (ok && j + kStep < cnt) {
+              if constexpr (kTwo) {
+                if (j + 1 < nA) next_s(0, j, kn, j + 1 >= nB);
+                if (ok && j + 1 < nB) next_s(1, j, kn, true);
+              } else {
+                next_s(j & 1, j >> 1, kn, true);
+              }
+              kn = k;
+            }
+            if constexpr (kTwo) {
+              if (ok && j < nA) pv(0, j, v, j >= nB);
+              if (ok && j < nB) pv(1, j, v, true);
+            } else {
+              if (ok) pv(j & 1, j >> 1, v, true);
+            }
+          } else if constexpr (kTwo) {  // the last stream that walks a block releases it
             if (ok && j < nA) turn(0, j, v, k, j + 1 < nA, j >= nB, j + 1 >= nB);
             if (ok && j < nB) turn(1, j, v, k, j + 1 < nB, true, true);
           } else {
@@ -621,7 +674,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int s = warp >> 3, qd = warp & 3, hf = (warp >> 2) & 1;
     const int r = 32 * qd + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(32 * qd) << 16);
-    const uint32_t tS = tl + s * kKeys + 64 * hf, tO = tl + kColO + s * D + (D / 2) * hf;
+    const uint32_t tS = tl + s * kKeys + 64 * hf, tP = tl + kColP + s * kStepP + kHalfP * hf, tO = tl + kColO + s * D + (D / 2) * hf;
     const int pair_bar = 1 + 4 * s + qd;  // named barrier of the two warps of these rows
     float* mx_own = reinterpret_cast<float*>(sm + Sh::kOffMax) + (2 * s + hf) * kRows + r;
     float* mx_other = reinterpret_cast<float*>(sm + Sh::kOffMax) + (2 * s + (hf ^ 1)) * kRows + r;
@@ -669,6 +722,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32(tS + 32 * c, x[c]);
         tmem_ld_wait();
+        if constexpr (kApart) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_read[s]);
+        }
         if ((j + 1) * kKeys > whole) {
           const int rem = lim - j * kKeys - 64 * hf;
 #pragma unroll
@@ -687,8 +745,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float mine = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         // Nearly always the reference of the earlier blocks serves: no row of either half is more
         // than 2^8 above it.  Only where one is do the halves exchange their maxima.  (The next
-        // block's may overwrite them: its S is there only after both warps have handed over this
-        // block's P, and so have read these.)
+        // block's may overwrite them: both warps have met at its barrier then, and so have read these.)
         float alpha = 1.0f;
         const bool any = wg_barrier_any<64>(pair_bar, mine * sl2 > ref + kRescaleLog2);
         if (any) {
@@ -703,9 +760,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float base = ref == -INFINITY ? 0.0f : ref;  // no key seen so far: every weight is 2^-inf = 0
         const float2 sc2 = make_float2(sl2, sl2), nb2 = make_float2(-base, -base);
         float2 sum2 = make_float2(0.0f, 0.0f);
+        uint32_t pk2[kApart ? 2 : 1][16];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
+          uint32_t (&pk)[16] = pk2[kApart ? c : 0];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float2 t = __ffma2_rn(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sc2, nb2);
@@ -714,7 +772,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             sum2 = __fadd2_rn(sum2, t);
             pk[e] = pack_bf16(t.x, t.y);
           }
-          tmem_st_32x32b_x16(tS + 16 * c, pk);
+          if (!kApart) tmem_st_32x32b_x16(tP + 16 * c, pk);
+        }
+        if constexpr (kApart) {  // the P V before has read its P, and O holds it
+          if (i > 0) {
+            ok = ok && warp_wait(&o_full[s], static_cast<uint32_t>(done + i - 1) & 1, &abort_flag);
+            tc_fence_after();
+          }
+          tmem_st_32x32b_x16(tP, pk2[0]);
+          tmem_st_32x32b_x16(tP + 16, pk2[kApart ? 1 : 0]);
         }
         l = fmaf(l, alpha, sum2.x + sum2.y);
         if (any && i > 0) {
@@ -737,7 +803,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       done += n;
       if (ok && n > 0) {  // the stream's products are done
-        ok = warp_wait(&o_full[s], static_cast<uint32_t>(outs) & 1, &abort_flag);
+        ok = warp_wait(&o_full[s], static_cast<uint32_t>(kApart ? done - 1 : outs) & 1, &abort_flag);
         tc_fence_after();
       }
       outs += n > 0 ? 1 : 0;
