@@ -371,10 +371,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tbase = static_cast<uint32_t>(uniform(static_cast<int>(tmem_slot)));
+  if (warp == kSoftWarps) {  // made the barriers, and needs nothing of the others: its loads may start
+    __syncwarp();
+    asm volatile("bar.arrive 0, %0;" ::"n"(kTileThreads) : "memory");
+  } else {
+    tc_fence_before();
+    asm volatile("bar.sync 0, %0;" ::"n"(kTileThreads) : "memory");
+    tc_fence_after();
+  }
+  const uint32_t tbase = warp == kSoftWarps ? 0u : static_cast<uint32_t>(uniform(static_cast<int>(tmem_slot)));
   // columns: S of the streams, then O, then P where it does not take the place of S
   constexpr uint32_t kColO = 256, kColP = kApart ? kColO + 2 * D : 0, kStepP = kApart ? 64 : kKeys;
   // where the second 64 keys' P begins: over S behind it, so that half a row's warp overwrites
