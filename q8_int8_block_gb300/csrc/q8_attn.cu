@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   constexpr int NS = Sh::kStages;
   constexpr bool kSteal = !kPrefix, kApart = Sh::kApart;
   constexpr int kLead = Sh::kLead;
-  // the requests' own keys, or the join, may start (one token behind 2000 keys: 16.5 us, 18.5 without)
+  // the requests' own keys, or the join, may start (2 us of one token behind 2000 keys)
   if (kPrefix || p.to_parts != 0) pdl_launch_dependents();
   extern __shared__ __align__(1024) uint8_t sm[];
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = static_cast<int>(threadIdx.x & 31);
@@ -970,9 +970,9 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
   const int nb = tile_blocks<false>(it, it.tok, p.nt);
   const int per = blocks_per_split(nb, p.splits), used = per > 0 ? (nb + per - 1) / per : 0;
   const int64_t rows = p.a.Tq * p.a.H;
-  for (int r = blockIdx.y * 8 + warp; r < p.nt * p.G; r += 8 * gridDim.y) {
-    const int64_t tok = it.tok + r / p.G;
-    if (tok >= it.tok_end) break;
+  const int r = static_cast<int>(blockIdx.y) * 8 + warp;
+  const int64_t tok = it.tok + r / p.G;
+  if (r < p.nt * p.G && tok < it.tok_end) {
     const int64_t head = hk * p.G + r % p.G, row = tok * p.a.H + head;
     float l, acc[E];
     join_parts<D>(used, 0, 1, lane, p.part_ml, p.part_o, [&](int s) { return s * rows + row; }, l, acc);
@@ -1401,10 +1401,12 @@ PromptPlan prompt_plan(int64_t B, int64_t Tq, int64_t Tk, int64_t H, int64_t Hkv
   const int64_t n = pl.two ? 2 * nt : nt;
   pl.nslots = Tq / n + B;
   // Keys are split where the blocks in work leave SMs without any (a sequence counts as one block at
-  // least: 64 single tokens of 2048 keys take 86 us so, 114 in two splits), eight key blocks a
-  // split at least: with four, 128 tokens behind 1000 take 17 us instead of 14.5
+  // least: 64 single tokens of 2048 keys take 86 us so, 114 in two splits): four key blocks a split
+  // at least (one token behind 2000 keys: 11.9 us, 14.2 with eight), sixteen splits at most (behind
+  // 16384: 18.0, 19.5 with nineteen), and none of so few keys that two would do (128 tokens behind
+  // 1000: 11.8 us, 13.7 in two)
   const int64_t busy = (Tq / n + std::min(B, Tq)) * Hkv, blocks = (Tk + kKeys - 1) / kKeys;
-  pl.splits = static_cast<int>(std::max<int64_t>(1, std::min(dev.sm_count / busy, blocks / 8)));
+  pl.splits = blocks < 12 ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({dev.sm_count / busy, 16, blocks / 4})));
   return pl;
 }
 
@@ -1423,7 +1425,8 @@ cudaError_t prompt_attention(const PromptArgs& a, const DeviceInfo& dev, cudaStr
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<int64_t>(pl.splits) * a.Tq * a.H * D);
   cudaError_t e = pl.two ? launch_tiles<D, true, false>(p, dev, stream) : launch_tiles<D, false, false>(p, dev, stream);
   if (e != cudaSuccess || pl.splits == 1) return e;
-  const dim3 grid(static_cast<unsigned>(pl.nslots * a.Hkv), 4);
+  // a warp a row (128 tokens behind 16384: 40.1 us, 45.4 with four rows a warp)
+  const dim3 grid(static_cast<unsigned>(pl.nslots * a.Hkv), kRows / 8);
   return launch_with(prompt_join_kernel<D>, grid, 256, 0, true, 1, stream, p);
 }
 
@@ -1445,15 +1448,18 @@ PrefixPlan prefix_plan(int64_t B, int64_t P, int64_t cap, int64_t H, int64_t Hkv
   pl.nslots = (B + n - 1) / n;
   pl.chunks = static_cast<int>((G + kOwnRows - 1) / kOwnRows);
   const int64_t busy = B * Hkv * pl.chunks;
-  // Alone: few shared keys are read again for every request, which costs less than a second
-  // and a third launch, where no request has so many keys that its few blocks end last (device
-  // time, 1 request behind 1000 keys: 10.5 us against 13.6 with three launches; 64 requests
-  // with up to 2000 keys: 44 us alone; 16 behind 1000: 18 against 13.7)
-  pl.alone = B * P <= 4096 && P + cap <= (busy > 3 * dev.sm_count ? 1024 : 2048);
+  // Alone: few shared keys are read again for every request, which costs less than a second and a
+  // third launch where a block has few keys (device time: 1 request behind 1000 keys 8.0 us, 9.6 with
+  // three launches; 16 with up to 100 own ones behind 256: 8.7 against 9.6).  Not where the cluster's
+  // blocks or the SMs are too few for that (8 requests with up to 2000 keys: 13.1 us alone, 10.3 with
+  // more blocks and a join), and with one block a row while it ends soon (256 requests with up to 300
+  // keys: 25.3 us against 28.2; 64 with up to 512: 16.5 against 12.9)
+  const int64_t keys = P + cap;
+  const int64_t one = std::max<int64_t>(1, std::min<int64_t>({8, 3 * dev.sm_count / busy, (keys + 127) / 128}));
+  pl.alone = B * P <= 4096 && keys <= one * (one > 1 ? 160 : 384);
   if (pl.alone) {
     pl.prefix_splits = 0;
-    const int64_t s = std::min(3 * dev.sm_count / busy, (P + cap + 127) / 128);
-    pl.own_splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, s)));
+    pl.own_splits = static_cast<int>(one);
     return pl;
   }
   const int64_t s = std::max<int64_t>(1, std::min(dev.sm_count / (pl.nslots * Hkv), blocks / 2));

@@ -406,7 +406,7 @@ def test_long_prefix_and_large_batches(q8):
     _prefix(q8, 1, 60, 30011, [30011], 8, 2, 128)
 
 
-@pytest.mark.parametrize("B,P,cap", [(1, 1024, 1024), (1, 1025, 1024), (4, 1024, 200), (4, 1025, 200), (70, 58, 900),
+@pytest.mark.parametrize("B,P,cap", [(1, 640, 640), (1, 641, 640), (1, 1024, 1024), (4, 1024, 200), (4, 1025, 200), (70, 58, 900), (64, 64, 320), (64, 64, 321),
                                      (70, 0, 1030), (300, 0, 70), (2, 1, 2047), (2, 1, 2048)])
 @pytest.mark.parametrize("H,Hkv,d", [(8, 8, 64), (20, 1, 128)])
 def test_both_sides_of_the_single_launch(q8, B, P, cap, H, Hkv, d):
