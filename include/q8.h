@@ -227,7 +227,8 @@ q8_status q8_bsa_attention(const uint16_t* q, const uint16_t* k, const uint16_t*
  * contiguous, every stride is a multiple of 16 bytes and not negative (else Q8_ERR_ALIGN,
  * Q8_ERR_SHAPE).  A stride of 0 repeats an input: the tokens of q8_qk_norm_rope, the heads of
  * k and v, the requests of the own caches; elsewhere, and between rows of an output that would
- * overlap, it is refused (Q8_ERR_SHAPE).
+ * overlap, it is refused (Q8_ERR_SHAPE).  So are strides from 2^38 elements on, and counts of
+ * tokens, or of tokens and sequences times heads, above 2^31 - 1025.
  *
  * q8_qk_norm_rope -- RMSNorm of every query and key head and the rotation of its first rot
  * channels by the token's position, in one pass.
