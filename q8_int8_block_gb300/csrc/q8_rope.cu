@@ -15,7 +15,8 @@
 //    cosines once, in shared memory, while the first heads are on their way from memory; the
 //    teams then walk the heads.  Small blocks of 64 registers, eight on an SM, hide both phases
 //    of one another: 8192 tokens of 40 heads of 128 from binary32 take 47 us (5.3 TB/s, 0.79 of
-//    the measured copy rate), 62 us with blocks of 256 threads that loaded further ahead.
+//    the measured copy rate), 62 us with blocks of 256 threads that loaded further ahead, 49 and 51
+//    with six and ten blocks an SM.
 //  - Angles: the fraction of a turn that one position advances is formed as a 64-bit
 //    fixed-point number; position * step modulo 2^64 is then the exact fraction of a turn at
 //    any position, and only its top 32 bits become binary32.  Binary64 arithmetic would cost

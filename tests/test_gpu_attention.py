@@ -580,3 +580,51 @@ def test_a_layer_from_prompt_to_next_tokens(q8):
     (_, tq), (ck, tk) = _cum([1, 1]), _cum([191, 176])
     R.assert_within(q8.q8_prompt_attention(q1, ks, vs, tq, tk), *R.prompt(q1, ks, vs, [0, 1, 2], ck), "as prompts")
     assert q8.q8_device_error() == 0
+
+
+def test_a_decode_step_captured_once(q8):
+    """Rotation in place, the new key into the cache, attention behind the prefix: one graph,
+    replayed for the next tokens with positions and lengths advanced on the device."""
+    B, P, cap, H, Hkv, d = 5, 300, 40, 8, 2, 128
+    kp, vp = _rand(1, P, Hkv, d), _rand(2, P, Hkv, d)
+    ko, vo = (torch.full((B, cap, Hkv, d), NAN, dtype=BF16, device="cuda") for _ in range(2))
+    inv = 1e6 ** (-torch.arange(0, d, 2, device="cuda", dtype=torch.float64) / d)
+    x = torch.empty(B, H + 2 * Hkv, d, dtype=BF16, device="cuda")  # the projection's rows
+    q, k, v = x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:]
+    ln = torch.tensor([0, 3, 1, 0, 7], dtype=torch.int32, device="cuda")
+    for c, s in ((ko, 3), (vo, 4)):
+        for b, n in enumerate(ln.tolist()):
+            c[b, :n] = _rand(s + 10 * b, n, Hkv, d)
+    rows = torch.arange(B, device="cuda")
+
+    def step():
+        q8.q8_qk_norm_rope(q, k, ln + P, inv, q_out=q, k_out=k)
+        at = ln.long()
+        ko[rows, at] = k
+        vo[rows, at] = v
+        ln.add_(1)
+        return q8.q8_prefix_attention(q, kp, vp, ko, vo, ln)
+
+    saved = [t.clone() for t in (ko, vo, ln)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        x.copy_(_rand(50, *x.shape))
+        step()
+    torch.cuda.synchronize()
+    for t, s in zip((ko, vo, ln), saved):
+        t.copy_(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o = step()
+    for i in range(6):
+        new = _rand(60 + i, *x.shape)
+        x.copy_(new)
+        before = ln.tolist()
+        g.replay()
+        torch.cuda.synchronize()
+        assert ln.tolist() == [n + 1 for n in before]
+        pos = torch.tensor(before, device="cuda", dtype=torch.int32) + P
+        R.assert_within(q, *R.norm_rope(new[:, :H], pos, inv, None, 1e-6, False), "rotated")
+        R.assert_within(o, *R.prefix(q, kp, vp, ko, vo, ln.tolist()), f"step {i}")
+    assert q8.q8_device_error() == 0

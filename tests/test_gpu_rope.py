@@ -185,3 +185,23 @@ def test_refusals(q8):
     x = torch.empty(4, 4 * 64 + 4, dtype=BF16, device="cuda")
     with pytest.raises(q8.Q8Error, match="Q8_ERR_ALIGN"):
         q8.q8_qk_norm_rope(x[:, 4:].view(4, 4, 64), k, pos, inv)
+
+
+def test_captured_and_replayed_and_on_another_stream(q8):
+    q, k, pos, (qw, kw) = _inputs(9, 6, 2, 128, BF16)
+    inv = _freq(128)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    qo, ko = q8.q8_qk_norm_rope(q, k, pos, inv, q_weight=qw, k_weight=kw, stream=side)
+    side.synchronize()
+    _check(qo, q, pos, inv, qw, what="q")
+    _check(ko, k, pos, inv, kw, what="k")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        go = q8.q8_qk_norm_rope(q, k, pos, inv, q_weight=qw, k_weight=kw)
+    for far in (0, 5, 123456):
+        pos.copy_(torch.arange(9, dtype=torch.int32) + far)
+        g.replay()
+        torch.cuda.synchronize()
+        _check(go[0], q, pos, inv, qw, what=f"q {far}")
+        _check(go[1], k, pos, inv, kw, what=f"k {far}")
