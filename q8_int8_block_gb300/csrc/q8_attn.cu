@@ -78,6 +78,11 @@ constexpr int kRows = 128;     // query rows of a tile: 128 / G tokens x G heads
 constexpr int kKeys = 128;     // keys of a block
 constexpr int kSoftWarps = 16;  // softmax: 8 warps a stream, two (a half of the keys each) for 32 rows
 constexpr int kTileThreads = 32 * (kSoftWarps + 2);  // and one warp for the loads, one for the MMAs
+// Barrier 0 is the one at the kernel's end.  The softmax warps use 1 to 8 (two warps of 32 rows)
+// and 9, 10 (a stream).  The start has a number of its own: the load warp only arrives there, and
+// a barrier counts arrivals, not warps, so its arrival at the end must not be able to stand in
+// for a warp that is still on its way to the start.
+constexpr int kStartBar = 11;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -374,10 +379,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   if (warp == kSoftWarps) {  // made the barriers, and needs nothing of the others: its loads may start
     __syncwarp();
-    asm volatile("bar.arrive 0, %0;" ::"n"(kTileThreads) : "memory");
+    asm volatile("bar.arrive %0, %1;" ::"n"(kStartBar), "n"(kTileThreads) : "memory");
   } else {
     tc_fence_before();
-    asm volatile("bar.sync 0, %0;" ::"n"(kTileThreads) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"n"(kStartBar), "n"(kTileThreads) : "memory");
     tc_fence_after();
   }
   const uint32_t tbase = warp == kSoftWarps ? 0u : static_cast<uint32_t>(uniform(static_cast<int>(tmem_slot)));
