@@ -1460,8 +1460,12 @@ struct PrefixPlan {
 PrefixPlan prefix_plan(int64_t B, int64_t P, int64_t cap, int64_t H, int64_t Hkv, const DeviceInfo& dev) {
   const int64_t G = H / Hkv, nt = kRows / G;
   PrefixPlan pl;
-  // Two tiles a block only where one already fills the GPU twice: with one, half as many partial
-  // results are written (64 requests behind 8192 keys: 31 us a call against 33)
+  // Two tiles a block only where one already fills the GPU twice: fewer blocks would have to split
+  // the keys, and each split writes partial results (64 requests behind 8192 keys: 31 us a call
+  // with one tile, 33 with two).  Beyond that K and V are loaded half as often (device time with two
+  // tiles and one, 32/8 heads of 128: 1216 requests behind 1000 keys 111 and 117 us, 2432 behind
+  // 8192 333 and 351; the other way round by 2 to 3 % for 2432 requests of 64-wide heads behind 8192,
+  // 282 and 278, and 1000 of 40 heads behind 4000, 314 and 304)
   pl.two = (B + nt - 1) / nt * Hkv >= 2 * dev.sm_count;
   const int64_t n = pl.two ? 2 * nt : nt, blocks = (P + kKeys - 1) / kKeys;
   pl.nslots = (B + n - 1) / n;
