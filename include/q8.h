@@ -266,7 +266,10 @@ q8_status q8_qk_norm_rope(const void* q, const void* k, q8_dtype xtype, int64_t 
  *     keys its query i sees its keys j <= i + lk - lq: the queries are the last lq tokens of
  *     the context (lk > lq: the earlier keys were cached before).  A query that sees no key
  *     gets 0.  Rows of o outside every sequence are left as they are, and nothing outside a
- *     sequence's own keys reaches its outputs.  A sequence that is not inside [0, Tq] x
+ *     sequence's own keys reaches its outputs.  Inside a sequence v has to be finite: masked
+ *     keys take part in the products with a weight of 0, so a NaN or an infinity in a row of v
+ *     may make NaN of queries up to 255 tokens in front of those that see it (not of queries
+ *     that see no key).  A sequence that is not inside [0, Tq] x
  *     [0, Tk] or has a negative length is skipped and sets bit 9 of the device error word (the
  *     ones beside it are then found only where cu_q still rises);
  *   o = sum_j p_j v_j / sum_j p_j, p_j = exp(scale * (q . k_j) - max); scale finite and > 0

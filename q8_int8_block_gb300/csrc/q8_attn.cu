@@ -844,7 +844,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool valid = rt < p.nt && tok < o->tok_end;
         const int head = o->hk * p.G + (r - rt * p.G);
         const bool final_out = p.to_parts == 0;
-        const float over = final_out ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
+        const bool saw = l > 0.0f || l != l;
+        // A row without a key is 0, whatever is in the V that its tile's other rows see (its
+        // accumulator has 0 V, NaN where V is not finite); looked at a warp at a time
+        const bool all_saw = __all_sync(0xFFFFFFFFu, saw);
+        const float over = final_out && saw ? 1.0f / l : 1.0f;
         const float inv = scale * over, inv_other = other_scale * over;
         const int64_t row = static_cast<int64_t>(o->split) * p.a.Tq * p.a.H + static_cast<int64_t>(tok) * p.a.H + head;
         if (!final_out && valid && cnt > 0 && hf == 0) p.part_ml[row] = make_float2(ref, l);
@@ -881,6 +885,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(t[e]), inv_other, f[e]);
+          }
+          if (!all_saw) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = saw ? f[e] : 0.0f;
           }
         };
         if (final_out) {

@@ -80,3 +80,26 @@ def test_repeated_caches(q8, P, cap, d):
         R.assert_within(o, *R.prefix(q, *a, lens), what)
         assert torch.equal(o, q8.q8_prefix_attention(q, *(x.contiguous() for x in a), ln)), what
     assert q8.q8_device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("many,nq,nk,at", [
+    (False, 4, 1, 0), (False, 300, 200, 0), (False, 100, 90, 40), (False, 1600, 1540, 3), (False, 1600, 1540, 1539),
+    (True, 4, 1, 0), (True, 300, 200, 0), (True, 200, 60, 59), (True, 255, 127, 0)])
+def test_a_query_without_a_key_is_zero_whatever_the_values_are(q8, many, nq, nk, at, value, d):
+    """A row of v that is not finite reaches the queries that see it, not the ones that see no
+    key (1600 queries, 1540 keys: these are split and joined)."""
+    H, Hkv = _heads(many) if nk < 1000 else (1, 1)
+    q, k, v = _rand(1, nq, H, d), _rand(2, nk, Hkv, d), _rand(3, nk, Hkv, d)
+    v[at] = value
+    o = torch.full_like(q, 3.0)
+    q8.q8_prompt_attention(q, k, v, _int([0, nq]), _int([0, nk]), o=o)
+    assert (o[:nq - nk] == 0).all()
+    assert not o[nq - nk + at:].isfinite().any()
+    # far enough in front of the row it reaches nothing
+    clean = max(nq - nk, nq - nk + at - 255)
+    v[at] = 0.0
+    want = q8.q8_prompt_attention(q, k, v, _int([0, nq]), _int([0, nk]))
+    assert torch.equal(o[:clean], want[:clean])
+    assert q8.q8_device_error() == 0
