@@ -239,7 +239,8 @@ q8_status q8_bsa_attention(const uint16_t* q, const uint16_t* k, const uint16_t*
  *     (else Q8_ERR_VALUE);
  *   positions [T] int32, inv_freq [rot / 2] double: pair i of a head turns by the angle
  *     positions[t] * inv_freq[i] (any scaling of the frequencies is the caller's), kept exact
- *     to 2^-32 turns for |position| < 2^31 and frequencies up to 1;  pair (a, b) becomes
+ *     to 2^-32 turns for |position| < 2^31 and frequencies up to 1;  a frequency of 2^32 or
+ *     more in magnitude, or one that is not finite, makes NaN of its pairs;  pair (a, b) becomes
  *     (a cos - b sin, a sin + b cos).  interleaved 0: pair i is channels (i, i + rot / 2);
  *     1: channels (2 i, 2 i + 1);
  *   q_out, k_out: bfloat16 bits, rounded once (to nearest even), tokens q_out_stride and

@@ -50,14 +50,16 @@ struct RopeParams {
 
 // inv_freq / (2 pi) as a fraction of a turn in units of 2^-64, modulo whole turns, from the
 // bits of the binary64 value m 2^e: m 2^11 times the leading 64 bits of 2 / pi, shifted.
-__device__ __forceinline__ uint64_t turn_step(double f) {
+// Of frequencies from 2^32 on, infinities and NaN the 64 bits say too little: *ok is false.
+__device__ __forceinline__ uint64_t turn_step(double f, bool* ok) {
   const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
   const int ex = static_cast<int>((bits >> 52) & 0x7FF);
+  *ok = ex < 1023 + 32;
   if (ex == 0) return 0;  // zero; a subnormal frequency turns by less than 2^-64
   const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull;
   const uint64_t x = __umul64hi(m << 11, 0xA2F9836E4E441529ull);  // floor(m (2 / pi) 2^11)
   const int sh = ex - 1075 + 51;  // f / (2 pi) 2^64 = x 2^(ex - 1075 + 51)
-  const uint64_t s = sh <= -64 ? 0 : sh < 0 ? x >> -sh : sh < 64 ? x << sh : 0;
+  const uint64_t s = sh <= -64 ? 0 : sh < 0 ? x >> -sh : x << (sh & 63);
   return (bits >> 63) != 0 ? 0 - s : s;
 }
 
@@ -141,8 +143,11 @@ __global__ void __launch_bounds__(kThreads, 8) qk_norm_rope_kernel(const RopePar
     const int tok = i / half, f = i - tok * half;
     if (t0 + tok < p.T) {
       const int64_t pos = p.positions[t0 + tok];
-      const int32_t frac = static_cast<int32_t>((static_cast<uint64_t>(pos) * turn_step(p.inv_freq[f])) >> 32);
-      sincospif(static_cast<float>(frac) * 4.656612873077392578125e-10f, &sin_s[i], &cos_s[i]);  // 2^-31
+      bool ok;
+      const uint64_t step = turn_step(p.inv_freq[f], &ok);
+      const int32_t frac = static_cast<int32_t>((static_cast<uint64_t>(pos) * step) >> 32);
+      const float half_turns = ok ? static_cast<float>(frac) * 4.656612873077392578125e-10f : NAN;  // 2^-31
+      sincospif(half_turns, &sin_s[i], &cos_s[i]);
     }
   }
   for (int i = threadIdx.x; i < 2 * p.d; i += kThreads) {
