@@ -236,11 +236,13 @@ q8_status q8_bsa_attention(const uint16_t* q, const uint16_t* k, const uint16_t*
  *     (views of a fused projection's rows are fine), heads d elements apart;
  *   q_weight, k_weight [d] float: z = x * r * weight, r = 1 / sqrt(mean_d x^2 + eps); NULL:
  *     those heads are not normalised (z = x); eps finite and > 0 where a weight is given
- *     (else Q8_ERR_VALUE);
+ *     (else Q8_ERR_VALUE); the sum of a normalised head's squares has to stay within binary32
+ *     (|x| below ~1e18);
  *   positions [T] int32, inv_freq [rot / 2] double: pair i of a head turns by the angle
- *     positions[t] * inv_freq[i] (any scaling of the frequencies is the caller's), kept exact
- *     to 2^-32 turns for |position| < 2^31 and frequencies up to 1;  a frequency of 2^32 or
- *     more in magnitude, or one that is not finite, makes NaN of its pairs;  pair (a, b) becomes
+ *     positions[t] * inv_freq[i] (any scaling of the frequencies is the caller's), kept to
+ *     2^-25 turns at every position and frequencies up to 1 in magnitude, above to
+ *     |position * frequency| 2^-63 turns beside that;  a frequency of 2^32 or more in
+ *     magnitude, or one that is not finite, makes NaN of its pairs;  pair (a, b) becomes
  *     (a cos - b sin, a sin + b cos).  interleaved 0: pair i is channels (i, i + rot / 2);
  *     1: channels (2 i, 2 i + 1);
  *   q_out, k_out: bfloat16 bits, rounded once (to nearest even), tokens q_out_stride and

@@ -18,9 +18,10 @@
 //    the measured copy rate), 62 us with blocks of 256 threads that loaded further ahead, 49 and 51
 //    with six and ten blocks an SM.
 //  - Angles: the fraction of a turn that one position advances is formed as a 64-bit
-//    fixed-point number; position * step modulo 2^64 is then the exact fraction of a turn at
-//    any position, and only its top 32 bits become binary32.  Binary64 arithmetic would cost
-//    more than the memory traffic on this GPU.
+//    fixed-point number; position * step modulo 2^64 is then the fraction of a turn at any
+//    position (to 2^-31 turns for frequencies up to 1), and its top 32 bits become binary32,
+//    which rounds off up to 2^-26 turns, about what sine and cosine are rounded to.  Binary64
+//    arithmetic would cost more than the memory traffic on this GPU.
 #include <cuda_bf16.h>
 
 #include <algorithm>
