@@ -351,8 +351,10 @@ q8_status q8_block_sums(const int8_t* xq, const int8_t* Wq, int32_t* isum, int64
 /*
  * q8_device_error -- synchronizes the current device, then returns (and clears) the
  * library's device error word: bit 0 = a bounded device-side wait gave up (the results
- * of that call are undefined), bit 1 = a kernel met launch parameters it cannot handle.
- * 0 means no error.  Returns Q8_ERR_CUDA through *status if the sync itself failed.
+ * of that call are undefined), bit 1 = a kernel met launch parameters it cannot handle,
+ * bit 8 = q8_bsa_attention skipped a listed key block, bit 9 = q8_prompt_attention skipped a
+ * malformed sequence or q8_prefix_attention clamped a cache length (the rest of these calls'
+ * results stands).  0 means no error.  Returns Q8_ERR_CUDA through *status if the sync itself failed.
  */
 uint32_t q8_device_error(q8_status* status);
 
