@@ -353,8 +353,8 @@ q8_status q8_block_sums(const int8_t* xq, const int8_t* Wq, int32_t* isum, int64
  * library's device error word: bit 0 = a bounded device-side wait gave up (the results
  * of that call are undefined), bit 1 = a kernel met launch parameters it cannot handle,
  * bit 8 = q8_bsa_attention skipped a listed key block, bit 9 = q8_prompt_attention skipped a
- * malformed sequence or q8_prefix_attention clamped a cache length (the rest of these calls'
- * results stands).  0 means no error.  Returns Q8_ERR_CUDA through *status if the sync itself failed.
+ * malformed sequence or q8_prefix_attention clamped a cache length (each says what becomes of
+ * the rest).  0 means no error.  Returns Q8_ERR_CUDA through *status if the sync itself failed.
  */
 uint32_t q8_device_error(q8_status* status);
 

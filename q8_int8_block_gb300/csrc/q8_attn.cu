@@ -3,7 +3,7 @@
 // The attention layers of the hybrid models that "CUDA inference engine for running
 // Qwen3.5/3.6 hybrid models on mining cards (CMP 100-210)" (news.hada.io topic 29953) runs:
 // o = softmax(scale q . k) v over the keys a query sees, H query heads over Hkv key/value
-// heads.
+// heads of 64 or 128 channels (two S and two O of 256 would not fit the 512 columns of TMEM).
 //
 // Both entry points walk the keys once with a running reference m and sum l per row (online
 // softmax; Milakov and Gimelshein, 2018): for a block of scores s, w = 2^(s' - m) with
@@ -11,7 +11,10 @@
 // O are first scaled by 2^(m - m').  Parts of a row that different blocks walked are joined by
 // o = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p, M = max m_p, in a fixed order.
 // Scores, m, l and O are binary32; w is rounded to bfloat16 for the product with V only (l sums
-// the unrounded weights), o once at the end.
+// the unrounded weights), o once at the end.  The MMAs take A and B of one type, and V is
+// bfloat16: w in more bits would be a second product for its rest, half as many tensor cycles
+// again.  It moves o by less than its own rounding does (with both, 1.2 to 1.5 times the error
+// of the rounded o alone over the measured cases).
 //
 //  attn_tile_kernel    whole prompts, and a batch's queries over its shared prefix: tensor work
 //  attn_own_kernel     a request's own keys, which no other reads: the bytes of its cache
@@ -52,8 +55,8 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // a causal tile of few tokens wastes little of its diagonal block.
 //
 // Bound: the tensor pipe.  A block of 128 keys takes d / 16 + 8 MMAs of 64 cycles (S = Q K^T, and
-// O += P V): 1024 cycles at d = 128.  Its softmax takes about 1500 from the S committed to the
-// P handed over, so one stream of blocks would leave the pipe idle most of the time.  Hence
+// O += P V): 1024 cycles at d = 128.  Its softmax takes about 1100, 1500 from the S committed to
+// the P handed over, so one stream of blocks would leave the pipe idle most of the time.  Hence
 // two streams, A and B, each with its S (128 columns of TMEM) and O (d columns): while one is in its
 // softmax the pipe works on the other.
 //  - kTwo: the streams are two tiles behind one another in the sequence that walk the same
@@ -71,9 +74,10 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // The blocks are persistent: the next item (tile, head, split) is asked for while the current
 // one is in work, the last ones of a sequence, which see the most keys, first.
 //
-// 32 query heads, 8 key/value heads of 128: 8192 tokens in 345 us (1.59 PFLOP/s counted over the
-// causal half, 0.84 of the measured dense rate), 16384 tokens at 1.85 PFLOP/s.  What is left
-// there is the clock under load, and the ends: the first S and the last O of a block's items.
+// 32 query heads, 8 key/value heads of 128: 8192 tokens in 344 us (1.60 PFLOP/s counted over the
+// causal half, 0.84 of the measured dense rate; 1762 MHz under the power cap), 16384 tokens in
+// 1320 (1.67 PFLOP/s, 1717 MHz).  What is left there is the clock under load, and the ends: the
+// first S and the last O of a block's items.
 constexpr int kRows = 128;     // query rows of a tile: 128 / G tokens x G heads
 constexpr int kKeys = 128;     // keys of a block
 constexpr int kSoftWarps = 16;  // softmax: 8 warps a stream, two (a half of the keys each) for 32 rows
@@ -1005,8 +1009,10 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
 // three CTAs on an SM keep 192 KB in flight.  The products run on mma.sync: 16 rows are all
 // there is, and the tensor pipe is not what bounds this.  Rows behind the request's keys are
 // not read (zeros are filled in).
-// Long caches are read at 0.94 to 1.0 of the copy rate; with two warps a block and six blocks an SM, 64
-// requests with up to 512 keys took 24.6 us instead of 16.2.
+// Long caches are read at the copy rate (32/8 heads of 128: 64 requests with 4096 keys 161
+// us, 6.7 TB/s; 8 with 65536 309 us, 6.9 TB/s), short ones below it (64 with 512: 28 us, 4.8
+// TB/s); with two warps a block and six blocks an SM, 64 requests with up to 512 keys took 24.6 us
+// instead of 16.2.
 // kAlone: no other kernel works on this call.  The prefix, short or of one request only, is
 // walked here in front of the own keys, and the CTAs that share a row's keys are a cluster
 // that joins them through its shared memory: one launch and no workspace.
