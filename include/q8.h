@@ -314,6 +314,97 @@ size_t q8_prefix_attention_workspace_size(int64_t B, int64_t P, int64_t cap, int
                                           int64_t Hkv, int64_t d);
 
 /*
+ * A paged cache of keys and values in 4 bits, for serving.  The post keeps long contexts in a
+ * compressed cache ("CUDA inference engine for running Qwen3.5/3.6 hybrid models on mining cards
+ * (CMP 100-210)", news.hada.io topic 29953, feature list); this one is written by
+ * q8_kv4_append, read by q8_kv4_attention (the newest tokens of each request) and by
+ * q8_kv4_gather (keys and values back, as for q8_prompt_attention).
+ *
+ * cache [pages][Hkv][page / 32][36 d] bytes: page p is at cache + p * page_stride (bytes, a
+ *   multiple of 16, at least the page's own Hkv * page / 32 * 36 d), tokens of a page in tiles of
+ *   32, a tile 36 d bytes: 4.5 bits an element, codes of 4 bits and a bfloat16 scale for 32
+ *   channels of a token.  The order inside a tile is the kernels' (whole pages may be copied
+ *   and shared).  d = 64, 128 or 256; page a multiple of 32, up to 65536; pages * page, and the
+ *   tokens of a request, at most 2^31 - 1025; Hkv at most 65535.
+ * block_table [B][width] int32: entry i of request b is the page of its tokens i * page ..
+ *   (i + 1) * page - 1; entries of tokens that a call does not touch may hold anything.
+ * A slot, page, length or sequence outside its range is skipped or cut (each entry point says how)
+ * and sets bit 10 of the device error word; nothing is read or written outside the arrays.
+ *
+ * q8_rope_table -- a step's rotations, for all its layers: table [T][2][half] float, the cosines and
+ * then the sines of positions[axis[i]][t] * inv_freq[i].
+ *   positions [axes][T] int32 (text: one axis; images and video: time, height, width), inv_freq
+ *     [half] double, axis [half] int32 (NULL: axis 0 for all); half % 8 == 0, half <= 1024.
+ *   The angle is kept to 2^-31 turns for frequencies up to 1 in magnitude, above to |position *
+ *   frequency| 2^-63 turns beside that.  A frequency of 2^32 or more in magnitude, one that is
+ *   not finite, or an axis outside [0, axes) makes NaN of its pair.
+ */
+q8_status q8_rope_table(const int32_t* positions, int64_t axes, const double* inv_freq, const int32_t* axis,
+                        float* table, int64_t T, int64_t half, cudaStream_t stream);
+
+/*
+ * q8_kv4_append -- RMSNorm of every query and key head, the rotation of their first rot channels,
+ * and the tokens' keys and values into the cache, in one pass.
+ *   q [T][H][d], k and v [T][Hkv][d] of type xtype, strides[4] = elements between the tokens of q,
+ *     k, v and q_out (NULL: contiguous; views of a fused projection's rows are fine, a stride of 0
+ *     repeats an input), heads d elements apart.  H may be 0.
+ *   q_weight, k_weight [d] float: z = x * weight, r = 1 / sqrt(mean_d x^2 + eps); NULL: z = x,
+ *     r = 1;  eps finite and > 0 where a weight is given (else Q8_ERR_VALUE).
+ *   table [T][2][rot / 2] from q8_rope_table: pair (a, b) of z becomes (a cos - b sin, a sin + b
+ *     cos), pairs as q8_qk_norm_rope's (interleaved 0: channels (i, i + rot / 2); 1: (2 i, 2 i + 1)).
+ *     rot % 16 == 0, 0 <= rot <= d.
+ *   q_out [T][H][d]: bfloat16 bits of r times the turned z, rounded once; it may be q itself
+ *     (bfloat16, the same strides), and may not overlap an input in another way.
+ *   slots [T] int32: page * page_index + offset of the token; a negative one keeps the token out of
+ *     the cache; one behind the cache is skipped and sets bit 10.  The slots of a call differ: of
+ *     tokens with the same slot, any one's bytes may be kept, place by place.
+ *   A key's z is turned with every product and sum rounded to binary32, a value's z is v.  Blocks of
+ *     32 channels: codes rint(fl(z * fl(7 / amax))) in [-7, 7], amax = max |z|; scale
+ *     bfloat16(fl(fl(amax * r) * fl(1 / 7))); amax < 2^-120 makes zeros.  Codes do not depend on
+ *     how r was summed.
+ */
+q8_status q8_kv4_append(const void* q, const void* k, const void* v, q8_dtype xtype, const int64_t* strides,
+                        const float* q_weight, const float* k_weight, float eps, const float* table, int64_t rot,
+                        int interleaved, const int32_t* slots, uint8_t* cache, int64_t page_stride, int64_t pages,
+                        int64_t page, uint16_t* q_out, int64_t T, int64_t H, int64_t Hkv, int64_t d,
+                        cudaStream_t stream);
+
+/*
+ * q8_kv4_gather -- keys and values of the cache as they stand for: row cu[b] + i of k and v
+ * [T][Hkv][d] (binary32, or bfloat16 rounded once) is token first[b] + i of request b, for the
+ * rows cu[b] .. cu[b + 1] - 1.  cu [B + 1] int32, rising; first [B] int32 (NULL: 0).  Rows
+ * outside every sequence are left as they are, and so are rows whose token or page is outside
+ * the cache (bit 10).
+ */
+q8_status q8_kv4_gather(const uint8_t* cache, int64_t page_stride, int64_t pages, int64_t page,
+                        const int32_t* block_table, int64_t width, const int32_t* first, const int32_t* cu, void* k,
+                        void* v, q8_dtype otype, int64_t B, int64_t T, int64_t Hkv, int64_t d, cudaStream_t stream);
+
+/*
+ * q8_kv4_attention -- attention of each request's newest tokens over its cache.
+ *   q, o [Tq][H][d] bfloat16 bits, strides[4] = {q token, q head, o token, o head} in elements (NULL:
+ *     contiguous), H / Hkv <= 128.  Request b has the queries cu_q[b] .. cu_q[b + 1] - 1 (cu_q [B + 1]
+ *     int32; NULL: one each, Tq == B) and kv_len[b] int32 tokens in the cache, the queries' own
+ *     among them: its query i of lq sees the keys j <= i + kv_len[b] - lq.  A query that sees no
+ *     key gets 0.  Rows of o outside every sequence are left as they are.
+ *   A sequence that is not inside [0, Tq] or has a negative length is skipped; kv_len[b] outside
+ *     [0, width * page] is taken as the nearest length inside; tokens of a page outside the cache
+ *     are not seen.  Each sets bit 10.
+ *   Rows of the cache behind kv_len[b] are not used, whatever they hold.  |q| below 2^90.
+ *   Meant for few queries a request (a decode step, drafted tokens); any number is right, and for
+ *     whole chunks of a prompt q8_kv4_gather with q8_prompt_attention is faster.
+ * Scores and sums are binary32; a weight, and its product with a value's scale, are each rounded to
+ * bfloat16; o is rounded once.  The order of all sums is fixed by the lengths.
+ * workspace: at least q8_kv4_attention_workspace_size() bytes, 16-byte aligned (one_query: cu_q is
+ * NULL).  Calls that overlap in time need one each.  Never allocates.
+ */
+q8_status q8_kv4_attention(const uint16_t* q, const uint8_t* cache, int64_t page_stride, int64_t pages, int64_t page,
+                           const int32_t* block_table, int64_t width, const int32_t* kv_len, const int32_t* cu_q,
+                           uint16_t* o, int64_t B, int64_t Tq, int64_t H, int64_t Hkv, int64_t d, float scale,
+                           const int64_t* strides, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t q8_kv4_attention_workspace_size(int64_t H, int64_t Hkv, int64_t d, int one_query);
+
+/*
  * Prepared weights for the tensor-core path.  The tensor path feeds the MMA binary16
  * copies of the int8 codes (exact: |q| <= 127); q8_linear / q8_linear_ex / q8_linear_fused
  * widen the codes on every call (read N*K bytes, write and re-read 2*N*K).  For weights
@@ -353,8 +444,8 @@ q8_status q8_block_sums(const int8_t* xq, const int8_t* Wq, int32_t* isum, int64
  * library's device error word: bit 0 = a bounded device-side wait gave up (the results
  * of that call are undefined), bit 1 = a kernel met launch parameters it cannot handle,
  * bit 8 = q8_bsa_attention skipped a listed key block, bit 9 = q8_prompt_attention skipped a
- * malformed sequence or q8_prefix_attention clamped a cache length (each says what becomes of
- * the rest).  0 means no error.  Returns Q8_ERR_CUDA through *status if the sync itself failed.
+ * malformed sequence or q8_prefix_attention clamped a cache length, bit 10 = a slot, page, length or
+ * sequence of a q8_kv4 call was outside its range (each says what becomes of the rest).  0 means no error.  Returns Q8_ERR_CUDA through *status if the sync itself failed.
  */
 uint32_t q8_device_error(q8_status* status);
 

@@ -19,6 +19,11 @@ this package fails.
     q, k = q8_qk_norm_rope(q, k, positions, inv_freq, q_weight=wq, k_weight=wk)  # heads' norm + rotation
     o = q8_prompt_attention(q, k, v, cu_q)             # causal, packed sequences of any lengths
     o = q8_prefix_attention(q, kp, vp, ko, vo, n)      # one new token a request, shared prefix
+    tab = q8_rope_table(positions, inv_freq)           # a step's rotations, for all layers
+    cache = torch.zeros(q8_kv4_cache_shape(pages, page, Hkv, d), dtype=torch.uint8, device="cuda")
+    qr = q8_kv4_append(k, v, cache, slots, table=tab, q=q, q_weight=wq, k_weight=wk)  # 4-bit paged cache
+    o = q8_kv4_attention(qr, cache, block_table, kv_len)  # newest tokens over their caches
+    k, v = q8_kv4_gather(cache, block_table, cu, tokens)  # the cache read back
     codes, scales = q8_kv3_encode(kv)                  # kv [..., 128] -> 3-bit codes + scales
     kv_hat = q8_kv3_decode(codes, scales, torch.bfloat16)
     isum = q8_block_sums(xq, Wq, path="decode")  # int32 [M,N,K/32]
@@ -34,7 +39,8 @@ __all__ = ["Q8Error", "q8_quantize_weights", "q8_quantize_act", "q8_quantize_act
            "q8_weights_to_f16", "q8_linear_prepared", "q8_linear_prepared_workspace_size",
            "q8_bsa_attention", "q8_qk_norm_rope", "q8_prompt_attention",
            "q8_prompt_attention_workspace_size", "q8_prefix_attention",
-           "q8_prefix_attention_workspace_size",
+           "q8_prefix_attention_workspace_size", "q8_rope_table", "q8_kv4_cache_shape", "q8_kv4_append",
+           "q8_kv4_gather", "q8_kv4_attention", "q8_kv4_attention_workspace_size", "KV4_TILE",
            "q8_linear_fused", "EPILOGUES",
            "q8_linear_workspace_size", "q8_block_sums", "q8_device_error", "q8_release",
            "q8_set_timing_events", "q8_linear_noalloc", "NOALLOC_SCRATCH_BYTES",
@@ -83,6 +89,10 @@ def _load():
         "q8_qk_norm_rope": [p, p, i32, i64, i64, p, p, f32, p, p, i64, i32, p, p, i64, i64, i64, i64, i64, i64, p],
         "q8_prompt_attention": [p, p, p, p, p, p, i64, i64, i64, i64, i64, i64, f32, p, p, sz, p],
         "q8_prefix_attention": [p, p, p, p, p, p, p, i64, i64, i64, i64, i64, i64, f32, p, p, sz, p],
+        "q8_rope_table": [p, i64, p, p, p, i64, i64, p],
+        "q8_kv4_append": [p, p, p, i32, p, p, p, f32, p, i64, i32, p, p, i64, i64, i64, p, i64, i64, i64, i64, p],
+        "q8_kv4_gather": [p, i64, i64, i64, p, i64, p, p, p, p, i32, i64, i64, i64, i64, p],
+        "q8_kv4_attention": [p, p, i64, i64, i64, p, i64, p, p, p, i64, i64, i64, i64, i64, f32, p, p, sz, p],
         "q8_linear_prepared": [p, i32, p, f32, p, p, i32, p, p, i32, i64, i64, i64, p, sz, p],
     }
     for name, args in sigs.items():
@@ -98,6 +108,8 @@ def _load():
     for name in ("q8_prompt_attention_workspace_size", "q8_prefix_attention_workspace_size"):
         getattr(L, name).argtypes = [i64] * 6
         getattr(L, name).restype = sz
+    L.q8_kv4_attention_workspace_size.argtypes = [i64, i64, i64, i32]
+    L.q8_kv4_attention_workspace_size.restype = sz
     L.q8_device_error.argtypes = [ctypes.POINTER(i32)]
     L.q8_device_error.restype = ctypes.c_uint32
     L.q8_status_string.argtypes = [i32]
@@ -547,6 +559,194 @@ def q8_prefix_attention(q, k_prefix, v_prefix, k_own, v_own, own_len, scale=None
                    so[0], so[1]), pw, nbytes, _stream_on(stream, dev))
     if status:
         raise Q8Error(status, "q8_prefix_attention")
+    return o
+
+
+KV4_TILE = 32  # tokens of a tile
+
+
+def q8_kv4_cache_shape(pages, page, Hkv, d):
+    """The shape of a paged 4-bit cache (uint8): [pages, Hkv, page/32, 36 d], page a multiple of 32."""
+    if page % KV4_TILE or page < KV4_TILE or d not in (64, 128, 256):
+        raise ValueError(f"page: a multiple of {KV4_TILE}, d: 64, 128 or 256; got {page} and {d}")
+    return pages, Hkv, page // KV4_TILE, 36 * d
+
+
+def _kv4_cache(cache, Hkv, d, dev):
+    """(page stride in bytes, pages, page): cache is a uint8 tensor of q8_kv4_cache_shape on CUDA device
+    dev whose pages are contiguous (but may lie apart from one another)."""
+    if cache.dtype is not torch.uint8:
+        raise TypeError(f"cache: expected torch.uint8, got {cache.dtype}")
+    if cache.dim() != 4 or cache.shape[1] != Hkv or cache.shape[3] != 36 * d:
+        raise ValueError(f"cache: expected shape (pages, {Hkv}, page/32, {36 * d}), got {tuple(cache.shape)}")
+    if cache.get_device() != dev:
+        raise ValueError(f"cache: must be a CUDA tensor on the current device (cuda:{dev})")
+    pages, _, tiles, size = cache.shape
+    st = cache.stride()
+    if (st[3] != 1 and size > 1) or (st[2] != size and tiles > 1) or (st[1] != tiles * size and Hkv > 1):
+        raise ValueError("cache: the bytes of a page must be contiguous")
+    return (st[0] if pages > 1 else Hkv * tiles * size), pages, KV4_TILE * tiles
+
+
+def _block_table(block_table, B, dev):
+    """(address, width) of a contiguous int32 [B, width] on CUDA device dev."""
+    if block_table.dtype is not torch.int32:
+        raise TypeError(f"block_table: expected torch.int32, got {block_table.dtype}")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table: expected shape ({B}, width), got {tuple(block_table.shape)}")
+    if block_table.get_device() != dev or not block_table.is_contiguous():
+        raise ValueError(f"block_table: must be a contiguous CUDA tensor on the current device (cuda:{dev})")
+    return block_table.data_ptr(), block_table.shape[1]
+
+
+def q8_rope_table(positions, inv_freq, axis=None, table=None, stream=None):
+    """A step's rotations, for all its layers: positions int32 [T], or [axes, T] with axis int32 [half]
+    (which axis turns a pair; None: the first), inv_freq float64 [half] -> float32 [T, 2, half],
+    cosines then sines."""
+    dev = torch.cuda.current_device()
+    if positions.dtype is not torch.int32:
+        raise TypeError(f"positions: expected torch.int32, got {positions.dtype}")
+    if positions.dim() not in (1, 2):
+        raise ValueError(f"positions: expected shape (T,) or (axes, T), got {tuple(positions.shape)}")
+    if positions.get_device() != dev or not positions.is_contiguous():
+        raise ValueError(f"positions: must be a contiguous CUDA tensor on the current device (cuda:{dev})")
+    axes, T = (1, positions.shape[0]) if positions.dim() == 1 else positions.shape
+    (half,) = inv_freq.shape
+    if table is None:
+        table = _empty((T, 2, half), torch.float32, positions.device, stream)
+    elif table.dtype is not torch.float32:
+        raise TypeError(f"table: expected torch.float32, got {table.dtype}")
+    elif table.shape != (T, 2, half) or table.get_device() != dev or not table.is_contiguous():
+        raise ValueError(f"table: a contiguous CUDA tensor of shape {(T, 2, half)} on the current device (cuda:{dev})")
+    status = _L.q8_rope_table(positions.data_ptr(), axes, _vector("inv_freq", inv_freq, torch.float64, half, dev),
+                              None if axis is None else _vector("axis", axis, torch.int32, half, dev),
+                              table.data_ptr(), T, half, _stream_on(stream, dev))
+    if status:
+        raise Q8Error(status, "q8_rope_table")
+    return table
+
+
+_STRIDES4 = struct.Struct("4q").pack
+
+
+def q8_kv4_append(k, v, cache, slots, table=None, q=None, q_weight=None, k_weight=None, eps=1e-6,
+                  interleaved=False, q_out=None, stream=None):
+    """A step's keys and values into the paged 4-bit cache, and its queries made ready: RMSNorm of the
+    query and key heads (weights float32 [d], None: none), their rotation by table (float32
+    [T, 2, rot/2] from q8_rope_table, None: none), and the quantiser.  k, v [T,Hkv,d] and q [T,H,d]
+    bfloat16 or float32 (views of a projection's rows are fine), cache uint8 of
+    q8_kv4_cache_shape, slots int32 [T] (page * index + offset; negative: not kept)
+    -> q_out [T,H,d] bfloat16 (None without q)."""
+    dev = torch.cuda.current_device()
+    T, Hkv, d = k.shape
+    dtype, f32 = k.dtype, torch.float32
+    xtype = DTYPES.get(dtype)
+    if xtype is None:
+        raise TypeError(f"k: expected bfloat16 or float32, got {dtype}")
+    sk, sv = _heads("k", k, dtype, (T, Hkv, d), dev), _heads("v", v, dtype, (T, Hkv, d), dev)
+    if Hkv > 1 and (sk[1] != d or sv[1] != d):
+        raise ValueError("k, v: the heads of a token must be contiguous")
+    H, sq, sqo, pq, po = 0, (0,), (0,), None, None
+    if q is not None:
+        H = q.shape[1]
+        sq = _heads("q", q, dtype, (T, H, d), dev)
+        if q_out is None:
+            q_out = _empty((T, H, d), torch.bfloat16, q.device, stream)
+        sqo = _heads("q_out", q_out, torch.bfloat16, (T, H, d), dev)
+        if H > 1 and (sq[1] != d or sqo[1] != d):
+            raise ValueError("q, q_out: the heads of a token must be contiguous")
+        pq, po = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out: given without q")
+    rot, pt = 0, None
+    if table is not None:
+        if table.dtype is not f32:
+            raise TypeError(f"table: expected torch.float32, got {table.dtype}")
+        if table.dim() != 3 or table.shape[:2] != (T, 2):
+            raise ValueError(f"table: expected shape ({T}, 2, rot/2), got {tuple(table.shape)}")
+        if table.get_device() != dev or not table.is_contiguous():
+            raise ValueError(f"table: must be a contiguous CUDA tensor on the current device (cuda:{dev})")
+        rot, pt = 2 * table.shape[2], table.data_ptr()
+    page_stride, pages, page = _kv4_cache(cache, Hkv, d, dev)
+    status = _L.q8_kv4_append(
+        pq, k.data_ptr(), v.data_ptr(), xtype, _STRIDES4(sq[0], sk[0], sv[0], sqo[0]),
+        None if q_weight is None else _vector("q_weight", q_weight, f32, d, dev),
+        None if k_weight is None else _vector("k_weight", k_weight, f32, d, dev), eps, pt, rot,
+        1 if interleaved else 0, _vector("slots", slots, torch.int32, T, dev), cache.data_ptr(), page_stride, pages,
+        page, po, T, H, Hkv, d, _stream_on(stream, dev))
+    if status:
+        raise Q8Error(status, "q8_kv4_append")
+    return q_out
+
+
+def q8_kv4_gather(cache, block_table, cu, tokens, first=None, out_dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """The cache read back: row cu[b] + i of k and v [tokens,Hkv,d] (out_dtype bfloat16 or float32) is
+    token first[b] + i (None: i) of request b; cu int32 [B+1], first int32 [B], block_table int32
+    [B, width].  New k and v are not initialised outside the sequences."""
+    dev = torch.cuda.current_device()
+    if out_dtype not in DTYPES:
+        raise TypeError(f"out_dtype: expected bfloat16 or float32, got {out_dtype}")
+    if cache.dim() != 4:
+        raise ValueError(f"cache: expected shape (pages, Hkv, page/32, 36 d), got {tuple(cache.shape)}")
+    Hkv, d = cache.shape[1], cache.shape[3] // 36
+    page_stride, pages, page = _kv4_cache(cache, Hkv, d, dev)
+    n = cu.numel()
+    if n < 1:
+        raise ValueError("cu: expected at least one entry")
+    pc, (pb, width) = _vector("cu", cu, torch.int32, n, dev), _block_table(block_table, n - 1, dev)
+    shape = (tokens, Hkv, d)
+    out = []
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            t = _empty(shape, out_dtype, cache.device, stream)
+        elif t.dtype is not out_dtype:
+            raise TypeError(f"{name}: expected {out_dtype}, got {t.dtype}")
+        elif t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{name}: a contiguous CUDA tensor of shape {shape} on the current device (cuda:{dev})")
+        out.append(t)
+    status = _L.q8_kv4_gather(
+        cache.data_ptr(), page_stride, pages, page, pb, width,
+        None if first is None else _vector("first", first, torch.int32, n - 1, dev), pc, out[0].data_ptr(),
+        out[1].data_ptr(), DTYPES[out_dtype], n - 1, tokens, Hkv, d, _stream_on(stream, dev))
+    if status:
+        raise Q8Error(status, "q8_kv4_gather")
+    return out[0], out[1]
+
+
+def q8_kv4_attention_workspace_size(H, Hkv, d, one_query=True) -> int:
+    return int(_L.q8_kv4_attention_workspace_size(H, Hkv, d, 1 if one_query else 0))
+
+
+def q8_kv4_attention(q, cache, block_table, kv_len, cu_q=None, scale=None, o=None, workspace=None, stream=None):
+    """Attention of each request's newest tokens over its cache: q [Tq,H,d] bfloat16 (strided views are
+    fine), cache uint8 of q8_kv4_cache_shape, block_table int32 [B, width], kv_len int32 [B] tokens
+    of each request (the queries' own among them), cu_q int32 [B+1] (None: one query each, Tq = B):
+    query i of lq sees the keys j <= i + kv_len - lq -> o [Tq,H,d] bfloat16 (a new o is not
+    initialised outside the sequences).  scale None: 1/sqrt(d).  workspace None: allocated here with
+    torch (as a new o, on `stream`)."""
+    dev = torch.cuda.current_device()
+    Tq, H, d = q.shape
+    sq = _heads("q", q, torch.bfloat16, (Tq, H, d), dev)
+    Hkv = cache.shape[1] if cache.dim() == 4 else 0
+    page_stride, pages, page = _kv4_cache(cache, Hkv, d, dev)
+    B = Tq if cu_q is None else cu_q.numel() - 1
+    if B < 0:
+        raise ValueError("cu_q: expected at least one entry")
+    pc = None if cu_q is None else _vector("cu_q", cu_q, torch.int32, B + 1, dev)
+    (pb, width), pn = _block_table(block_table, B, dev), _vector("kv_len", kv_len, torch.int32, B, dev)
+    if o is None:
+        o = _empty((Tq, H, d), torch.bfloat16, q.device, stream)
+        so = (H * d, d)
+    else:
+        so = _heads("o", o, torch.bfloat16, (Tq, H, d), dev)
+    workspace, pw, nbytes = _workspace(
+        workspace, _L.q8_kv4_attention_workspace_size(H, Hkv, d, 1 if cu_q is None else 0), q.device, dev, stream)
+    status = _L.q8_kv4_attention(
+        q.data_ptr(), cache.data_ptr(), page_stride, pages, page, pb, width, pn, pc, o.data_ptr(), B, Tq, H, Hkv, d,
+        (d or 1) ** -0.5 if scale is None else scale, _STRIDES4(sq[0], sq[1], so[0], so[1]), pw, nbytes,
+        _stream_on(stream, dev))
+    if status:
+        raise Q8Error(status, "q8_kv4_attention")
     return o
 
 

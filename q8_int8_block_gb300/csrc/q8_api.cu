@@ -209,6 +209,22 @@ q8_status take_strides(int64_t* st, const int64_t* plain, const int64_t* given, 
   return Q8_OK;
 }
 
+// The 4-bit cache: heads of 64, 128 or 256 channels, pages of whole tiles that do not overlap, slots
+// that fit 32 bits.
+q8_status check_cache(const void* cache, int64_t page_stride, int64_t pages, int64_t page, int64_t Hkv, int64_t d) {
+  if ((d != 64 && d != 128 && d != 256) || Hkv < 0 || Hkv > 65535 || pages < 0 || page < 32 || page % 32 != 0 || page > 65536 ||
+      pages > kSizeLimit || pages * page > kSizeLimit || page_stride < 0 || page_stride >= (kStrideLimit << 1) ||
+      (pages > 1 && page_stride < page / 32 * Hkv * 36 * d))
+    return Q8_ERR_SHAPE;
+  return aligned16(cache) && (pages < 2 || page_stride % 16 == 0) ? Q8_OK : Q8_ERR_ALIGN;
+}
+
+// [B][width] pages of a request: its tokens fit 32 bits.
+bool table_ok(int64_t B, int64_t width, int64_t page) {
+  return width >= 0 && width <= kSizeLimit && page > 0 && page <= 65536 && width * page <= kSizeLimit &&
+         static_cast<double>(B) * static_cast<double>(width) < 281474976710656.0;
+}
+
 q8_status launch_status(cudaError_t e) { return e == cudaSuccess ? Q8_OK : cuda_fail(e); }
 
 // ---- timing hook (q8_set_timing_events) ----------------------------------------------
@@ -627,6 +643,155 @@ size_t q8_prefix_attention_workspace_size(int64_t B, int64_t P, int64_t cap, int
   DeviceInfo dev;
   if (current_device(&dev) != Q8_OK) return 0;
   return prefix_ws_bytes(B, P, cap, H, Hkv, d, dev);
+}
+
+q8_status q8_rope_table(const int32_t* positions, int64_t axes, const double* inv_freq, const int32_t* axis,
+                        float* table, int64_t T, int64_t half, cudaStream_t stream) {
+  if (T < 0 || T > kSizeLimit || axes < 1 || axes > kSizeLimit || half < 0 || half > 1024 || half % 8 != 0)
+    return Q8_ERR_SHAPE;
+  if (T > 0 && half > 0 && (positions == nullptr || inv_freq == nullptr || table == nullptr)) return Q8_ERR_NULL;
+  if (!aligned16(table) || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(axis) & 3u) != 0 || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0)
+    return Q8_ERR_ALIGN;
+  DeviceInfo dev;
+  const q8_status st = current_device(&dev);
+  if (st != Q8_OK) return st;
+  return launch_status(launch_rope_table(positions, static_cast<int>(axes), inv_freq, axis, table, T,
+                                         static_cast<int>(half), dev, stream));
+}
+
+q8_status q8_kv4_append(const void* q, const void* k, const void* v, q8_dtype xtype, const int64_t* strides,
+                        const float* q_weight, const float* k_weight, float eps, const float* table, int64_t rot,
+                        int interleaved, const int32_t* slots, uint8_t* cache, int64_t page_stride, int64_t pages,
+                        int64_t page, uint16_t* q_out, int64_t T, int64_t H, int64_t Hkv, int64_t d,
+                        cudaStream_t stream) {
+  if (xtype != Q8_F32 && xtype != Q8_BF16) return Q8_ERR_DTYPE;
+  if (T < 0 || T > kSizeLimit || H < 0 || Hkv < 0 || static_cast<double>(T) * static_cast<double>(H + 2 * Hkv) > kRowLimit ||
+      H > kSizeLimit || Hkv > kSizeLimit || rot < 0 || rot > d || rot % 16 != 0)
+    return Q8_ERR_SHAPE;
+  q8_status st = check_cache(cache, page_stride, pages, page, Hkv, d);
+  if (st == Q8_ERR_SHAPE) return st;
+  Kv4AppendArgs a = {};
+  const int64_t heads[4] = {H, Hkv, Hkv, H};
+  const int64_t per16 = xtype == Q8_F32 ? 4 : 8;
+  bool unaligned = st == Q8_ERR_ALIGN;
+  for (int i = 0; i < 4; ++i) {
+    a.st[i] = strides != nullptr && T > 1 ? strides[i] : heads[i] * d;
+    // an input's tokens may repeat (stride 0), an output's may not overlap
+    if (!stride_ok(a.st[i], T) || (i == 3 && T > 1 && H > 0 && a.st[i] < H * d)) return Q8_ERR_SHAPE;
+    unaligned = unaligned || a.st[i] % (i == 3 ? 8 : per16) != 0;
+  }
+  if ((q_weight != nullptr || k_weight != nullptr) && (!(eps > 0.0f) || !std::isfinite(eps))) return Q8_ERR_VALUE;
+  const bool any_q = T > 0 && H > 0, any_k = T > 0 && Hkv > 0;
+  if ((any_q && (q == nullptr || q_out == nullptr)) || (any_k && (k == nullptr || v == nullptr || (pages > 0 && cache == nullptr))) ||
+      (T > 0 && H + Hkv > 0 && (slots == nullptr || (rot > 0 && table == nullptr))))
+    return Q8_ERR_NULL;
+  if (unaligned || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(q_weight) ||
+      !aligned16(k_weight) || !aligned16(table) || (reinterpret_cast<uintptr_t>(slots) & 3u) != 0)
+    return Q8_ERR_ALIGN;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != Q8_OK) return st;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.f32 = xtype == Q8_F32;
+  a.interleaved = interleaved != 0;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.table = table;
+  a.rot = static_cast<int>(rot);
+  a.slots = slots;
+  a.cache = cache;
+  a.page_stride = page_stride;
+  a.pages = pages;
+  a.page = page;
+  a.q_out = q_out;
+  a.T = T;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.d = d;
+  return launch_status(launch_kv4_append(a, dev, stream));
+}
+
+q8_status q8_kv4_gather(const uint8_t* cache, int64_t page_stride, int64_t pages, int64_t page,
+                        const int32_t* block_table, int64_t width, const int32_t* first, const int32_t* cu, void* k,
+                        void* v, q8_dtype otype, int64_t B, int64_t T, int64_t Hkv, int64_t d, cudaStream_t stream) {
+  if (otype != Q8_F32 && otype != Q8_BF16) return Q8_ERR_DTYPE;
+  if (B < 0 || B >= kSizeLimit || T < 0 || T > kSizeLimit || Hkv < 0 || !table_ok(B, width, page) ||
+      static_cast<double>(T) * static_cast<double>(Hkv) > kRowLimit)
+    return Q8_ERR_SHAPE;
+  q8_status st = check_cache(cache, page_stride, pages, page, Hkv, d);
+  if (st == Q8_ERR_SHAPE) return st;
+  const bool any = B > 0 && T > 0 && Hkv > 0;
+  if (any && (cu == nullptr || k == nullptr || v == nullptr || (pages > 0 && cache == nullptr) ||
+              (width > 0 && block_table == nullptr)))
+    return Q8_ERR_NULL;
+  if (st != Q8_OK || !aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(block_table) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(first) & 3u) != 0 || (reinterpret_cast<uintptr_t>(cu) & 3u) != 0)
+    return Q8_ERR_ALIGN;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != Q8_OK) return st;
+  const Kv4GatherArgs a = {cache, page_stride, pages, page, block_table, width, first, cu, k, v, otype == Q8_BF16,
+                           B, T, Hkv, d, nullptr};
+  return launch_status(launch_kv4_gather(a, dev, stream));
+}
+
+q8_status q8_kv4_attention(const uint16_t* q, const uint8_t* cache, int64_t page_stride, int64_t pages, int64_t page,
+                           const int32_t* block_table, int64_t width, const int32_t* kv_len, const int32_t* cu_q,
+                           uint16_t* o, int64_t B, int64_t Tq, int64_t H, int64_t Hkv, int64_t d, float scale,
+                           const int64_t* strides, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (B < 0 || B >= kSizeLimit || Tq < 0 || Tq > kSizeLimit || H < 0 || Hkv <= 0 || H > kSizeLimit || H % Hkv != 0 ||
+      H / Hkv > 128 || (cu_q == nullptr && Tq != B) || !table_ok(B, width, page) ||
+      static_cast<double>(Tq + B) * static_cast<double>(H) > kRowLimit)
+    return Q8_ERR_SHAPE;
+  q8_status st = check_cache(cache, page_stride, pages, page, Hkv, d);
+  if (st == Q8_ERR_SHAPE) return st;
+  const bool unaligned = st == Q8_ERR_ALIGN;
+  Kv4AttentionArgs a = {};
+  const int64_t plain[4] = {H * d, d, H * d, d};
+  const int64_t extent[4] = {Tq, H, Tq, H};
+  if ((st = take_strides(a.st, plain, strides, extent, 4, 2, 0)) != Q8_OK) return st;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return Q8_ERR_VALUE;
+  const bool any = B > 0 && Tq > 0 && H > 0;
+  if (any && (q == nullptr || o == nullptr || kv_len == nullptr || (pages > 0 && cache == nullptr) ||
+              (width > 0 && block_table == nullptr)))
+    return Q8_ERR_NULL;
+  if (unaligned || !aligned16(q) || !aligned16(o) || !aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(block_table) & 3u) != 0 || (reinterpret_cast<uintptr_t>(kv_len) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(cu_q) & 3u) != 0)
+    return Q8_ERR_ALIGN;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != Q8_OK) return st;
+  if (!any) return Q8_OK;
+  const size_t need = kv4_attention_ws_bytes(H, Hkv, d, cu_q == nullptr, dev);
+  if (workspace == nullptr) return Q8_ERR_NULL;
+  if (workspace_bytes < need) return Q8_ERR_NOMEM;
+  a.q = q;
+  a.cache = cache;
+  a.page_stride = page_stride;
+  a.pages = pages;
+  a.page = page;
+  a.block_table = block_table;
+  a.width = width;
+  a.kv_len = kv_len;
+  a.cu_q = cu_q;
+  a.o = o;
+  a.B = B;
+  a.Tq = Tq;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.scale = scale;
+  a.part = workspace;
+  return launch_status(launch_kv4_attention(a, dev, stream));
+}
+
+size_t q8_kv4_attention_workspace_size(int64_t H, int64_t Hkv, int64_t d, int one_query) {
+  if (H <= 0 || Hkv <= 0 || H > kSizeLimit || H % Hkv != 0 || H / Hkv > 128 || (d != 64 && d != 128 && d != 256)) return 0;
+  DeviceInfo dev;
+  if (current_device(&dev) != Q8_OK) return 0;
+  return kv4_attention_ws_bytes(H, Hkv, d, one_query != 0, dev);
 }
 
 q8_status q8_kv3_encode(const void* x, q8_dtype xtype, uint32_t* codes, float* scales,

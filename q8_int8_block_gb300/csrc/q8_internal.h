@@ -159,6 +159,57 @@ size_t prefix_ws_bytes(int64_t B, int64_t P, int64_t cap, int64_t H, int64_t Hkv
 cudaError_t launch_prompt_attention(PromptArgs a, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_prefix_attention(PrefixArgs a, const DeviceInfo& dev, cudaStream_t stream);
 
+// ---- q8_kv4.cu, q8_kv4_attn.cu ----------------------------------------------------
+// The paged 4-bit cache (q8_kv4.cuh).  Arguments of the entry points, checked; strides in
+// elements, of a page in bytes.
+struct Kv4AppendArgs {
+  const void *q, *k, *v;
+  bool f32, interleaved;
+  int64_t st[4];  // q, k, v, q_out: between tokens
+  const float *q_weight, *k_weight;
+  float eps;
+  const float* table;
+  int rot;
+  const int32_t* slots;
+  uint8_t* cache;
+  int64_t page_stride, pages, page;
+  uint16_t* q_out;
+  int64_t T, H, Hkv, d;
+  uint32_t* err;
+};
+struct Kv4GatherArgs {
+  const uint8_t* cache;
+  int64_t page_stride, pages, page;
+  const int32_t* block_table;
+  int64_t width;
+  const int32_t *first, *cu;
+  void *k, *v;
+  bool bf16;
+  int64_t B, T, Hkv, d;
+  uint32_t* err;
+};
+struct Kv4AttentionArgs {
+  const uint16_t* q;
+  const uint8_t* cache;
+  int64_t page_stride, pages, page;
+  const int32_t* block_table;
+  int64_t width;
+  const int32_t *kv_len, *cu_q;
+  uint16_t* o;
+  int64_t B, Tq, H, Hkv, d;
+  float scale;
+  int64_t st[4];  // q token, q head, o token, o head
+  void* part;
+  uint32_t* err;
+};
+cudaError_t launch_rope_table(const int32_t* positions, int axes, const double* inv_freq, const int32_t* axis,
+                              float* table, int64_t T, int half, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_kv4_append(Kv4AppendArgs a, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_kv4_gather(Kv4GatherArgs a, const DeviceInfo& dev, cudaStream_t stream);
+// one_query: the call has no cu_q, every request one query
+size_t kv4_attention_ws_bytes(int64_t H, int64_t Hkv, int64_t d, bool one_query, const DeviceInfo& dev);
+cudaError_t launch_kv4_attention(Kv4AttentionArgs a, const DeviceInfo& dev, cudaStream_t stream);
+
 // ---- q8_gemm.cu -------------------------------------------------------------------
 // Tensor-core GEMM on binary16 codes: A16 [M,K] activation codes, B16 [N,K] weight codes,
 // xd [M,K/32] f32, Wd [N,K/32] binary16 bits.  Writes y [M,N] (rescaled sum) or, when
