@@ -33,6 +33,9 @@
 #include "q8_internal.h"
 #include "q8_kv4.cuh"
 
+#ifndef KVWEXPR
+#define KVWEXPR (D == 64 ? (NT == 2 ? 12 : 16) : D == 128 && NT == 1 ? 12 : 8)
+#endif
 namespace q8 {
 namespace {
 
@@ -45,7 +48,7 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                "{%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -58,9 +61,19 @@ __device__ __forceinline__ uint32_t mul_bf16(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// an 8 x 8 matrix of 16-bit elements, two of a row to a lane, transposed
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
+#ifndef KVX
+#define KVX 2
+#endif
+constexpr int kExtra = KVX;
 constexpr float kNone = -1e30f;     // reference of a row that has seen no key
 constexpr float kLift = 64.0f;      // weights are carried as 2^64 p
 constexpr float kSlack = 10.0f;     // a reference may lag behind the largest score by 2^10
@@ -69,182 +82,226 @@ struct Kv4Params {
   Kv4AttentionArgs a;
   int G;
   float scale_log2;
-  int per_thread;    // requests whose counts a thread sums up
-  float* part;       // [blocks][2], then [blocks][warps] partial results
-  int4* meta;        // [blocks][2]: request, head, rows, flags
+  int per_lane;      // requests whose counts a lane sums up
+  uint64_t by_grid, by_G;  // 2^64 / n + 1: the high half of x times it is x / n (x n < 2^64)
+  float* part;       // [blocks][2] partial results
+  struct Record* meta;  // [blocks][2]
 };
+constexpr int kMaxBlocks = 256;     // of the attention kernel
 enum : int { kPartHeld = 1, kPartFromFront = 2, kPartGoesOn = 4 };  // flags of a partial result
+struct __align__(16) Record {  // whose partial result it is
+  int h, group, lq, flags;
+  int64_t q0;
+};
+
+// A group of rows of a request: the unit whose keys are walked.
+struct Item {
+  int64_t b, q0;     // request, its first query
+  int lq, len;       // its queries, keys
+  int tiles;         // of keys (one at least: rows without a key are written too)
+  int groups;        // of rows of a head
+  int h, group;      // key/value head, group
+  int start;         // its place in the work list, from the warp's first on
+};
 
 template <int D, int NT>
 struct Kv4Shape {
   using Tile = Kv4Tile<D>;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kWarps = D == 256 ? 8 : NT == 2 && D == 128 ? 12 : 16;
+  static constexpr int kWarps = KVWEXPR;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kStages = 221184 / (Tile::kBytes * kWarps);
-  static constexpr int kRing = kStages * Tile::kBytes;       // of a warp
   static constexpr int kPad = D + 4;                         // floats of a row's partial result: o, reference, sum
   static constexpr int kPart = kRows * kPad;                 // floats of a partial result
-  static constexpr int kOffBar = kWarps * kRing;
-  static constexpr int kOffPre = kOffBar + kWarps * kStages * 8;
-  static constexpr int kOffBad = kOffPre + (kThreads + 1) * 8;
-  static constexpr int kOffMeta = (kOffBad + kWarps * kStages * 4 + 15) / 16 * 16;
-  static constexpr int kSmem = kOffMeta + kWarps * 2 * 16;
-  static_assert(kSmem <= 226 * 1024, "shared memory of a block");
+  static constexpr int kStages = (225 * 1024 / kWarps - kPart * 4) / Tile::kBytes;
+  static constexpr int kRing = kStages * Tile::kBytes;       // of a warp
+  static constexpr int kOffAside = kWarps * kRing;           // a warp's partial result while the ring is in use
+  static constexpr int kOffRec = kOffAside + kWarps * kPart * 4;
+  static constexpr int kOffItem = kOffRec + kWarps * 2 * static_cast<int>(sizeof(Record));
+  static constexpr int kOffBar = kOffItem + kWarps * static_cast<int>(sizeof(Item));
+  static constexpr int kOffBad = kOffBar + kWarps * kStages * 8;
+  static constexpr int kSmem = kOffBad + kWarps * kStages * 4;
+  static_assert(kSmem <= 227 * 1024 - 64, "shared memory of a block");
   static_assert(kPart * 4 <= kRing, "a partial result in the ring's place");
   static_assert(kRing % 16 == 0, "alignment of bulk copies");
+  static_assert(kStages < 32 && kWarps < 32, "a lane for each");
 };
 
-// What a request asks for.
-struct Request {
-  int64_t q0;        // its first query
-  int lq, len;       // queries, keys
-  uint32_t tiles;    // of keys (one at least: rows without a key are written too)
-  uint32_t groups;   // of rows
-};
 template <int NT>
-__device__ __forceinline__ Request request(const Kv4Params& p, int64_t b, bool* bad) {
-  Request r;
+__device__ __forceinline__ void request(const Kv4Params& p, Item& it, bool* bad) {  // what request it.b asks for
   const Kv4AttentionArgs& a = p.a;
-  r.q0 = b;
+  it.q0 = it.b;
   int64_t lq = 1;
   if (a.cu_q != nullptr) {
-    r.q0 = a.cu_q[b];
-    lq = a.cu_q[b + 1] - r.q0;
-    if (r.q0 < 0 || lq < 0 || r.q0 + lq > a.Tq) {
+    it.q0 = a.cu_q[it.b];
+    lq = a.cu_q[it.b + 1] - it.q0;
+    if (it.q0 < 0 || lq < 0 || it.q0 + lq > a.Tq) {
       *bad = true;
       lq = 0;
     }
   }
-  int64_t len = a.kv_len[b];
+  int64_t len = a.kv_len[it.b];
   const int64_t most = a.width * a.page;
   if (len < 0 || len > most) {
     *bad = true;
     len = len < 0 ? 0 : most;
   }
-  r.lq = static_cast<int>(lq);
-  r.len = static_cast<int>(len);
-  r.tiles = len > 0 ? static_cast<uint32_t>((len + 31) >> 5) : 1u;
-  r.groups = static_cast<uint32_t>((lq * p.G + 8 * NT - 1) / (8 * NT));
-  return r;
+  it.lq = static_cast<int>(lq);
+  it.len = static_cast<int>(len);
+  it.tiles = len > 0 ? static_cast<int>((len + 31) >> 5) : 1;
+  it.groups = static_cast<int>((static_cast<uint32_t>(it.lq) * static_cast<uint32_t>(p.G) + 8 * NT - 1) / (8 * NT));
 }
-__device__ __forceinline__ uint64_t count(const Kv4Params& p, const Request& r) {
-  return static_cast<uint64_t>(r.tiles) * r.groups * static_cast<uint32_t>(p.a.Hkv);
+__device__ __forceinline__ uint64_t count(const Kv4Params& p, const Item& it) {
+  return static_cast<uint64_t>(it.tiles + kExtra) * static_cast<uint32_t>(it.groups) * static_cast<uint32_t>(p.a.Hkv);
 }
-
-// Where a place of the work list is.
-struct Place {
-  int64_t b;
-  uint32_t h, group, tile;
-  Request r;
-};
-template <int D, int NT>
-__device__ __forceinline__ Place place(const Kv4Params& p, const uint64_t* pre, uint64_t at) {
-  int lo = 0, hi = Kv4Shape<D, NT>::kThreads - 1;  // the last thread whose requests begin at or in front of it
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= at) lo = mid;
-    else hi = mid - 1;
-  }
-  Place w;
-  bool bad;
-  w.b = static_cast<int64_t>(lo) * p.per_thread;
-  uint64_t rest = at - pre[lo];
-  w.r = request<NT>(p, w.b, &bad);
-  for (uint64_t n = count(p, w.r); rest >= n; n = count(p, w.r)) {
-    rest -= n;
-    ++w.b;
-    w.r = request<NT>(p, w.b, &bad);
-  }
-  if (rest >> 32 == 0) {
-    const uint32_t x = static_cast<uint32_t>(rest), y = x / w.r.tiles;
-    w.tile = x - y * w.r.tiles;
-    w.h = y / w.r.groups;
-    w.group = y - w.h * w.r.groups;
-  } else {
-    const uint64_t y = rest / w.r.tiles;
-    w.tile = static_cast<uint32_t>(rest - y * w.r.tiles);
-    w.h = static_cast<uint32_t>(y / w.r.groups);
-    w.group = static_cast<uint32_t>(y - static_cast<uint64_t>(w.h) * w.r.groups);
-  }
-  return w;
-}
-
-// Row `row` of a group of rows: its query token and head; false behind the request's last.
+// the group of rows behind it (there is one)
 template <int NT>
-__device__ __forceinline__ bool row_at(const Kv4Params& p, const Request& r, uint32_t h, uint32_t group, int row,
-                                       int64_t* tok, int64_t* head) {
-  const int64_t x = static_cast<int64_t>(group) * (8 * NT) + row, i = x / p.G;
-  *tok = r.q0 + i;
-  *head = static_cast<int64_t>(h) * p.G + (x - i * p.G);
-  return i < r.lq;
+__device__ __forceinline__ void next_item(const Kv4Params& p, Item& it) {
+  it.start += it.tiles + kExtra;
+  if (++it.group < it.groups) return;
+  it.group = 0;
+  if (++it.h < p.a.Hkv) return;
+  it.h = 0;
+  bool bad;
+  do {
+    ++it.b;
+    request<NT>(p, it, &bad);
+  } while (it.groups == 0 && it.b + 1 < p.a.B);
+}
+
+// Place `at` of the work list, `before` the work in front of each lane's requests; returns the first
+// tile at or behind it.
+template <int NT>
+__device__ __forceinline__ int place(const Kv4Params& p, uint64_t before, uint64_t at, Item& it) {
+  const int c = __popc(__ballot_sync(kFull, before <= at)) - 1;  // the last lane that begins at or in front of it
+  uint64_t rest = at - __shfl_sync(kFull, before, c);
+  bool bad;
+  it.b = static_cast<int64_t>(c) * p.per_lane;
+  request<NT>(p, it, &bad);
+  for (uint64_t m = count(p, it); rest >= m; m = count(p, it)) {
+    rest -= m;
+    ++it.b;
+    request<NT>(p, it, &bad);
+  }
+  const uint32_t size = static_cast<uint32_t>(it.tiles + kExtra);
+  uint64_t y;
+  if (rest >> 32 == 0) y = static_cast<uint32_t>(rest) / size;
+  else y = rest / size;
+  const uint32_t y32 = static_cast<uint32_t>(y);  // groups of a request: below 2^31
+  it.h = static_cast<int>(y32 / static_cast<uint32_t>(it.groups));
+  it.group = static_cast<int>(y32 - static_cast<uint32_t>(it.h) * static_cast<uint32_t>(it.groups));
+  it.start = -static_cast<int>(rest - y * size);
+  return it.start < -kExtra ? -it.start - kExtra : 0;
+}
+
+// Row `row` of a group of rows: its query token (of the request) and head; false behind the last.
+template <int NT>
+__device__ __forceinline__ bool row_at(const Kv4Params& p, int lq, int h, int group, int row, int* query, int64_t* head) {
+  const uint32_t x = static_cast<uint32_t>(group) * (8 * NT) + row;
+  const uint32_t i = p.G == 1 ? x : static_cast<uint32_t>(__umul64hi(x, p.by_G));
+  *query = static_cast<int>(i);
+  *head = static_cast<int64_t>(h) * p.G + (x - i * static_cast<uint32_t>(p.G));
+  return i < static_cast<uint32_t>(lq);
 }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_kernel(const __grid_constant__ Kv4Params p) {
   using Sh = Kv4Shape<D, NT>;
   using Tile = Kv4Tile<D>;
-  constexpr int NB = Tile::kBlocks, S = Sh::kStages, kThreads = Sh::kThreads;
+  constexpr int NB = Tile::kBlocks, S = Sh::kStages;
   pdl_launch_dependents();
-  extern __shared__ __align__(1024) uint8_t sm[];
-  __shared__ uint64_t warp_sum[Sh::kWarps];
+  extern __shared__ __align__(16) uint8_t sm[];
   __shared__ int abort_flag;
-  uint64_t* pre = reinterpret_cast<uint64_t*>(sm + Sh::kOffPre);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int g = lane >> 2, t = lane & 3;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::kOffBar) + warp * S;
   int* bad_s = reinterpret_cast<int*>(sm + Sh::kOffBad) + warp * S;
   uint8_t* ring = sm + warp * Sh::kRing;
+  if (threadIdx.x == 0) abort_flag = 0;
+
+  // the work in front of each lane's requests: every warp for itself
+  uint64_t before = 0, all;
+  {
+    uint64_t mine = 0;
+    bool bad = false;
+    Item it;
+    it.b = static_cast<int64_t>(lane) * p.per_lane;
+    const int64_t b1 = it.b + p.per_lane < p.a.B ? it.b + p.per_lane : p.a.B;
+    for (; it.b < b1; ++it.b) {
+      request<NT>(p, it, &bad);
+      mine += count(p, it);
+    }
+    if (bad && blockIdx.x == 0 && warp == 0) atomicOr(p.a.err, kErrBadCache);
+    before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t x = __shfl_up_sync(kFull, before, o);
+      if (lane >= o) before += x;
+    }
+    all = __shfl_sync(kFull, before, 31);
+    before -= mine;
+  }
   if (lane == 0) {
     for (int i = 0; i < S; ++i) mbar_init(&bars[i], 1);
     fence_barrier_init();
   }
-  if (threadIdx.x == 0) abort_flag = 0;
+  // equal runs: a block's, and of that a warp's; the longer ones are spread over the blocks
+  const uint64_t q = __umul64hi(all, p.by_grid);
+  const uint32_t r = static_cast<uint32_t>(all - q * gridDim.x);
+  const uint32_t r0 = static_cast<uint32_t>(__umul64hi(r * blockIdx.x, p.by_grid));
+  const uint32_t r1 = static_cast<uint32_t>(__umul64hi(r * (blockIdx.x + 1), p.by_grid));
+  const uint64_t block0 = q * blockIdx.x + r0, run = q + r1 - r0;
+  const uint64_t per = (run + Sh::kWarps - 1) / Sh::kWarps, skip = static_cast<uint64_t>(warp) * per;
+  const uint64_t from = block0 + skip;
+  const int n = skip >= run ? 0 : static_cast<int>(run - skip < per ? run - skip : per);
+  __syncwarp();
 
-  // the work of the requests in front of each thread's
-  {
-    uint64_t mine = 0;
-    bool bad = false;
-    const int64_t b0 = static_cast<int64_t>(threadIdx.x) * p.per_thread;
-    for (int64_t b = b0; b < b0 + p.per_thread && b < p.a.B; ++b) mine += count(p, request<NT>(p, b, &bad));
-    if (bad && blockIdx.x == 0) atomicOr(p.a.err, kErrBadCache);
-    uint64_t sum = mine;
+  Item* item = reinterpret_cast<Item*>(sm + Sh::kOffItem) + warp;  // the current one
+  int tile = 0, tiles = 0, len = 0;
+  // its queries as they are loaded: row g (+ 8 x), channels 32 b + 8 t ..
+  auto load_queries = [&](const Item& it, uint4 (&qv)[NT][NB]) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t x = __shfl_up_sync(kFull, sum, o);
-      if (lane >= o) sum += x;
+    for (int x = 0; x < NT; ++x) {
+      int query;
+      int64_t head;
+      const bool on = row_at<NT>(p, it.lq, it.h, it.group, g + 8 * x, &query, &head);
+      const uint16_t* row = p.a.q + (it.q0 + query) * p.a.st[0] + head * p.a.st[1] + 8 * t;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        qv[x][b] = on ? *reinterpret_cast<const uint4*>(row + 32 * b) : make_uint4(0u, 0u, 0u, 0u);
     }
-    if (lane == 31) warp_sum[warp] = sum;
-    __syncthreads();
-    uint64_t front = 0;
-    for (int w = 0; w < warp; ++w) front += warp_sum[w];
-    pre[threadIdx.x] = front + sum - mine;
-    if (threadIdx.x == kThreads - 1) pre[kThreads] = front + sum;
-    __syncthreads();
+  };
+  if (n > 0) {
+    Item it;
+    tile = place<NT>(p, before, from, it);
+    if (lane == 0) *item = it;
+    __syncwarp();
   }
-  const uint64_t all = pre[kThreads];
-  const uint64_t block0 = all * blockIdx.x / gridDim.x, block1 = all * (blockIdx.x + 1) / gridDim.x;
-  const uint64_t per = (block1 - block0 + Sh::kWarps - 1) / Sh::kWarps;
-  const uint64_t from = block0 + warp * per < block1 ? block0 + warp * per : block1;
-  const int n = static_cast<int>((from + per < block1 ? from + per : block1) - from);
 
-  // loads: lane l finds the source of every 32nd tile and starts its copy
+  // loads: lane l finds the source of every 32nd tile, from the current item on, and starts its copy
   const uint8_t* src = nullptr;
-  auto fill = [&](int i) {
-    if (i >= n) return;
+  bool load = false;  // there is such a tile
+  auto fill = [&](int i, int ahead) {  // ahead: tiles between the current one and the i-th
     if ((i & 31) == 0) {
+      Item it = *item;
+      int x = tile + ahead + lane;
+      while (x >= it.tiles && it.start + it.tiles + 2 * kExtra < n) {
+        x -= it.tiles;
+        next_item<NT>(p, it);
+      }
       src = nullptr;
-      if (i + lane < n) {
-        const Place w = place<D, NT>(p, pre, from + i + lane);
-        const uint32_t tpp = static_cast<uint32_t>(p.a.page / 32), page_at = w.tile / tpp;
-        const int64_t page = w.r.len > 0 ? p.a.block_table[w.b * p.a.width + page_at] : -1;
+      load = x < it.tiles && it.start + kExtra + x < n;
+      if (load && it.len > 0) {
+        const uint32_t tpp = static_cast<uint32_t>(p.a.page) / 32, page_at = static_cast<uint32_t>(x) / tpp;
+        const int64_t page = p.a.block_table[it.b * p.a.width + page_at];
         if (page >= 0 && page < p.a.pages)
-          src = p.a.cache + page * p.a.page_stride + (static_cast<int64_t>(w.h) * tpp + (w.tile - page_at * tpp)) * Tile::kBytes;
-        else if (w.r.len > 0)
+          src = p.a.cache + page * p.a.page_stride +
+                (static_cast<int64_t>(it.h) * tpp + (static_cast<uint32_t>(x) - page_at * tpp)) * Tile::kBytes;
+        else
           atomicOr(p.a.err, kErrBadCache);
       }
+      __syncwarp();
     }
-    if (lane == (i & 31)) {
+    if (load && lane == (i & 31)) {
       const int st = i % S;
       bad_s[st] = src == nullptr;
       if (src != nullptr) {
@@ -255,31 +312,26 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
       }
     }
   };
-  for (int i = 0; i < S; ++i) fill(i);
 
-  Place w = {};
-  uint32_t qa[NB][2][2 * NT];  // queries as A operands: block, product, (row g, row g + 8) x (nibbles 0 / 2, 1 / 3)
-  float qsum[NT][NB];          // -8 2^-133 sum of a block's queries
-  float f[NT];                 // scores in units of log2
-  int lim[NT], lim0 = 0;       // keys that a lane's row sees; the first row
-  float ref[NT], l[NT];
+  uint32_t qb[NT][NB][2][2];   // queries as B operands: block, product, (nibbles 0 / 2, 1 / 3) with (4 / 6, 5 / 7)
+  float2 qsum[NT][NB];         // -8 2^-133 sum of a block's queries, rows 2 t and 2 t + 1
+  float f[NT][2];              // scores of these rows in units of log2
+  int lim[NT][2], lim0 = 0;    // keys that they see; that the first row sees
+  float ref[NT][2], l[NT][2];
   float o[NT][NB][2][4], bias[NT][4];
   uint32_t one[NB];            // -8 2^-133 in the rows of a block
 #pragma unroll
   for (int b = 0; b < NB; ++b) one[b] = g % NB == b ? 0x80088008u : 0u;
 
-  auto begin = [&]() {  // a new group of rows: w
+  auto begin = [&](const Item& it, const uint4 (&qv)[NT][NB]) {  // a new group of rows
+    tiles = it.tiles;
+    len = it.len;
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-      int64_t tok, head;
-      const bool on = row_at<NT>(p, w.r, w.h, w.group, g + 8 * x, &tok, &head);
-      const uint16_t* row = p.a.q + tok * p.a.st[0] + head * p.a.st[1] + 8 * t;
-      uint4 v[NB];
       float top = 0.0f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        v[b] = on ? *reinterpret_cast<const uint4*>(row + 32 * b) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t u[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+        const uint32_t u[4] = {qv[x][b].x, qv[x][b].y, qv[x][b].z, qv[x][b].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(u[e])), fabsf(bf16_hi(u[e]))));
       }
@@ -288,13 +340,23 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
       // 2^e at most the row's largest: times 2^(100 - e) (a row below 2^-27 keeps smaller values)
       const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -27);
       const float up = __uint_as_float(static_cast<uint32_t>(100 - e + 127) << 23);
-      f[x] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(33 + e, 127) + 127) << 23);
-      const int64_t seen = static_cast<int64_t>(w.r.len) - w.r.lq + (tok - w.r.q0) + 1;
-      lim[x] = on ? static_cast<int>(seen < 0 ? 0 : seen) : w.r.len;
-      if (x == 0) lim0 = __shfl_sync(kFull, lim[0], 0);
+      const float fg = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(33 + e, 127) + 127) << 23);
+      int query;
+      int64_t head;
+      const bool on = row_at<NT>(p, it.lq, it.h, it.group, g + 8 * x, &query, &head);
+      const int64_t seen = static_cast<int64_t>(it.len) - it.lq + query + 1;
+      const int lg = on ? static_cast<int>(seen < 0 ? 0 : seen) : it.len;
+      if (x == 0) lim0 = __shfl_sync(kFull, lg, 0);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        f[x][r] = __shfl_sync(kFull, fg, 8 * t + 4 * r);
+        lim[x][r] = __shfl_sync(kFull, lg, 8 * t + 4 * r);
+        ref[x][r] = kNone;
+        l[x][r] = 0.0f;
+      }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint32_t u[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+        const uint32_t u[4] = {qv[x][b].x, qv[x][b].y, qv[x][b].z, qv[x][b].w};
         float c[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -304,15 +366,14 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
         float sum = ((c[0] + c[1]) + (c[2] + c[3])) + ((c[4] + c[5]) + (c[6] + c[7]));
         sum += __shfl_xor_sync(kFull, sum, 1);
         sum += __shfl_xor_sync(kFull, sum, 2);
-        qsum[x][b] = sum * -1.1754943508222875e-38f * 0.0625f;  // -8 2^-133 = -2^-126 2^-4
+        sum *= -1.1754943508222875e-38f * 0.0625f;  // -8 2^-133 = -2^-126 2^-4
+        qsum[x][b] = make_float2(__shfl_sync(kFull, sum, 8 * t), __shfl_sync(kFull, sum, 8 * t + 4));
         // nibbles 1, 3 (and 5, 7) of a word are taken four bits higher, times 16
-        qa[b][0][x] = pack_bf16(c[0], c[4]);
-        qa[b][0][NT + x] = pack_bf16(c[1] * 0.0625f, c[5] * 0.0625f);
-        qa[b][1][x] = pack_bf16(c[2], c[6]);
-        qa[b][1][NT + x] = pack_bf16(c[3] * 0.0625f, c[7] * 0.0625f);
+        qb[x][b][0][0] = pack_bf16(c[0], c[4]);
+        qb[x][b][0][1] = pack_bf16(c[1] * 0.0625f, c[5] * 0.0625f);
+        qb[x][b][1][0] = pack_bf16(c[2], c[6]);
+        qb[x][b][1][1] = pack_bf16(c[3] * 0.0625f, c[7] * 0.0625f);
       }
-      ref[x] = kNone;
-      l[x] = 0.0f;
 #pragma unroll
       for (int e2 = 0; e2 < 4; ++e2) {
         bias[x][e2] = 0.0f;
@@ -322,110 +383,109 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     }
   };
 
-  auto work = [&](const uint8_t* tile, int key0, bool bad) {  // 32 keys from key0 on
-    float2 s[NT][4];  // scores of row g (+ 8 x) with keys 8 t + 2 j, + 1
+  const unsigned pick = (g & 1) != 0 ? 0x3244u : 0x1044u;  // the lane's token of a pair, as binary32
+  auto work = [&](const uint8_t* at0, int key0, bool bad) {  // 32 keys from key0 on
+    // scores: rows of a product are the keys 8 (g / 2) + 2 j + g % 2 of j = 2 jp (elements 0, 1) and
+    // 2 jp + 1 (2, 3), columns the rows 2 t, 2 t + 1 (+ 8 x)
+    float2 s[NT][2][2];
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[x][j] = make_float2(0.0f, 0.0f);
-    const uint8_t* keys = tile + lane * Tile::kWords * 4;
+      for (int jp = 0; jp < 2; ++jp) s[x][jp][0] = s[x][jp][1] = make_float2(0.0f, 0.0f);
+    const uint8_t* keys = at0 + lane * Tile::kWords * 4;
 #pragma unroll
     for (int bq = 0; bq < Tile::kQuads; ++bq) {
-      uint32_t sc[Tile::kWords][4];
 #pragma unroll
-      for (int bw = 0; bw < Tile::kWords; ++bw) {
-        const uint4 v = *reinterpret_cast<const uint4*>(tile + Tile::kKeyScales + (4 * bq + bw) * 64 + 16 * t);
-        sc[bw][0] = v.x; sc[bw][1] = v.y; sc[bw][2] = v.z; sc[bw][3] = v.w;
-      }
+      for (int jp = 0; jp < 2; ++jp) {
+        uint32_t kw[2][Tile::kWords];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t kw[Tile::kWords];
-        const uint8_t* at = keys + (j * Tile::kQuads + bq) * 128 * Tile::kWords;
-        if constexpr (Tile::kWords == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(at);
-          kw[0] = v.x; kw[1] = v.y; kw[2] = v.z; kw[3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(at);
-          kw[0] = v.x; kw[1] = v.y;
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* at = keys + ((2 * jp + i) * Tile::kQuads + bq) * 128 * Tile::kWords;
+          if constexpr (Tile::kWords == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(at);
+            kw[i][0] = v.x; kw[i][1] = v.y; kw[i][2] = v.z; kw[i][3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(at);
+            kw[i][0] = v.x; kw[i][1] = v.y;
+          }
         }
 #pragma unroll
         for (int bw = 0; bw < Tile::kWords; ++bw) {
           const int b = 4 * bq + bw;
-          const uint32_t lo = kw[bw], hi = kw[bw] >> 8;
-          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma_bf16(c, qa[b][0][0], NT == 2 ? qa[b][0][NT - 1] : 0u, qa[b][0][NT], NT == 2 ? qa[b][0][2 * NT - 1] : 0u,
-                   lo & 0x000F000Fu, lo & 0x00F000F0u);
-          mma_bf16(c, qa[b][1][0], NT == 2 ? qa[b][1][NT - 1] : 0u, qa[b][1][NT], NT == 2 ? qa[b][1][2 * NT - 1] : 0u,
-                   hi & 0x000F000Fu, hi & 0x00F000F0u);
-          const float2 sf = make_float2(bf16_lo(sc[bw][j]), bf16_hi(sc[bw][j]));
+          const uint2 sc = *reinterpret_cast<const uint2*>(at0 + Tile::kKeyScales + b * 64 + 16 * (g >> 1) + 8 * jp);
+          const float s0 = __uint_as_float(__byte_perm(sc.x, 0u, pick)), s1 = __uint_as_float(__byte_perm(sc.y, 0u, pick));
+          const uint32_t k0 = kw[0][bw], k1 = kw[1][bw], h0 = k0 >> 8, h1 = k1 >> 8;
 #pragma unroll
           for (int x = 0; x < NT; ++x) {
-            const float2 d = __fadd2_rn(make_float2(c[2 * x], c[2 * x + 1]), make_float2(qsum[x][b], qsum[x][b]));
-            s[x][j] = __ffma2_rn(d, sf, s[x][j]);
+            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma_bf16(c, k0 & 0x000F000Fu, k1 & 0x000F000Fu, k0 & 0x00F000F0u, k1 & 0x00F000F0u, qb[x][b][0][0], qb[x][b][0][1]);
+            mma_bf16(c, h0 & 0x000F000Fu, h1 & 0x000F000Fu, h0 & 0x00F000F0u, h1 & 0x00F000F0u, qb[x][b][1][0], qb[x][b][1][1]);
+            s[x][jp][0] = __ffma2_rn(__fadd2_rn(make_float2(c[0], c[1]), qsum[x][b]), make_float2(s0, s0), s[x][jp][0]);
+            s[x][jp][1] = __ffma2_rn(__fadd2_rn(make_float2(c[2], c[3]), qsum[x][b]), make_float2(s1, s1), s[x][jp][1]);
           }
         }
       }
     }
     // keys that a row does not see; values behind the last key may hold anything
     uint32_t keep[4] = {kFull, kFull, kFull, kFull};
-    const bool edge = bad || key0 + 32 > lim0;
-    if (edge) {
+    if (bad || key0 + 32 > lim0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int key = key0 + 8 * t + 2 * j;
+        const int key = key0 + 8 * (g >> 1) + 2 * j + (g & 1), pair = key0 + 8 * t + 2 * j;
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-          if (bad || key >= lim[x]) s[x][j].x = -INFINITY;
-          if (bad || key + 1 >= lim[x]) s[x][j].y = -INFINITY;
+          if (bad || key >= lim[x][0]) s[x][j >> 1][j & 1].x = -INFINITY;
+          if (bad || key >= lim[x][1]) s[x][j >> 1][j & 1].y = -INFINITY;
         }
-        if (bad || key >= w.r.len) keep[j] &= 0xFFFF0000u;
-        if (bad || key + 1 >= w.r.len) keep[j] &= 0x0000FFFFu;
+        if (bad || pair >= len) keep[j] &= 0xFFFF0000u;
+        if (bad || pair + 1 >= len) keep[j] &= 0x0000FFFFu;
       }
     }
     // the reference follows the largest score only when that has run ahead
-    float top[NT];
+    float top[NT][2];
     bool grow = false;
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-      top[x] = fmaxf(fmaxf(fmaxf(s[x][0].x, s[x][0].y), fmaxf(s[x][1].x, s[x][1].y)),
-                     fmaxf(fmaxf(s[x][2].x, s[x][2].y), fmaxf(s[x][3].x, s[x][3].y)));
-      grow = grow || fmaf(top[x], f[x], -ref[x]) > kLift + kSlack;
+      top[x][0] = fmaxf(fmaxf(s[x][0][0].x, s[x][0][1].x), fmaxf(s[x][1][0].x, s[x][1][1].x));
+      top[x][1] = fmaxf(fmaxf(s[x][0][0].y, s[x][0][1].y), fmaxf(s[x][1][0].y, s[x][1][1].y));
+#pragma unroll
+      for (int r = 0; r < 2; ++r) grow = grow || fmaf(top[x][r], f[x][r], -ref[x][r]) > kLift + kSlack;
     }
     if (__any_sync(kFull, grow)) {
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        float m = fmaxf(top[x], __shfl_xor_sync(kFull, top[x], 1));
-        m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-        m = fmaxf(ref[x], fmaf(m, f[x], -kLift));
-        const float by = ex2(ref[x] - m);
-        ref[x] = m;
-        l[x] *= by;
-        const float by0 = __shfl_sync(kFull, by, 8 * t), by1 = __shfl_sync(kFull, by, 8 * t + 4);  // rows 2 t, 2 t + 1
+      for (int x = 0; x < NT; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float y = (e & 1) != 0 ? by1 : by0;
-          bias[x][e] *= y;
+        for (int r = 0; r < 2; ++r) {
+          float m = top[x][r];
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            o[x][b][0][e] *= y;
-            o[x][b][1][e] *= y;
-          }
+          for (int i = 4; i < 32; i <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, i));
+          m = fmaxf(ref[x][r], fmaf(m, f[x][r], -kLift));
+          const float by = ex2(ref[x][r] - m);
+          ref[x][r] = m;
+          l[x][r] *= by;
+          bias[x][r] *= by;
+          bias[x][2 + r] *= by;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int m2 = 0; m2 < 2; ++m2) {
+              o[x][b][m2][r] *= by;
+              o[x][b][m2][2 + r] *= by;
+            }
         }
-      }
     }
-    uint32_t pw[NT][4];
+    uint32_t pw[NT][4];  // weights as B operands: row g (+ 8 x), keys 8 t + 2 j, + 1
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
-      float sum = 0.0f;
+    for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float a = ex2(fmaf(s[x][j].x, f[x], -ref[x])), b = ex2(fmaf(s[x][j].y, f[x], -ref[x]));
-        sum += a + b;
-        pw[x][j] = pack_bf16(a, b);
+        const float2 v = s[x][j >> 1][j & 1];
+        const float a = ex2(fmaf(v.x, f[x][0], -ref[x][0])), b = ex2(fmaf(v.y, f[x][1], -ref[x][1]));
+        l[x][0] += a;
+        l[x][1] += b;
+        pw[x][j] = transpose_8x8(pack_bf16(a, b));
       }
-      l[x] += sum;
-    }
-    const uint8_t* values = tile + Tile::kValues + lane * Tile::kHalves * 4;
+    const uint8_t* values = at0 + Tile::kValues + lane * Tile::kHalves * 4;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {  // 16 keys: the lane's pairs j = 2 k and 2 k + 1
       uint32_t v[4][Tile::kHalves];
@@ -444,10 +504,10 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint2 sc = *reinterpret_cast<const uint2*>(tile + Tile::kValueScales + b * 64 + 16 * t + 8 * k);
+        const uint2 sc = *reinterpret_cast<const uint2*>(at0 + Tile::kValueScales + b * 64 + 16 * t + 8 * k);
         const int h = b >> 1;
-        const unsigned pick = (b & 1) == 0 ? 0x5410u : 0x7632u;
-        const uint32_t u0 = __byte_perm(v[0][h], v[1][h], pick), u1 = __byte_perm(v[2][h], v[3][h], pick);
+        const unsigned half = (b & 1) == 0 ? 0x5410u : 0x7632u;
+        const uint32_t u0 = __byte_perm(v[0][h], v[1][h], half), u1 = __byte_perm(v[2][h], v[3][h], half);
         const uint32_t s0 = sc.x & keep[2 * k], s1 = sc.y & keep[2 * k + 1];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
@@ -461,8 +521,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     }
   };
 
-  constexpr float k2p69 = 5.902958103587057e20f, k2m64 = 5.421010862427522e-20f;
   // The lane's share of a finished run: columns 2 t and 2 t + 1 of the rows, channels 32 b + 4 g .. + 3
+  constexpr float k2p69 = 5.902958103587057e20f, k2m64 = 5.421010862427522e-20f;
   auto total = [&](int x, int b, int e, float (&v)[4]) {  // column 2 t + e; times 2^133
     const float c = __shfl_sync(kFull, bias[x][e], 4 * b + t);
     v[0] = o[x][b][0][e] + c;
@@ -470,185 +530,235 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     v[2] = o[x][b][1][e] + c;
     v[3] = fmaf(o[x][b][1][2 + e], 0.0625f, c);
   };
-  int4* meta_s = reinterpret_cast<int4*>(sm + Sh::kOffMeta);  // [warp][2]: put aside, at the end
-  // A run that is not a whole group of rows: to `part`, row by row o, reference and sum.
-  auto put_part = [&](float* part) {
+  auto row_sum = [&](int x, int e) {
+    float sum = l[x][e];
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v[4];
-          total(x, b, e, v);
-          *reinterpret_cast<float4*>(part + (8 * x + 2 * t + e) * Sh::kPad + 32 * b + 4 * g) =
-              make_float4(v[0] * k2p69, v[1] * k2p69, v[2] * k2p69, v[3] * k2p69);
-        }
-      float sum = l[x] + __shfl_xor_sync(kFull, l[x], 1);
-      sum += __shfl_xor_sync(kFull, sum, 2);
-      if (t == 0)
-        *reinterpret_cast<float2*>(part + (8 * x + g) * Sh::kPad + D) = make_float2(ref[x] + kLift, sum * k2m64);
-    }
+    for (int i = 4; i < 32; i <<= 1) sum += __shfl_xor_sync(kFull, sum, i);
+    return sum * k2m64;
   };
-  auto put_rows = [&]() {  // a whole group of rows: to o
+  Record* rec = reinterpret_cast<Record*>(sm + Sh::kOffRec);  // [warp][2]: put aside, at the end
+  // The end of a run: a whole group of rows goes to o, others to `part`, row by row o, reference and sum.
+  auto put = [&](float* part, bool rows) {
+    const Item it = *item;
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
-      float sum = l[x] + __shfl_xor_sync(kFull, l[x], 1);
-      sum = (sum + __shfl_xor_sync(kFull, sum, 2)) * k2m64;
-      const float inv = sum != 0.0f ? k2p69 / sum : 0.0f;
+    for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float by = __shfl_sync(kFull, inv, 4 * (2 * t + e));
-        int64_t tok, head;
-        const bool on = row_at<NT>(p, w.r, w.h, w.group, 8 * x + 2 * t + e, &tok, &head);
-        uint16_t* row = p.a.o + tok * p.a.st[2] + head * p.a.st[3] + 4 * g;
+        const int r = 8 * x + 2 * t + e;
+        const float sum = row_sum(x, e);
+        float by = k2p69;
+        if (rows) by = sum != 0.0f ? k2p69 / sum : 0.0f;
+        int query;
+        int64_t head;
+        const bool on = row_at<NT>(p, it.lq, it.h, it.group, r, &query, &head);
+        uint16_t* dst = p.a.o + (it.q0 + query) * p.a.st[2] + head * p.a.st[3] + 4 * g;
+        float* row = part + r * Sh::kPad;
+        if (!rows && g == 0) *reinterpret_cast<float2*>(row + D) = make_float2(ref[x][e] + kLift, sum);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           float v[4];
           total(x, b, e, v);
-          if (on) *reinterpret_cast<uint2*>(row + 32 * b) = make_uint2(pack_bf16(v[0] * by, v[1] * by), pack_bf16(v[2] * by, v[3] * by));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] *= by;
+          if (!rows) *reinterpret_cast<float4*>(row + 32 * b + 4 * g) = make_float4(v[0], v[1], v[2], v[3]);
+          else if (on) *reinterpret_cast<uint2*>(dst + 32 * b) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
         }
       }
-    }
   };
-  // a run that ends inside the warp's: it waits in global memory, as the ring is still in use
-  float* aside = p.part + (static_cast<int64_t>(gridDim.x) * 2 + static_cast<int64_t>(blockIdx.x) * Sh::kWarps) * Sh::kPart;
+  // a run that ends inside the warp's waits beside the ring, which is still in use
+  float* aside = reinterpret_cast<float*>(sm + Sh::kOffAside);
 
-  if (lane < 2) meta_s[2 * warp + lane] = make_int4(0, 0, 0, 0);
+  if (lane < 2) rec[2 * warp + lane].flags = 0;
   __syncwarp();
-  bool ok = true, front = false;
-  for (int i = 0; i < n; ++i) {
-    if (i == 0 || w.tile == w.r.tiles) {
-      w = place<D, NT>(p, pre, from + i);
-      front = w.tile != 0;
-      begin();
+  bool front = tile != 0, ok = true;  // the current run begins inside its item
+  bool more = n > 0 && item->start + kExtra + tile < n;
+  for (int i = 0, st = 0, ph = 0; more;) {
+    int end;
+    {
+      uint4 qv[NT][NB];
+      const Item it = *item;
+      load_queries(it, qv);
+      if (i == 0) {  // behind the queries, which would wait for them
+        for (int k = 0; k < S; ++k) fill(k, k);
+      }
+      begin(it, qv);
+      end = n - kExtra - it.start < tiles ? n - kExtra - it.start : tiles;
     }
-    const int st = i % S;
-    ok = warp_wait(&bars[st], static_cast<uint32_t>(i / S) & 1u, &abort_flag);
-    if (!ok) {
+    for (; tile < end; ++i) {
+      ok = warp_wait(&bars[st], static_cast<uint32_t>(ph), &abort_flag);
+      if (!ok) break;
+      work(ring + st * Tile::kBytes, tile * 32, bad_s[st] != 0);
+      __syncwarp();  // every lane has read the stage
+      fill(i + S, S);
+      if (++st == S) {
+        st = 0;
+        ph ^= 1;
+      }
+      ++tile;
+    }
+    if (!ok) {  // a copy did not come: report it, and wait for those still under way
       report_error(p.a.err, kErrWaitTimeout, &abort_flag);
-      for (int k = i; k < n && k < i + S; ++k) mbar_wait(&bars[k % S], static_cast<uint32_t>(k / S) & 1u, nullptr);
+      for (int k = i; k < i + S; ++k)
+        if ((k >> 5) < ((i + S - 1) >> 5) || __shfl_sync(kFull, load, k & 31)) mbar_wait(&bars[k % S], static_cast<uint32_t>(k / S) & 1u, nullptr);
       break;
     }
-    work(ring + st * Tile::kBytes, static_cast<int>(w.tile) * 32, bad_s[st] != 0);
-    __syncwarp();  // every lane has read the stage
-    fill(i + S);
-    ++w.tile;
-    const bool whole = w.tile == w.r.tiles, last = i == n - 1;
-    if (whole && !front) {
-      put_rows();
-    } else if (whole || last) {
-      put_part(last ? reinterpret_cast<float*>(ring) : aside + static_cast<int64_t>(warp) * Sh::kPart);
-      if (lane == 0)
-        meta_s[2 * warp + (last ? 1 : 0)] =
-            make_int4(static_cast<int>(w.b), static_cast<int>(w.h), static_cast<int>(w.group),
-                      kPartHeld | (front ? kPartFromFront : 0) | (whole ? 0 : kPartGoesOn));
+    Item it = *item;
+    const bool whole = tile == tiles, rows = whole && !front;
+    more = whole && it.start + tiles + 2 * kExtra < n;
+    put(more ? aside + warp * Sh::kPart : reinterpret_cast<float*>(ring), rows);
+    if (!rows && lane == 0)
+      rec[2 * warp + (more ? 0 : 1)] = {it.h, it.group, it.lq,
+                                        kPartHeld | (front ? kPartFromFront : 0) | (whole ? 0 : kPartGoesOn), it.q0};
+    if (more) {
+      next_item<NT>(p, it);
+      __syncwarp();  // every lane has read the old one
+      if (lane == 0) *item = it;
+      __syncwarp();
+      tile = 0;
+      front = false;
     }
   }
   __syncthreads();
   if (abort_flag != 0) return;
 
-  // The block's chains: a run at a warp's end, those of the warps behind it while it goes on.
-  int4 out0 = make_int4(0, 0, 0, 0), out1 = out0;
-  auto join = [&](int w0, int n_end, bool tail) {  // the runs at the end of warps w0 .. w0 + n_end - 1, then one put aside
-    const int4 head = n_end > 0 ? meta_s[2 * w0 + 1] : meta_s[2 * w0];
-    const int v = w0 + n_end;
-    const int4 end = tail ? meta_s[2 * v] : meta_s[2 * (v - 1) + 1];
-    const bool from_front = (head.w & kPartFromFront) != 0, goes_on = (end.w & kPartGoesOn) != 0;
-    const int4 who = make_int4(head.x, head.y, head.z, kPartHeld | (from_front ? kPartFromFront : 0) | (goes_on ? kPartGoesOn : 0));
-    if (from_front) out0 = who;
-    else if (goes_on) out1 = who;
-    bool bad = false;
-    Request r = {};
-    if (!from_front && !goes_on) r = request<NT>(p, head.x, &bad);
-    const int members = n_end + (tail ? 1 : 0);
-    auto member = [&](int m) -> const float* {
-      return m < n_end ? reinterpret_cast<const float*>(sm + (w0 + m) * Sh::kRing) : aside + static_cast<int64_t>(v) * Sh::kPart;
-    };
-    for (int at = static_cast<int>(threadIdx.x); at < Sh::kRows * (D / 2); at += kThreads) {
-      const int row = at / (D / 2), c = 2 * (at - row * (D / 2));
-      float top = kNone;
-      for (int m = 0; m < members; ++m) top = fmaxf(top, member(m)[row * Sh::kPad + D]);
-      float sum = 0.0f;
-      float2 acc = make_float2(0.0f, 0.0f);
+  // The block's chains: a run at a warp's end and those of the warps behind it while it goes on, in the
+  // end one put aside.  A warp takes one row of a chain at a time.
+  Record out[2];
+  out[0].flags = out[1].flags = 0;
+  const int fa = lane < Sh::kWarps ? rec[2 * lane].flags : 0, fe = lane < Sh::kWarps ? rec[2 * lane + 1].flags : 0;
+  const unsigned asides = __ballot_sync(kFull, fa != 0), ends = __ballot_sync(kFull, fe != 0);
+  const unsigned fronts = __ballot_sync(kFull, (fe & kPartFromFront) != 0), onward = __ballot_sync(kFull, (fe & kPartGoesOn) != 0);
+  const unsigned stops = ~onward | asides >> 1 | ~((asides | ends) >> 1);  // the chain's last run at a warp's end
+  int task = 0;
+#pragma unroll 1
+  for (unsigned todo = (ends & (~fronts | 1u)) << 1 | (asides & 1u); todo != 0; todo &= todo - 1) {
+    constexpr int E = D / 32;
+    const int w1 = __ffs(todo) - 1, w0 = w1 > 0 ? w1 - 1 : 0;  // 0: the run that warp 0 put aside, alone
+    const int n_end = w1 > 0 ? __ffs(stops >> w0) : 0;         // warps whose runs at the end belong to it
+    const bool tail = w1 == 0 || ((onward >> (w0 + n_end - 1) & 1u) != 0 && (asides >> (w0 + n_end) & 1u) != 0);
+    Record who = rec[w1 > 0 ? 2 * w0 + 1 : 0];
+    const int end = tail ? 0 : rec[2 * (w0 + n_end - 1) + 1].flags;  // what is put aside does not go on
+    const int v = w0 + n_end, members = n_end + (tail ? 1 : 0);
+    const bool from_front = (who.flags & kPartFromFront) != 0, goes_on = (end & kPartGoesOn) != 0;
+    who.flags = kPartHeld | (from_front ? kPartFromFront : 0) | (goes_on ? kPartGoesOn : 0);
+    if (from_front) out[0] = who;
+    else if (goes_on) out[1] = who;
+#pragma unroll 1
+    for (int row = (warp + Sh::kWarps - task % Sh::kWarps) % Sh::kWarps; row < Sh::kRows; row += Sh::kWarps) {
+      auto member = [&](int m) {
+        return reinterpret_cast<const float*>(m < n_end ? sm + (w0 + m) * Sh::kRing : sm + Sh::kOffAside + v * Sh::kPart * 4) + row * Sh::kPad;
+      };
+      const float2 ml = lane < members ? *reinterpret_cast<const float2*>(member(lane) + D) : make_float2(kNone, 0.0f);
+      float top = ml.x, acc[E] = {};
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
+      const float by = ex2(ml.x - top);
+      float sum = ml.y * by;
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(kFull, sum, i);
+#pragma unroll 4
       for (int m = 0; m < members; ++m) {
-        const float* src2 = member(m) + row * Sh::kPad;
-        const float2 ml = *reinterpret_cast<const float2*>(src2 + D), v2 = *reinterpret_cast<const float2*>(src2 + c);
-        const float by = ex2(ml.x - top);
-        sum = fmaf(ml.y, by, sum);
-        acc.x = fmaf(v2.x, by, acc.x);
-        acc.y = fmaf(v2.y, by, acc.y);
+        const float* from_m = member(m) + E * lane;
+        const float by_m = __shfl_sync(kFull, by, m);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(from_m + e);
+          acc[e] = fmaf(x.x, by_m, acc[e]);
+          acc[e + 1] = fmaf(x.y, by_m, acc[e + 1]);
+        }
       }
       if (from_front || goes_on) {
         float* dst = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (from_front ? 0 : 1)) * Sh::kPart + row * Sh::kPad;
-        *reinterpret_cast<float2*>(dst + c) = acc;
-        if (c == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(top, sum);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(dst + E * lane + e) = make_float2(acc[e], acc[e + 1]);
+        if (lane == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(top, sum);
       } else {
-        int64_t tok, hd;
-        if (row_at<NT>(p, r, static_cast<uint32_t>(head.y), static_cast<uint32_t>(head.z), row, &tok, &hd)) {
+        int query;
+        int64_t head;
+        if (row_at<NT>(p, who.lq, who.h, who.group, row, &query, &head)) {
           const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-          *reinterpret_cast<uint32_t*>(p.a.o + tok * p.a.st[2] + hd * p.a.st[3] + c) = pack_bf16(acc.x * inv, acc.y * inv);
+          uint32_t* dst = reinterpret_cast<uint32_t*>(p.a.o + (who.q0 + query) * p.a.st[2] + head * p.a.st[3] + E * lane);
+#pragma unroll
+          for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
         }
       }
     }
-  };
-  if (meta_s[0].w != 0) join(0, 0, true);
-  for (int w0 = 0; w0 < Sh::kWarps; ++w0) {
-    const int fl = meta_s[2 * w0 + 1].w;
-    if (fl == 0 || (w0 > 0 && (fl & kPartFromFront) != 0)) continue;
-    int n_end = 1;
-    bool tail = false, on = (fl & kPartGoesOn) != 0;
-    while (on && w0 + n_end < Sh::kWarps) {
-      if (meta_s[2 * (w0 + n_end)].w != 0) {
-        tail = true;
-        break;
-      }
-      const int nx = meta_s[2 * (w0 + n_end) + 1].w;
-      if (nx == 0) break;  // the block's last warps have no work: the run goes on in the next block
-      ++n_end;
-      on = (nx & kPartGoesOn) != 0;
-    }
-    join(w0, n_end, tail);
+    task += Sh::kRows;
   }
   if (threadIdx.x == 0) {
-    p.meta[2 * blockIdx.x] = out0;
-    p.meta[2 * blockIdx.x + 1] = out1;
+    p.meta[2 * blockIdx.x] = out[0];
+    p.meta[2 * blockIdx.x + 1] = out[1];
   }
 }
 
-// Runs that cross blocks: block x joins the one that begins in block x of the attention kernel, row y.
+// Runs that cross blocks: block x joins the one that begins in block x of the attention kernel, row
+// y.  Its members are found by all lanes at once, and each warp adds every fourth: their loads do
+// not wait for one another.
+constexpr int kJoinWarps = 4;
 template <int D, int NT>
-__global__ void __launch_bounds__(D / 2) kv4_join_kernel(const __grid_constant__ Kv4Params p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const __grid_constant__ Kv4Params p) {
   using Sh = Kv4Shape<D, NT>;
+  constexpr int E = D / 32;
+  __shared__ int slots[kMaxBlocks];
+  __shared__ float2 ml_s[kMaxBlocks];
+  __shared__ float acc_s[kJoinWarps][D];
+  __shared__ float sum_s[kJoinWarps];
   pdl_wait();
-  const int4 who = p.meta[2 * blockIdx.x + 1];
-  if ((who.w & kPartHeld) == 0) return;
-  bool bad;
-  const Request r = request<NT>(p, who.x, &bad);
-  const int row = static_cast<int>(blockIdx.y), c = 2 * static_cast<int>(threadIdx.x);
-  int64_t tok, head;
-  if (!row_at<NT>(p, r, static_cast<uint32_t>(who.y), static_cast<uint32_t>(who.z), row, &tok, &head)) return;
-  const int nb = static_cast<int>(gridDim.x);
-  float top = kNone, sum = 0.0f;
-  float2 acc = make_float2(0.0f, 0.0f);
-  auto add = [&](int slot) {
-    const float* src = p.part + static_cast<int64_t>(slot) * Sh::kPart + row * Sh::kPad;
-    const float2 ml = *reinterpret_cast<const float2*>(src + D), v = *reinterpret_cast<const float2*>(src + c);
-    const float m = fmaxf(top, ml.x), old = ex2(top - m), by = ex2(ml.x - m);
-    top = m;
-    sum = fmaf(sum, old, ml.y * by);
-    acc.x = fmaf(acc.x, old, v.x * by);
-    acc.y = fmaf(acc.y, old, v.y * by);
-  };
-  add(2 * static_cast<int>(blockIdx.x) + 1);
-  for (int x = static_cast<int>(blockIdx.x) + 1; x < nb; ++x) {
-    const int flags = p.meta[2 * x].w;
-    if (flags == 0) continue;  // a block without work
-    add(2 * x);
-    if ((flags & kPartGoesOn) == 0) break;
+  const int x = static_cast<int>(blockIdx.x), nb = static_cast<int>(gridDim.x), row = static_cast<int>(blockIdx.y);
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const Record who = p.meta[2 * x + 1];
+  if (who.flags == 0) return;
+  int query;
+  int64_t head;
+  if (!row_at<NT>(p, who.lq, who.h, who.group, row, &query, &head)) return;
+  int n = 1;  // members
+  bool open = true;
+  for (int b0 = x + 1; b0 < nb && open; b0 += 32) {
+    const int flags = b0 + lane < nb ? p.meta[2 * (b0 + lane)].flags : 0;  // 0: a block without work
+    const unsigned held = __ballot_sync(kFull, flags != 0), ends = __ballot_sync(kFull, flags != 0 && (flags & kPartGoesOn) == 0);
+    const unsigned mine = ends != 0 ? held & (ends ^ (ends - 1)) : held;  // up to the first that ends
+    if (((mine >> lane) & 1u) != 0 && warp == 0) slots[n + __popc(mine & ((1u << lane) - 1))] = 2 * (b0 + lane);
+    n += __popc(mine);
+    open = ends == 0;
   }
-  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-  *reinterpret_cast<uint32_t*>(p.a.o + tok * p.a.st[2] + head * p.a.st[3] + c) = pack_bf16(acc.x * inv, acc.y * inv);
+  if (threadIdx.x == 0) slots[0] = 2 * x + 1;
+  __syncthreads();
+  for (int m = static_cast<int>(threadIdx.x); m < n; m += 32 * kJoinWarps)
+    ml_s[m] = *reinterpret_cast<const float2*>(p.part + static_cast<int64_t>(slots[m]) * Sh::kPart + row * Sh::kPad + D);
+  __syncthreads();
+  float top = kNone;
+  for (int m = lane; m < n; m += 32) top = fmaxf(top, ml_s[m].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+  float sum = 0.0f, acc[E] = {};
+#pragma unroll 4
+  for (int m = warp; m < n; m += kJoinWarps) {
+    const float* src = p.part + static_cast<int64_t>(slots[m]) * Sh::kPart + row * Sh::kPad + E * lane;
+    const float2 ml = ml_s[m];
+    const float by = ex2(ml.x - top);
+    sum = fmaf(ml.y, by, sum);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(src + e);
+      acc[e] = fmaf(v.x, by, acc[e]);
+      acc[e + 1] = fmaf(v.y, by, acc[e + 1]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc_s[warp][E * lane + e] = acc[e];
+  if (lane == 0) sum_s[warp] = sum;
+  __syncthreads();
+  for (int c = 2 * static_cast<int>(threadIdx.x); c < D; c += 64 * kJoinWarps) {
+    float t = 0.0f, u = 0.0f, v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      t += sum_s[w];
+      u += acc_s[w][c];
+      v += acc_s[w][c + 1];
+    }
+    const float inv = t != 0.0f ? 1.0f / t : 0.0f;
+    *reinterpret_cast<uint32_t*>(p.a.o + (who.q0 + query) * p.a.st[2] + head * p.a.st[3] + c) = pack_bf16(u * inv, v * inv);
+  }
 }
 
 // ---- host ------------------------------------------------------------------------------------
@@ -656,11 +766,13 @@ __global__ void __launch_bounds__(D / 2) kv4_join_kernel(const __grid_constant__
 // not fit the registers).
 int row_tiles(int64_t G, bool one_query, int64_t d) { return d == 256 || (one_query && G <= 8) ? 1 : 2; }
 
+int grid_blocks(const DeviceInfo& dev) { return std::min(dev.sm_count, kMaxBlocks); }
+
 template <int D, int NT>
 size_t ws_bytes(const DeviceInfo& dev) {
   using Sh = Kv4Shape<D, NT>;
-  const size_t blocks = static_cast<size_t>(dev.sm_count);
-  return blocks * (2 + Sh::kWarps) * Sh::kPart * 4 + blocks * 2 * sizeof(int4);
+  const size_t blocks = static_cast<size_t>(grid_blocks(dev));
+  return blocks * 2 * (Sh::kPart * 4 + sizeof(Record));
 }
 
 template <int D, int NT>
@@ -670,10 +782,12 @@ cudaError_t attention(const Kv4AttentionArgs& a, const DeviceInfo& dev, cudaStre
   p.a = a;
   p.G = static_cast<int>(a.H / a.Hkv);
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  p.per_thread = static_cast<int>((a.B + Sh::kThreads - 1) / Sh::kThreads);
-  const unsigned blocks = static_cast<unsigned>(dev.sm_count);
+  p.per_lane = static_cast<int>((a.B + 31) / 32);
+  p.by_G = ~uint64_t{0} / static_cast<uint64_t>(p.G) + 1;  // unused for 1
+  p.by_grid = ~uint64_t{0} / static_cast<uint64_t>(grid_blocks(dev)) + 1;
+  const unsigned blocks = static_cast<unsigned>(grid_blocks(dev));
   p.part = static_cast<float*>(a.part);
-  p.meta = reinterpret_cast<int4*>(p.part + static_cast<size_t>(blocks) * (2 + Sh::kWarps) * Sh::kPart);
+  p.meta = reinterpret_cast<Record*>(p.part + static_cast<size_t>(blocks) * 2 * Sh::kPart);
   const auto kernel = kv4_attention_kernel<D, NT>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), Sh::kSmem, dev.device);
   if (e != cudaSuccess) return e;
@@ -681,7 +795,7 @@ cudaError_t attention(const Kv4AttentionArgs& a, const DeviceInfo& dev, cudaStre
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, Sh::kRows);
-  cfg.blockDim = dim3(D / 2);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
