@@ -396,13 +396,14 @@ q8_status q8_kv4_gather(const uint8_t* cache, int64_t page_stride, int64_t pages
  * Scores and sums are binary32; a weight, and its product with a value's scale, are each rounded to
  * bfloat16; o is rounded once.  The order of all sums is fixed by the lengths.
  * workspace: at least q8_kv4_attention_workspace_size() bytes, 16-byte aligned (one_query: cu_q is
- * NULL).  Calls that overlap in time need one each.  Never allocates.
+ * NULL; NULL where that size is 0).  Calls that overlap in time need one each.  Never allocates.
  */
 q8_status q8_kv4_attention(const uint16_t* q, const uint8_t* cache, int64_t page_stride, int64_t pages, int64_t page,
                            const int32_t* block_table, int64_t width, const int32_t* kv_len, const int32_t* cu_q,
                            uint16_t* o, int64_t B, int64_t Tq, int64_t H, int64_t Hkv, int64_t d, float scale,
                            const int64_t* strides, void* workspace, size_t workspace_bytes, cudaStream_t stream);
-size_t q8_kv4_attention_workspace_size(int64_t H, int64_t Hkv, int64_t d, int one_query);
+size_t q8_kv4_attention_workspace_size(int64_t B, int64_t width, int64_t page, int64_t H, int64_t Hkv, int64_t d,
+                                       int one_query);
 
 /*
  * Prepared weights for the tensor-core path.  The tensor path feeds the MMA binary16

@@ -108,7 +108,7 @@ def _load():
     for name in ("q8_prompt_attention_workspace_size", "q8_prefix_attention_workspace_size"):
         getattr(L, name).argtypes = [i64] * 6
         getattr(L, name).restype = sz
-    L.q8_kv4_attention_workspace_size.argtypes = [i64, i64, i64, i32]
+    L.q8_kv4_attention_workspace_size.argtypes = [i64] * 6 + [i32]
     L.q8_kv4_attention_workspace_size.restype = sz
     L.q8_device_error.argtypes = [ctypes.POINTER(i32)]
     L.q8_device_error.restype = ctypes.c_uint32
@@ -572,31 +572,35 @@ def q8_kv4_cache_shape(pages, page, Hkv, d):
     return pages, Hkv, page // KV4_TILE, 36 * d
 
 
-def _kv4_cache(cache, Hkv, d, dev):
-    """(page stride in bytes, pages, page): cache is a uint8 tensor of q8_kv4_cache_shape on CUDA device
-    dev whose pages are contiguous (but may lie apart from one another)."""
+def _kv4_cache(cache, d, dev):
+    """(page stride in bytes, pages, page, Hkv): cache is a uint8 tensor of q8_kv4_cache_shape on CUDA
+    device dev whose pages are contiguous (but may lie apart from one another)."""
     if cache.dtype is not torch.uint8:
         raise TypeError(f"cache: expected torch.uint8, got {cache.dtype}")
-    if cache.dim() != 4 or cache.shape[1] != Hkv or cache.shape[3] != 36 * d:
-        raise ValueError(f"cache: expected shape (pages, {Hkv}, page/32, {36 * d}), got {tuple(cache.shape)}")
+    shape = cache.shape
+    if len(shape) != 4 or shape[3] != 36 * d:
+        raise ValueError(f"cache: expected shape (pages, Hkv, page/32, {36 * d}), got {tuple(shape)}")
     if cache.get_device() != dev:
         raise ValueError(f"cache: must be a CUDA tensor on the current device (cuda:{dev})")
-    pages, _, tiles, size = cache.shape
+    pages, Hkv, tiles, size = shape
+    if cache.is_contiguous():
+        return Hkv * tiles * size, pages, KV4_TILE * tiles, Hkv
     st = cache.stride()
     if (st[3] != 1 and size > 1) or (st[2] != size and tiles > 1) or (st[1] != tiles * size and Hkv > 1):
         raise ValueError("cache: the bytes of a page must be contiguous")
-    return (st[0] if pages > 1 else Hkv * tiles * size), pages, KV4_TILE * tiles
+    return (st[0] if pages > 1 else Hkv * tiles * size), pages, KV4_TILE * tiles, Hkv
 
 
 def _block_table(block_table, B, dev):
     """(address, width) of a contiguous int32 [B, width] on CUDA device dev."""
+    shape = block_table.shape
     if block_table.dtype is not torch.int32:
         raise TypeError(f"block_table: expected torch.int32, got {block_table.dtype}")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table: expected shape ({B}, width), got {tuple(block_table.shape)}")
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"block_table: expected shape ({B}, width), got {tuple(shape)}")
     if block_table.get_device() != dev or not block_table.is_contiguous():
         raise ValueError(f"block_table: must be a contiguous CUDA tensor on the current device (cuda:{dev})")
-    return block_table.data_ptr(), block_table.shape[1]
+    return block_table.data_ptr(), shape[1]
 
 
 def q8_rope_table(positions, inv_freq, axis=None, table=None, stream=None):
@@ -667,7 +671,9 @@ def q8_kv4_append(k, v, cache, slots, table=None, q=None, q_weight=None, k_weigh
         if table.get_device() != dev or not table.is_contiguous():
             raise ValueError(f"table: must be a contiguous CUDA tensor on the current device (cuda:{dev})")
         rot, pt = 2 * table.shape[2], table.data_ptr()
-    page_stride, pages, page = _kv4_cache(cache, Hkv, d, dev)
+    page_stride, pages, page, heads = _kv4_cache(cache, d, dev)
+    if heads != Hkv:
+        raise ValueError(f"cache: expected {Hkv} key/value heads, got {heads}")
     status = _L.q8_kv4_append(
         pq, k.data_ptr(), v.data_ptr(), xtype, _STRIDES4(sq[0], sk[0], sv[0], sqo[0]),
         None if q_weight is None else _vector("q_weight", q_weight, f32, d, dev),
@@ -686,10 +692,8 @@ def q8_kv4_gather(cache, block_table, cu, tokens, first=None, out_dtype=torch.bf
     dev = torch.cuda.current_device()
     if out_dtype not in DTYPES:
         raise TypeError(f"out_dtype: expected bfloat16 or float32, got {out_dtype}")
-    if cache.dim() != 4:
-        raise ValueError(f"cache: expected shape (pages, Hkv, page/32, 36 d), got {tuple(cache.shape)}")
-    Hkv, d = cache.shape[1], cache.shape[3] // 36
-    page_stride, pages, page = _kv4_cache(cache, Hkv, d, dev)
+    d = cache.shape[-1] // 36
+    page_stride, pages, page, Hkv = _kv4_cache(cache, d, dev)
     n = cu.numel()
     if n < 1:
         raise ValueError("cu: expected at least one entry")
@@ -713,8 +717,8 @@ def q8_kv4_gather(cache, block_table, cu, tokens, first=None, out_dtype=torch.bf
     return out[0], out[1]
 
 
-def q8_kv4_attention_workspace_size(H, Hkv, d, one_query=True) -> int:
-    return int(_L.q8_kv4_attention_workspace_size(H, Hkv, d, 1 if one_query else 0))
+def q8_kv4_attention_workspace_size(B, width, page, H, Hkv, d, one_query=True) -> int:
+    return int(_L.q8_kv4_attention_workspace_size(B, width, page, H, Hkv, d, 1 if one_query else 0))
 
 
 def q8_kv4_attention(q, cache, block_table, kv_len, cu_q=None, scale=None, o=None, workspace=None, stream=None):
@@ -727,8 +731,7 @@ def q8_kv4_attention(q, cache, block_table, kv_len, cu_q=None, scale=None, o=Non
     dev = torch.cuda.current_device()
     Tq, H, d = q.shape
     sq = _heads("q", q, torch.bfloat16, (Tq, H, d), dev)
-    Hkv = cache.shape[1] if cache.dim() == 4 else 0
-    page_stride, pages, page = _kv4_cache(cache, Hkv, d, dev)
+    page_stride, pages, page, Hkv = _kv4_cache(cache, d, dev)
     B = Tq if cu_q is None else cu_q.numel() - 1
     if B < 0:
         raise ValueError("cu_q: expected at least one entry")
@@ -740,7 +743,8 @@ def q8_kv4_attention(q, cache, block_table, kv_len, cu_q=None, scale=None, o=Non
     else:
         so = _heads("o", o, torch.bfloat16, (Tq, H, d), dev)
     workspace, pw, nbytes = _workspace(
-        workspace, _L.q8_kv4_attention_workspace_size(H, Hkv, d, 1 if cu_q is None else 0), q.device, dev, stream)
+        workspace, _L.q8_kv4_attention_workspace_size(B, width, page, H, Hkv, d, 1 if cu_q is None else 0), q.device, dev,
+        stream)
     status = _L.q8_kv4_attention(
         q.data_ptr(), cache.data_ptr(), page_stride, pages, page, pb, width, pn, pc, o.data_ptr(), B, Tq, H, Hkv, d,
         (d or 1) ** -0.5 if scale is None else scale, _STRIDES4(sq[0], sq[1], so[0], so[1]), pw, nbytes,

@@ -764,9 +764,6 @@ q8_status q8_kv4_attention(const uint16_t* q, const uint8_t* cache, int64_t page
   DeviceInfo dev;
   if ((st = current_device(&dev)) != Q8_OK) return st;
   if (!any) return Q8_OK;
-  const size_t need = kv4_attention_ws_bytes(H, Hkv, d, cu_q == nullptr, dev);
-  if (workspace == nullptr) return Q8_ERR_NULL;
-  if (workspace_bytes < need) return Q8_ERR_NOMEM;
   a.q = q;
   a.cache = cache;
   a.page_stride = page_stride;
@@ -784,14 +781,29 @@ q8_status q8_kv4_attention(const uint16_t* q, const uint8_t* cache, int64_t page
   a.d = d;
   a.scale = scale;
   a.part = workspace;
+  const size_t need = kv4_attention_ws_bytes(a, dev);
+  if (need > 0 && workspace == nullptr) return Q8_ERR_NULL;
+  if (workspace_bytes < need) return Q8_ERR_NOMEM;
   return launch_status(launch_kv4_attention(a, dev, stream));
 }
 
-size_t q8_kv4_attention_workspace_size(int64_t H, int64_t Hkv, int64_t d, int one_query) {
-  if (H <= 0 || Hkv <= 0 || H > kSizeLimit || H % Hkv != 0 || H / Hkv > 128 || (d != 64 && d != 128 && d != 256)) return 0;
+size_t q8_kv4_attention_workspace_size(int64_t B, int64_t width, int64_t page, int64_t H, int64_t Hkv, int64_t d,
+                                       int one_query) {
+  if (B <= 0 || B >= kSizeLimit || H <= 0 || Hkv <= 0 || H > kSizeLimit || H % Hkv != 0 || H / Hkv > 128 ||
+      (d != 64 && d != 128 && d != 256) || page < 32 || page % 32 != 0 || !table_ok(B, width, page))
+    return 0;
   DeviceInfo dev;
   if (current_device(&dev) != Q8_OK) return 0;
-  return kv4_attention_ws_bytes(H, Hkv, d, one_query != 0, dev);
+  Kv4AttentionArgs a = {};
+  static const int32_t some = 0;
+  a.B = B;
+  a.width = width;
+  a.page = page;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.cu_q = one_query != 0 ? nullptr : &some;  // only looked at
+  return kv4_attention_ws_bytes(a, dev);
 }
 
 q8_status q8_kv3_encode(const void* x, q8_dtype xtype, uint32_t* codes, float* scales,

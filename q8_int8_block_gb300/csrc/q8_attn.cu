@@ -44,11 +44,6 @@ __device__ __forceinline__ bool sequence_ok(const PromptArgs& a, int64_t s) {
   return bounds_ok(a, a.cu_q[s], a.cu_q[s + 1], a.cu_k[s], a.cu_k[s + 1]);
 }
 
-__device__ __forceinline__ void pdl_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ---- the tile kernel ---------------------------------------------------------------------
 // The rows of a tile are the G heads of 128 / G neighbouring tokens: the heads that share a
 // key/value head are rows of the same products, so K and V are read once for all of them and
@@ -87,11 +82,6 @@ constexpr int kTileThreads = 32 * (kSoftWarps + 2);  // and one warp for the loa
 // a barrier counts arrivals, not warps, so its arrival at the end must not be able to stand in
 // for a warp that is still on its way to the start.
 constexpr int kStartBar = 11;
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 
 constexpr float kRescaleLog2 = 8.0f;  // move the exponent reference when a row's maximum gains > 2^8
 
@@ -1067,18 +1057,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// The block cluster: a barrier of all its threads, and a value in the shared memory of CTA `rank`.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float peer_load(const float* own, int rank) {
-  uint32_t at;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(own)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
-}
-
 template <int D, bool kAlone>
 __global__ void __launch_bounds__(32 * kOwnWarps, 3) attn_own_kernel(const __grid_constant__ OwnParams p) {
   using Sh = OwnShape<D>;

@@ -206,8 +206,8 @@ cudaError_t launch_rope_table(const int32_t* positions, int axes, const double* 
                               float* table, int64_t T, int half, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_kv4_append(Kv4AppendArgs a, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_kv4_gather(Kv4GatherArgs a, const DeviceInfo& dev, cudaStream_t stream);
-// one_query: the call has no cu_q, every request one query
-size_t kv4_attention_ws_bytes(int64_t H, int64_t Hkv, int64_t d, bool one_query, const DeviceInfo& dev);
+// by B, width, page, H, Hkv, d and whether cu_q is nullptr
+size_t kv4_attention_ws_bytes(const Kv4AttentionArgs& a, const DeviceInfo& dev);
 cudaError_t launch_kv4_attention(Kv4AttentionArgs a, const DeviceInfo& dev, cudaStream_t stream);
 
 // ---- q8_gemm.cu -------------------------------------------------------------------

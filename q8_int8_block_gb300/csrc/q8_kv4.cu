@@ -74,12 +74,21 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const TableParams p) {
 }
 
 // ---- append ----------------------------------------------------------------------------------
+#ifndef KVRB
+#define KVRB 2
+#endif
+#ifndef KVMINB
+#define KVMINB 7
+#endif
+#ifndef KVRF
+#define KVRF 2
+#endif
 constexpr int kAppendThreads = 128;
 
 struct AppendParams {
   Kv4AppendArgs a;
-  int nq, nk;         // warp rounds of query heads, of key (and of value) heads
-  int parts, per;     // warps of a token, rounds of a warp
+  int nq, nk;         // warp rounds of a token's query heads, of its key (and of its value) heads
+  int pq, parts;      // warps of its query heads, of all
   float inv_d;
 };
 
@@ -107,135 +116,265 @@ struct Eight {  // 8 channels as they are loaded
   }
 };
 
+__device__ __forceinline__ void store8(uint16_t* out, const float (&v)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+// 16 neighbours (a, then b) <-> their even ones (a) and odd ones (b)
+__device__ __forceinline__ void split_pairs(float (&a)[8], float (&b)[8]) {
+  const float x[16] = {a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], b[0], b[1], b[2], b[3], b[4], b[5], b[6], b[7]};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = x[2 * i];
+    b[i] = x[2 * i + 1];
+  }
+}
+__device__ __forceinline__ void join_pairs(float (&a)[8], float (&b)[8]) {
+  const float x[16] = {a[0], b[0], a[1], b[1], a[2], b[2], a[3], b[3], a[4], b[4], a[5], b[5], a[6], b[6], a[7], b[7]};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = x[i];
+    b[i] = x[8 + i];
+  }
+}
 __device__ __forceinline__ void load8(const float* s, float (&v)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(s)), b = __ldg(reinterpret_cast<const float4*>(s) + 1);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-template <int D, bool kF32, bool kInterleaved>
-__global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const __grid_constant__ AppendParams p) {
+constexpr uint32_t codes_offset() {
+  uint32_t w = 0;
+  for (int e = 0; e < 8; ++e) w = w * 16u + 0x4B400000u;
+  return 0u - w;
+}
+constexpr uint32_t kCodes = codes_offset();
+
+// The queries of a part: d / 16 lanes a head, each with two chunks of 8 channels whose channels pair
+// up, so that pair i = (a, b) needs nothing from another lane.  Norm weight and rotation are one
+// 2 x 2 matrix a pair, formed once for all heads.
+template <int D, bool kF32, bool kInterleaved, int kRounds>
+__device__ __forceinline__ void append_queries(const AppendParams& p, uint32_t t, int part, int lane) {
+  constexpr int L = D / 16, kTeams = 32 / L;
+  const Kv4AppendArgs& a = p.a;
+  const int c = lane % L, team = lane / L;
+  const bool turns = 16 * c < a.rot;
+  const int ca = !kInterleaved && turns ? c : 2 * c, cb = !kInterleaved && turns ? c + a.rot / 16 : 2 * c + 1;
+  const int heads = static_cast<int>(a.H), h0 = part * kRounds * kTeams + team;
+  Eight<kF32> xa[kRounds], xb[kRounds];
+  {
+    const int64_t at = t * a.st[0];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int h = h0 + i * kTeams;
+      if (h < heads) {
+        xa[i].load(a.q, at + static_cast<int64_t>(h) * D + 8 * ca);
+        xb[i].load(a.q, at + static_cast<int64_t>(h) * D + 8 * cb);
+      }
+    }
+  }
+  // (a, b) -> (a aa + b ab, a ba + b bb)
+  float aa[8], ab[8], ba[8], bb[8];
+  {
+    float wa[8], wb[8], cs[8], sn[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wa[i] = wb[i] = cs[i] = 1.0f, sn[i] = 0.0f;
+    if (a.q_weight != nullptr) {
+      load8(a.q_weight + 8 * ca, wa);
+      load8(a.q_weight + 8 * cb, wb);
+      if constexpr (kInterleaved) split_pairs(wa, wb);
+    }
+    if (turns) {
+      const float* row = a.table + static_cast<int64_t>(t) * a.rot + 8 * c;
+      load8(row, cs);
+      load8(row + a.rot / 2, sn);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      aa[i] = wa[i] * cs[i];
+      ab[i] = -wb[i] * sn[i];
+      ba[i] = wa[i] * sn[i];
+      bb[i] = wb[i] * cs[i];
+    }
+  }
+  uint16_t* out = a.q_out + t * a.st[3];
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    if (part * kRounds + i >= p.nq) break;
+    const int h = h0 + i * kTeams;
+    float za[8] = {}, zb[8] = {};
+    if (h < heads) {
+      xa[i].unpack(za);
+      xb[i].unpack(zb);
+    }
+    if constexpr (kInterleaved) split_pairs(za, zb);
+    float f = 1.0f;
+    if (a.q_weight != nullptr) {
+      float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float2 u = make_float2(za[e], za[e + 1]), v = make_float2(zb[e], zb[e + 1]);
+        s2 = __ffma2_rn(u, u, __ffma2_rn(v, v, s2));
+      }
+      float ss = s2.x + s2.y;
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+      f = rsqrtf(fmaf(ss, p.inv_d, a.eps));
+    }
+    float oa[8], ob[8];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const float2 f2 = make_float2(f, f);
+      const float2 u = __fmul2_rn(make_float2(za[e], za[e + 1]), f2), v = __fmul2_rn(make_float2(zb[e], zb[e + 1]), f2);
+      const float2 x = __ffma2_rn(u, make_float2(aa[e], aa[e + 1]), __fmul2_rn(v, make_float2(ab[e], ab[e + 1])));
+      const float2 y = __ffma2_rn(u, make_float2(ba[e], ba[e + 1]), __fmul2_rn(v, make_float2(bb[e], bb[e + 1])));
+      oa[e] = x.x; oa[e + 1] = x.y;
+      ob[e] = y.x; ob[e + 1] = y.y;
+    }
+    if constexpr (kInterleaved) join_pairs(oa, ob);
+    if (h < heads) {
+      store8(out + static_cast<int64_t>(h) * D + 8 * ca, oa);
+      store8(out + static_cast<int64_t>(h) * D + 8 * cb, ob);
+    }
+  }
+}
+
+// The keys or values of a part: d / 8 lanes a head, a chunk of 8 channels each.  kRounds: rounds of a
+// warp, all loaded before the first is worked on.
+template <int D, bool kF32, bool kInterleaved, int kRounds>
+__global__ void __launch_bounds__(kAppendThreads, KVMINB) kv4_append_kernel(const __grid_constant__ AppendParams p) {
   using Tile = Kv4Tile<D>;
   constexpr int L = D / 8, kTeams = 32 / L;  // lanes of a head, heads of a round
   const Kv4AppendArgs& a = p.a;
   const int lane = static_cast<int>(threadIdx.x & 31), c = lane % L, team = lane / L;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = unit / p.parts;
+  const uint32_t unit = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t t = unit / static_cast<uint32_t>(p.parts);
   if (t >= a.T) return;
-  const int total = p.nq + 2 * p.nk;
-  const int r0 = static_cast<int>(unit - t * p.parts) * p.per, r1 = r0 + p.per < total ? r0 + p.per : total;
-  if (r0 >= r1) return;
+  // the part's kind (0 query, 1 key, 2 value) and first round
+  int part = static_cast<int>(unit - t * p.parts);
+  const int pk = (p.parts - p.pq) / 2, kind = part < p.pq ? 0 : part < p.pq + pk ? 1 : 2;
+  part -= kind == 0 ? 0 : kind == 1 ? p.pq : p.pq + pk;
+  if (kind == 0) {
+    append_queries<D, kF32, kInterleaved, kRounds>(p, t, part, lane);
+    return;
+  }
+  const int r0 = part * kRounds, rounds = p.nk - r0, heads = static_cast<int>(a.Hkv);
 
-  // round r: its kind (0 query, 1 key, 2 value) and this lane's head
-  auto kind_of = [&](int r) { return r < p.nq ? 0 : r < p.nq + p.nk ? 1 : 2; };
-  auto head_of = [&](int r, int kind) { return (kind == 0 ? r : kind == 1 ? r - p.nq : r - p.nq - p.nk) * kTeams + team; };
-  Eight<kF32> x;
-  auto load = [&](int r) {
-    const int kind = kind_of(r), h = head_of(r, kind);
-    if (h < (kind == 0 ? a.H : a.Hkv))
-      x.load(kind == 0 ? a.q : kind == 1 ? a.k : a.v, t * a.st[kind] + static_cast<int64_t>(h) * D + 8 * c);
-  };
-  load(r0);
-
+  Eight<kF32> x[kRounds];
+  {
+    const void* from = kind == 1 ? a.k : a.v;
+    const int64_t at = t * a.st[kind] + 8 * c;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int h = (r0 + i) * kTeams + team;
+      if (h < heads) x[i].load(from, at + static_cast<int64_t>(h) * D);
+    }
+  }
   // the lane's rotation: halves (the chunk's eight pairs) or neighbours (its four pairs)
   const bool turns = 8 * c < a.rot, upper = !kInterleaved && 16 * c >= a.rot;
   const int half = a.rot / 2, other = a.rot / 16;
   const int partner = !kInterleaved && turns ? lane + (upper ? -other : other) : lane;
-  float cs[8] = {}, sn[8] = {};
-  if (turns) {
-    const float* row = a.table + t * 2 * half;
-    if constexpr (kInterleaved) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(row + 4 * c));
-      const float4 w = __ldg(reinterpret_cast<const float4*>(row + half + 4 * c));
-      cs[0] = u.x; cs[1] = u.y; cs[2] = u.z; cs[3] = u.w;
-      sn[0] = w.x; sn[1] = w.y; sn[2] = w.z; sn[3] = w.w;
-    } else {
-      load8(row + 8 * (upper ? c - other : c), cs);
-      load8(row + half + 8 * (upper ? c - other : c), sn);
+  float cs[8], sn[8], wv[8];  // no rotation: 1 and 0
+  const float* w = kind == 1 ? a.k_weight : nullptr;
+  if (kind == 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cs[i] = 1.0f;
+      sn[i] = 0.0f;
     }
-  }
-  // the token's place: its tile of head 0
-  const int64_t slot = a.slots[t];
-  const int64_t page = slot / a.page;
-  const int in_page = static_cast<int>(slot - page * a.page), tok = in_page & 31;
-  const bool keep = slot >= 0 && page < a.pages;
-  uint8_t* tile0 = a.cache + (keep ? page : 0) * a.page_stride + static_cast<int64_t>(in_page >> 5) * Tile::kBytes;
-  const int64_t head_bytes = a.page / 32 * Tile::kBytes;
-  if (slot >= 0 && !keep && lane == 0 && r0 == 0) atomicOr(a.err, kErrBadCache);
-
-  for (int r = r0; r < r1; ++r) {
-    const int kind = kind_of(r), h = head_of(r, kind);
-    const bool on = h < (kind == 0 ? a.H : a.Hkv);
-    float z[8] = {};
-    if (on) x.unpack(z);
-    if (r + 1 < r1) load(r + 1);
-    float f = 1.0f;  // the norm's factor
-    if (kind < 2) {
-      const float* w = kind == 0 ? a.q_weight : a.k_weight;
-      if (w != nullptr) {
-        float ss = 0.0f, wv[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(z[i], z[i], ss);
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-        f = rsqrtf(fmaf(ss, p.inv_d, a.eps));
-        load8(w + 8 * c, wv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = __fmul_rn(z[i], wv[i]);
-      }
-      // products and sums rounded one by one: the codes are then the same wherever they are formed
+    if (turns) {
+      const float* row = a.table + static_cast<int64_t>(t) * 2 * half;
       if constexpr (kInterleaved) {
-        if (turns) {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(row + 4 * c));
+        const float4 v = __ldg(reinterpret_cast<const float4*>(row + half + 4 * c));
+        cs[0] = u.x; cs[1] = u.y; cs[2] = u.z; cs[3] = u.w;
+        sn[0] = v.x; sn[1] = v.y; sn[2] = v.z; sn[3] = v.w;
+      } else {
+        load8(row + 8 * (upper ? c - other : c), cs);
+        load8(row + half + 8 * (upper ? c - other : c), sn);
+        if (!upper) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float u = z[2 * i], v = z[2 * i + 1];
-            z[2 * i] = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(v, sn[i]));
-            z[2 * i + 1] = __fadd_rn(__fmul_rn(u, sn[i]), __fmul_rn(v, cs[i]));
-          }
-        }
-      } else if (a.rot > 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = __shfl_sync(kFull, z[i], partner);
-          if (turns) {
-            const float u = __fmul_rn(z[i], cs[i]), v = __fmul_rn(o, sn[i]);
-            z[i] = upper ? __fadd_rn(v, u) : __fsub_rn(u, v);
-          }
+          for (int i = 0; i < 8; ++i) sn[i] = -sn[i];  // exact: a cos - b sin is a cos + b (-sin)
         }
       }
     }
-    if (kind == 0) {
-      if (on) {
-        uint32_t u[4];
+    if (w != nullptr) load8(w + 8 * c, wv);
+  }
+  // r and z = x w of a round, turned.  Products and sums are rounded one by one: the codes are then
+  // the same wherever they are formed.
+  auto normed = [&](float (&z)[8]) {
+    float f = 1.0f;
+    if (w != nullptr) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(z[i], z[i], ss);
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+      f = rsqrtf(fmaf(ss, p.inv_d, a.eps));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = __fmul_rn(z[i], wv[i]);
+    }
+    if constexpr (kInterleaved) {
+      if (turns) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(z[2 * i] * f, z[2 * i + 1] * f);
-          u[i] = *reinterpret_cast<const uint32_t*>(&b);
+          const float u = z[2 * i], v = z[2 * i + 1];
+          z[2 * i] = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(v, sn[i]));
+          z[2 * i + 1] = __fadd_rn(__fmul_rn(u, sn[i]), __fmul_rn(v, cs[i]));
         }
-        *reinterpret_cast<uint4*>(a.q_out + t * a.st[3] + static_cast<int64_t>(h) * D + 8 * c) = make_uint4(u[0], u[1], u[2], u[3]);
       }
-      continue;
+    } else if (a.rot > 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float o = __shfl_sync(kFull, z[i], partner);
+        z[i] = __fadd_rn(__fmul_rn(z[i], cs[i]), __fmul_rn(o, sn[i]));
+      }
     }
+    return f;
+  };
+
+  // the token's place: its tile of head 0
+  const int slot = a.slots[t];
+  const uint32_t page = static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page);  // behind the cache if slot < 0
+  const int in_page = static_cast<int>(static_cast<uint32_t>(slot) - page * static_cast<uint32_t>(a.page)), tok = in_page & 31;
+  const bool keep = slot >= 0 && page < a.pages;
+  if (slot >= 0 && !keep && lane == 0 && r0 == 0) atomicOr(a.err, kErrBadCache);
+  if (!keep) return;
+  const int64_t head_bytes = a.page / 32 * Tile::kBytes;
+  uint8_t* tile0 = a.cache + page * a.page_stride + static_cast<int64_t>(in_page >> 5) * Tile::kBytes;
+  const int b = c >> 2;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    if (i >= rounds) break;
+    const int h = (r0 + i) * kTeams + team;
+    const bool on = h < heads;
+    float z[8] = {}, f = 1.0f;
+    if (on) x[i].unpack(z);
+    if (kind == 1) f = normed(z);
     // the quantiser: lanes 4 b .. 4 b + 3 of a head hold block b
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(z[i]));
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(z[e]));
     top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
     top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
     const bool zero = top < kKv4Zero;
     const float inv = zero ? 0.0f : __fdiv_rn(7.0f, top);
     uint32_t word = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // 1.5 2^23 + 8 is even, so adding it rounds as rint does, and the code + 8 is in the low bits
-      const float m = __fadd_rn(__fmul_rn(z[i], inv), 12582920.0f);
-      word |= (__float_as_uint(m) & 15u) << (4 * i);
-    }
+    for (int e = 7; e >= 0; --e)
+      // 1.5 2^23 + 8 is even, so adding it rounds as rint does; its bits are 0x4B400000 + code + 8,
+      // and the first part of eight of them, each 16 times the next, is taken off at the end
+      word = word * 16u + __float_as_uint(__fadd_rn(__fmul_rn(z[e], inv), 12582920.0f));
+    word += kCodes;
     const __nv_bfloat16 sc = __float2bfloat16_rn(zero ? 0.0f : __fmul_rn(__fmul_rn(top, f), 1.0f / 7.0f));
-    uint8_t* tile = tile0 + static_cast<int64_t>(h) * head_bytes;
-    const int b = c >> 2;
+    uint8_t* tile = tile0 + h * head_bytes;
     if (kind == 1) {
-      if (on && keep) {
+      if (on) {
         *reinterpret_cast<uint32_t*>(tile + Tile::key_word(tok, c)) = word;
         if ((c & 3) == 0) *reinterpret_cast<__nv_bfloat16*>(tile + Tile::kKeyScales + Tile::scale(tok, b)) = sc;
       }
@@ -244,7 +383,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const __grid
       const uint32_t give = (b & 1) == 0 ? word >> 16 : word & 0xFFFFu;
       const uint32_t got = __shfl_xor_sync(kFull, give, 4);
       const uint32_t both = (b & 1) == 0 ? (word & 0xFFFFu) | got << 16 : got | (word & 0xFFFF0000u);
-      if (on && keep) {
+      if (on) {
         *reinterpret_cast<uint32_t*>(tile + Tile::value_word(tok, 2 * (c & 3) + (b & 1), b >> 1)) = both;
         if ((c & 3) == 0) *reinterpret_cast<__nv_bfloat16*>(tile + Tile::kValueScales + Tile::scale(tok, b)) = sc;
       }
@@ -253,130 +392,170 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const __grid
 }
 
 // ---- gather ----------------------------------------------------------------------------------
-constexpr int kGatherThreads = 256;
+constexpr int kGatherThreads = 128;
 
-struct GatherParams {
-  Kv4GatherArgs a;
-  int heads;  // of a block
-};
-
-template <int D, bool kBf16>
-__global__ void __launch_bounds__(kGatherThreads) kv4_gather_kernel(const __grid_constant__ GatherParams p) {
+// A warp takes 32 rows of one head, or (kFew) as many as its teams of d / 8 lanes copy at once, four
+// each.  Each lane finds one row's place in the cache.  Of 32 rows a team copies those at once that
+// are 8 tokens apart, as they share the sectors that their values lie in.
+template <int D, bool kBf16, bool kFew>
+__global__ void __launch_bounds__(kGatherThreads) kv4_gather_kernel(const __grid_constant__ Kv4GatherArgs a) {
   using Tile = Kv4Tile<D>;
-  constexpr int L = D / 8, kTeams = kGatherThreads / L;
-  const Kv4GatherArgs& a = p.a;
-  __shared__ const uint8_t* tile_s[32];  // of head 0; nullptr: no row
-  __shared__ int tok_s[32];
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 32;
-  if (threadIdx.x < 32) {
-    const int64_t row = row0 + threadIdx.x;
-    const uint8_t* tile = nullptr;
-    int tok = 0;
-    if (row < a.T) {
-      int64_t lo = 0, hi = a.B;  // the last sequence that begins at or in front of the row
+  constexpr int L = D / 8, kTeams = 32 / L, kAhead = 4, kRows = kFew ? kAhead * kTeams : 32;
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const uint32_t unit = blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t chunk = unit / static_cast<uint32_t>(a.Hkv);
+  const int h = static_cast<int>(unit - chunk * static_cast<uint32_t>(a.Hkv));
+  const int64_t row0 = static_cast<int64_t>(chunk) * kRows;
+  if (row0 >= a.T) return;
+  const uint8_t* mine = nullptr;  // the tile of row row0 + lane; nullptr: no row
+  int mine_tok = 0;
+  {
+    // the last sequence that begins at or in front of the first row: of 32 at a time
+    int64_t lo = 0, n = a.B;
+    while (n > 1) {
+      const int64_t step = (n + 31) / 32, at = static_cast<int64_t>(lane) * step;
+      const int in = __popc(__ballot_sync(kFull, at < n && a.cu[lo + at] <= row0));
+      if (in == 0) break;
+      lo += (in - 1) * step;
+      n = n - (in - 1) * step < step ? n - (in - 1) * step : step;
+    }
+    const int64_t row = row0 + lane;
+    // the lane's own: among the 32 behind it, or further on
+    const int64_t next = lo + 1 + lane < a.B ? a.cu[lo + 1 + lane] : a.T;
+    int ahead = 0;
+    if (__shfl_sync(kFull, next, 0) < row0 + kRows) {
+#pragma unroll 4
+      for (int i = 0; i < kRows; ++i) {
+        const int passed = __popc(__ballot_sync(kFull, next <= row0 + i));
+        ahead = lane == i ? passed : ahead;
+      }
+    }
+    lo += ahead;
+    if (ahead == 32) {
+      int64_t hi = a.B - 1;
       while (lo < hi) {
         const int64_t mid = (lo + hi + 1) >> 1;
-        if (mid < a.B && a.cu[mid] <= row) lo = mid;
+        if (a.cu[mid] <= row) lo = mid;
         else hi = mid - 1;
       }
+    }
+    if (lane < kRows && row < a.T) {
       const int64_t begin = a.cu[lo];
       if (begin <= row && row < a.cu[lo + 1]) {
         const int64_t pos = (a.first != nullptr ? a.first[lo] : 0) + (row - begin);
-        const int64_t at = pos >= 0 ? pos / a.page : a.width;
-        const int64_t page = at < a.width ? a.block_table[lo * a.width + at] : -1;
+        int64_t page = -1;
+        int in_page = 0;
+        if (pos >= 0 && pos < a.width * a.page) {  // below 2^31
+          const uint32_t at = static_cast<uint32_t>(pos) / static_cast<uint32_t>(a.page);
+          in_page = static_cast<int>(static_cast<uint32_t>(pos) - at * static_cast<uint32_t>(a.page));
+          page = a.block_table[lo * a.width + at];
+        }
         if (page >= 0 && page < a.pages) {
-          const int in_page = static_cast<int>(pos - at * a.page);
-          tok = in_page & 31;
-          tile = a.cache + page * a.page_stride + static_cast<int64_t>(in_page >> 5) * Tile::kBytes;
-        } else {
+          mine_tok = in_page & 31;
+          mine = a.cache + page * a.page_stride +
+                 (static_cast<int64_t>(h) * (a.page / 32) + (in_page >> 5)) * Tile::kBytes;
+        } else if (h == 0) {
           atomicOr(a.err, kErrBadCache);
         }
       }
     }
-    tile_s[threadIdx.x] = tile;
-    tok_s[threadIdx.x] = tok;
   }
-  __syncthreads();
-  const int lane = static_cast<int>(threadIdx.x & 31), c = lane % L, b = c >> 2, u = c & 3;
-  const int h0 = static_cast<int>(blockIdx.y) * p.heads, nh = a.Hkv - h0 < p.heads ? static_cast<int>(a.Hkv - h0) : p.heads;
-  const int64_t head_bytes = a.page / 32 * Tile::kBytes;
-  for (int i = static_cast<int>(threadIdx.x) / L; i < 32 * nh; i += kTeams) {  // 32 nh is a multiple of a warp's teams
-    const int r = i & 31, h = h0 + (i >> 5), tok = tok_s[r];
-    const uint8_t* tile = tile_s[r];
-    const bool on = tile != nullptr;
-    tile += on ? h * head_bytes : 0;
-    uint32_t kw = 0, vw = 0, ks = 0, vs = 0;
-    if (on) {
-      kw = __ldg(reinterpret_cast<const uint32_t*>(tile + Tile::key_word(tok, c)));
-      vw = __ldg(reinterpret_cast<const uint32_t*>(tile + Tile::value_word(tok, 2 * u + (b & 1), b >> 1)));
-      ks = __ldg(reinterpret_cast<const uint16_t*>(tile + Tile::kKeyScales + Tile::scale(tok, b)));
-      vs = __ldg(reinterpret_cast<const uint16_t*>(tile + Tile::kValueScales + Tile::scale(tok, b)));
-    }
-    const uint32_t got = __shfl_xor_sync(kFull, (b & 1) == 0 ? vw >> 16 : vw & 0xFFFFu, 4);
-    vw = (b & 1) == 0 ? (vw & 0xFFFFu) | got << 16 : got | (vw & 0xFFFF0000u);
-    if (!on) continue;
-    const int64_t at = ((row0 + r) * a.Hkv + h) * D + 8 * c;
-    auto put = [&](void* out, uint32_t w, uint32_t s16) {
-      const float s = __uint_as_float(s16 << 16);
-      float v[8];  // exact: 4 bits times 8
+  __syncwarp();
+  const int c = lane % L, team = lane / L, b = c >> 2, u = c & 3;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(static_cast<int>((w >> (4 * e)) & 15u) - 8) * s;
-      if constexpr (kBf16) {
-        uint32_t o[4];
+  for (int i = 0; i < kRows / (kAhead * kTeams); ++i) {
+    uint32_t kw[kAhead], vw[kAhead], ks[kAhead], vs[kAhead];
+    bool on[kAhead];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-          o[e] = *reinterpret_cast<const uint32_t*>(&x);
-        }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        float4* f = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-        f[0] = make_float4(v[0], v[1], v[2], v[3]);
-        f[1] = make_float4(v[4], v[5], v[6], v[7]);
+    for (int e = 0; e < kAhead; ++e) {
+      const int r = i * kTeams + team + (kFew ? kTeams : 8) * e;
+      const uint8_t* tile = reinterpret_cast<const uint8_t*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(mine), r));
+      const int tok = __shfl_sync(kFull, mine_tok, r);
+      on[e] = tile != nullptr;
+      kw[e] = vw[e] = ks[e] = vs[e] = 0;
+      if (on[e]) {
+        kw[e] = __ldg(reinterpret_cast<const uint32_t*>(tile + Tile::key_word(tok, c)));
+        vw[e] = __ldg(reinterpret_cast<const uint32_t*>(tile + Tile::value_word(tok, 2 * u + (b & 1), b >> 1)));
+        ks[e] = __ldg(reinterpret_cast<const uint16_t*>(tile + Tile::kKeyScales + Tile::scale(tok, b)));
+        vs[e] = __ldg(reinterpret_cast<const uint16_t*>(tile + Tile::kValueScales + Tile::scale(tok, b)));
       }
-    };
-    put(a.k, kw, ks);
-    put(a.v, vw, vs);
+    }
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const uint32_t got = __shfl_xor_sync(kFull, (b & 1) == 0 ? vw[e] >> 16 : vw[e] & 0xFFFFu, 4);
+      const uint32_t both = (b & 1) == 0 ? (vw[e] & 0xFFFFu) | got << 16 : got | (vw[e] & 0xFFFF0000u);
+      if (!on[e]) continue;
+      const int64_t at = ((row0 + i * kTeams + team + (kFew ? kTeams : 8) * e) * a.Hkv + h) * D + 8 * c;
+      auto put = [&](void* out, uint32_t w, uint32_t s16) {
+        if constexpr (kBf16) {
+          // pairs of nibbles (j, j + 4) as 128 + n, less 136 (exact), times the scale (rounded once)
+          const uint32_t s2 = s16 | s16 << 16;
+          uint32_t y[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t n = ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u, m = 0xC308C308u;  // -136
+            const __nv_bfloat162 z = __hmul2(__hadd2(*reinterpret_cast<const __nv_bfloat162*>(&n), *reinterpret_cast<const __nv_bfloat162*>(&m)),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&s2));
+            y[j] = *reinterpret_cast<const uint32_t*>(&z);
+          }
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
+              make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410), __byte_perm(y[0], y[1], 0x7632),
+                         __byte_perm(y[2], y[3], 0x7632));
+        } else {
+          const float s = __uint_as_float(s16 << 16);
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)  // 2^23 + n, less 2^23 + 8, times the scale: exact, 4 bits times 8
+            v[j] = (__uint_as_float(((w >> (4 * j)) & 15u) | 0x4B000000u) - 8388616.0f) * s;
+          float4* f = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+          f[0] = make_float4(v[0], v[1], v[2], v[3]);
+          f[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      };
+      put(a.k, kw[e], ks[e]);
+      put(a.v, both, vs[e]);
+    }
   }
 }
 
-template <int D, bool kF32>
-cudaError_t append_kernels(const AppendParams& p, bool interleaved, unsigned grid, cudaStream_t stream) {
-  if (interleaved) kv4_append_kernel<D, kF32, true><<<grid, kAppendThreads, 0, stream>>>(p);
-  else kv4_append_kernel<D, kF32, false><<<grid, kAppendThreads, 0, stream>>>(p);
+template <int D, bool kF32, int kRounds>
+cudaError_t append_rounds(AppendParams p, cudaStream_t stream) {
+  const Kv4AppendArgs& a = p.a;
+  p.pq = (p.nq + kRounds - 1) / kRounds;
+  p.parts = p.pq + 2 * ((p.nk + kRounds - 1) / kRounds);
+  const int64_t blocks = (a.T * p.parts + kAppendThreads / 32 - 1) / (kAppendThreads / 32);  // a unit fits 32 bits: T (H + 2 Hkv) does
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (a.interleaved) kv4_append_kernel<D, kF32, true, kRounds><<<grid, kAppendThreads, 0, stream>>>(p);
+  else kv4_append_kernel<D, kF32, false, kRounds><<<grid, kAppendThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool kF32>
 cudaError_t append(const Kv4AppendArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
   AppendParams p = {};
   p.a = a;
-  constexpr int kTeams = 32 / (D / 8);
-  p.nq = static_cast<int>((a.H + kTeams - 1) / kTeams);
+  constexpr int kTeams = 32 / (D / 8), kMost = kF32 ? KVRF : KVRB;
+  p.nq = static_cast<int>((a.H + 2 * kTeams - 1) / (2 * kTeams));
   p.nk = static_cast<int>((a.Hkv + kTeams - 1) / kTeams);
   p.inv_d = 1.0f / D;
-  const int64_t rounds = p.nq + 2 * p.nk;
-  const int64_t want = (static_cast<int64_t>(dev.sm_count) * 32 + a.T - 1) / a.T;
-  p.parts = static_cast<int>(std::max<int64_t>(1, std::min(want, rounds)));
-  p.per = static_cast<int>((rounds + p.parts - 1) / p.parts);
-  p.parts = static_cast<int>((rounds + p.per - 1) / p.per);
-  const int64_t blocks = (a.T * p.parts + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(blocks);
-  return a.f32 ? append_kernels<D, true>(p, a.interleaved, grid, stream) : append_kernels<D, false>(p, a.interleaved, grid, stream);
+  const int64_t rounds = a.T * (p.nq + 2 * p.nk), warps = static_cast<int64_t>(dev.sm_count) * 16;
+  return rounds >= warps * kMost ? append_rounds<D, kF32, kMost>(p, stream) : append_rounds<D, kF32, 1>(p, stream);
+}
+
+template <int D, bool kFew>
+cudaError_t gather_rows(const Kv4GatherArgs& a, cudaStream_t stream) {
+  constexpr int kRows = kFew ? 4 * 32 / (D / 8) : 32;
+  const int64_t units = (a.T + kRows - 1) / kRows * a.Hkv;  // T Hkv fits 31 bits
+  const unsigned grid = static_cast<unsigned>((units + kGatherThreads / 32 - 1) / (kGatherThreads / 32));
+  if (a.bf16) kv4_gather_kernel<D, true, kFew><<<grid, kGatherThreads, 0, stream>>>(a);
+  else kv4_gather_kernel<D, false, kFew><<<grid, kGatherThreads, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t gather(const Kv4GatherArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  GatherParams p = {};
-  p.a = a;
-  const int64_t chunks = (a.T + 31) / 32;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(a.Hkv, (static_cast<int64_t>(dev.sm_count) * 8 + chunks - 1) / chunks));
-  p.heads = static_cast<int>((a.Hkv + want - 1) / want);
-  const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>((a.Hkv + p.heads - 1) / p.heads));
-  if (a.bf16) kv4_gather_kernel<D, true><<<grid, kGatherThreads, 0, stream>>>(p);
-  else kv4_gather_kernel<D, false><<<grid, kGatherThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  // few rows a warp where 32 would not give every SM eight warps
+  return (a.T + 31) / 32 * a.Hkv < 8 * static_cast<int64_t>(dev.sm_count) ? gather_rows<D, true>(a, stream) : gather_rows<D, false>(a, stream);
 }
 
 }  // namespace
@@ -393,7 +572,8 @@ cudaError_t launch_rope_table(const int32_t* positions, int axes, const double* 
 cudaError_t launch_kv4_append(Kv4AppendArgs a, const DeviceInfo& dev, cudaStream_t stream) {
   if (a.T == 0 || a.H + a.Hkv == 0) return cudaSuccess;
   a.err = dev.err_word;
-  return a.d == 64 ? append<64>(a, dev, stream) : a.d == 128 ? append<128>(a, dev, stream) : append<256>(a, dev, stream);
+  if (a.f32) return a.d == 64 ? append<64, true>(a, dev, stream) : a.d == 128 ? append<128, true>(a, dev, stream) : append<256, true>(a, dev, stream);
+  return a.d == 64 ? append<64, false>(a, dev, stream) : a.d == 128 ? append<128, false>(a, dev, stream) : append<256, false>(a, dev, stream);
 }
 
 cudaError_t launch_kv4_gather(Kv4GatherArgs a, const DeviceInfo& dev, cudaStream_t stream) {

@@ -41,21 +41,12 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
-__device__ __forceinline__ void pdl_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                "{%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
 }
 __device__ __forceinline__ uint32_t mul_bf16(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
@@ -83,15 +74,19 @@ struct Kv4Params {
   int G;
   float scale_log2;
   int per_lane;      // requests whose counts a lane sums up
-  uint64_t by_grid, by_G;  // 2^64 / n + 1: the high half of x times it is x / n (x n < 2^64)
+  uint64_t by_G, by_tpp;  // 2^64 / n + 1 of the heads of a group and the tiles of a page: the high half
+                          // of x times it is x / n (x n < 2^64; not used for n = 1)
+  uint32_t by_grid;       // 2^32 / blocks
+  int cluster;       // (alone) blocks of a cluster
   float* part;       // [blocks][2] partial results
-  struct Record* meta;  // [blocks][2]
+  struct Record* meta;  // [blocks]: the run that begins in the block and goes on in others
 };
 constexpr int kMaxBlocks = 256;     // of the attention kernel
 enum : int { kPartHeld = 1, kPartFromFront = 2, kPartGoesOn = 4 };  // flags of a partial result
 struct __align__(16) Record {  // whose partial result it is
   int h, group, lq, flags;
   int64_t q0;
+  int64_t end;       // where its item ends in the work list; in memory: the last block that has some of it
 };
 
 // A group of rows of a request: the unit whose keys are walked.
@@ -168,6 +163,14 @@ __device__ __forceinline__ void next_item(const Kv4Params& p, Item& it) {
   } while (it.groups == 0 && it.b + 1 < p.a.B);
 }
 
+// x / y, quicker for x below 2^22 (the quotient in binary32 is then off by one at most)
+__device__ __forceinline__ uint32_t divide(uint32_t x, uint32_t y) {
+  if (x >> 22 != 0) return x / y;
+  const uint32_t z = static_cast<uint32_t>(__fdividef(static_cast<float>(x), static_cast<float>(y)));
+  const int rest = static_cast<int>(x - z * y);
+  return rest < 0 ? z - 1 : rest >= static_cast<int>(y) ? z + 1 : z;
+}
+
 // Place `at` of the work list, `before` the work in front of each lane's requests; returns the first
 // tile at or behind it.
 template <int NT>
@@ -184,10 +187,10 @@ __device__ __forceinline__ int place(const Kv4Params& p, uint64_t before, uint64
   }
   const uint32_t size = static_cast<uint32_t>(it.tiles + kExtra);
   uint64_t y;
-  if (rest >> 32 == 0) y = static_cast<uint32_t>(rest) / size;
+  if (rest >> 32 == 0) y = divide(static_cast<uint32_t>(rest), size);
   else y = rest / size;
   const uint32_t y32 = static_cast<uint32_t>(y);  // groups of a request: below 2^31
-  it.h = static_cast<int>(y32 / static_cast<uint32_t>(it.groups));
+  it.h = it.groups == 1 ? static_cast<int>(y32) : static_cast<int>(divide(y32, static_cast<uint32_t>(it.groups)));
   it.group = static_cast<int>(y32 - static_cast<uint32_t>(it.h) * static_cast<uint32_t>(it.groups));
   it.start = -static_cast<int>(rest - y * size);
   return it.start < -kExtra ? -it.start - kExtra : 0;
@@ -203,12 +206,41 @@ __device__ __forceinline__ bool row_at(const Kv4Params& p, int lq, int h, int gr
   return i < static_cast<uint32_t>(lq);
 }
 
-template <int D, int NT>
+// A row of `members` partial results, member(m) the m-th's: reference, sum, the lane's channels.
+template <int D, typename F>
+__device__ __forceinline__ void add_up(int lane, int members, const F& member, float& top, float& sum, float (&acc)[D / 32]) {
+  constexpr int E = D / 32;
+  const float2 ml = lane < members ? *reinterpret_cast<const float2*>(member(lane) + D) : make_float2(kNone, 0.0f);
+  top = ml.x;
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
+  const float by = ex2(ml.x - top);
+  sum = ml.y * by;
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(kFull, sum, i);
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+  for (int m = 0; m < members; ++m) {
+    const float* part = member(m) + E * lane;
+    const float by_m = __shfl_sync(kFull, by, m);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(part + e);
+      acc[e] = fmaf(x.x, by_m, acc[e]);
+      acc[e + 1] = fmaf(x.y, by_m, acc[e + 1]);
+    }
+  }
+}
+
+// kAlone: each group of rows is one cluster's, whose blocks share its keys and join through one
+// another's shared memory: one launch and no workspace.
+template <int D, int NT, bool kAlone>
 __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_kernel(const __grid_constant__ Kv4Params p) {
   using Sh = Kv4Shape<D, NT>;
   using Tile = Kv4Tile<D>;
   constexpr int NB = Tile::kBlocks, S = Sh::kStages;
-  pdl_launch_dependents();
+  if constexpr (!kAlone) pdl_launch_dependents();
   extern __shared__ __align__(16) uint8_t sm[];
   __shared__ int abort_flag;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
@@ -218,46 +250,96 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
   uint8_t* ring = sm + warp * Sh::kRing;
   if (threadIdx.x == 0) abort_flag = 0;
 
-  // the work in front of each lane's requests: every warp for itself
-  uint64_t before = 0, all;
-  {
-    uint64_t mine = 0;
-    bool bad = false;
-    Item it;
-    it.b = static_cast<int64_t>(lane) * p.per_lane;
-    const int64_t b1 = it.b + p.per_lane < p.a.B ? it.b + p.per_lane : p.a.B;
-    for (; it.b < b1; ++it.b) {
-      request<NT>(p, it, &bad);
-      mine += count(p, it);
-    }
-    if (bad && blockIdx.x == 0 && warp == 0) atomicOr(p.a.err, kErrBadCache);
-    before = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t x = __shfl_up_sync(kFull, before, o);
-      if (lane >= o) before += x;
-    }
-    all = __shfl_sync(kFull, before, 31);
-    before -= mine;
-  }
+  Item* item = reinterpret_cast<Item*>(sm + Sh::kOffItem) + warp;  // the current one
+  int tile = 0, tiles = 0, len = 0;
+  int n = 0;                            // places of the work list that are this warp's
+  uint64_t from = 0, q = 0, run = 0;    // the first of them; a block's places, this block's
+  uint32_t r = 0;
+  const uint32_t nb = gridDim.x;
+  auto share = [&](uint32_t block) { return __umulhi(r * block, p.by_grid + 1); };  // r block / blocks: 2^16 at most
+  int users = 0;                        // (alone) warps of this block that have keys
   if (lane == 0) {
     for (int i = 0; i < S; ++i) mbar_init(&bars[i], 1);
     fence_barrier_init();
   }
-  // equal runs: a block's, and of that a warp's; the longer ones are spread over the blocks
-  const uint64_t q = __umul64hi(all, p.by_grid);
-  const uint32_t r = static_cast<uint32_t>(all - q * gridDim.x);
-  const uint32_t r0 = static_cast<uint32_t>(__umul64hi(r * blockIdx.x, p.by_grid));
-  const uint32_t r1 = static_cast<uint32_t>(__umul64hi(r * (blockIdx.x + 1), p.by_grid));
-  const uint64_t block0 = q * blockIdx.x + r0, run = q + r1 - r0;
-  const uint64_t per = (run + Sh::kWarps - 1) / Sh::kWarps, skip = static_cast<uint64_t>(warp) * per;
-  const uint64_t from = block0 + skip;
-  const int n = skip >= run ? 0 : static_cast<int>(run - skip < per ? run - skip : per);
-  __syncwarp();
-
-  Item* item = reinterpret_cast<Item*>(sm + Sh::kOffItem) + warp;  // the current one
-  int tile = 0, tiles = 0, len = 0;
-  // its queries as they are loaded: row g (+ 8 x), channels 32 b + 8 t ..
+  if constexpr (kAlone) {
+    // equal runs of the group's tiles: a block's, and of that a warp's
+    const uint32_t c = static_cast<uint32_t>(p.cluster), x = blockIdx.x / c, rank = blockIdx.x - x * c;
+    Item it;
+    bool bad = false;
+    it.b = x / static_cast<uint32_t>(p.a.Hkv);
+    it.h = static_cast<int>(x - static_cast<uint32_t>(it.b) * static_cast<uint32_t>(p.a.Hkv));
+    it.group = 0;
+    request<NT>(p, it, &bad);
+    if (bad && threadIdx.x == 0) atomicOr(p.a.err, kErrBadCache);
+    const int per_block = (it.tiles + static_cast<int>(c) - 1) / static_cast<int>(c), block0 = static_cast<int>(rank) * per_block;
+    const int mine = it.tiles - block0 < per_block ? it.tiles - block0 : per_block;
+    const int per = mine > 0 ? (mine + Sh::kWarps - 1) / Sh::kWarps : 1;
+    users = mine > 0 ? (mine + per - 1) / per : 0;
+    if (warp < users) {
+      tile = block0 + warp * per;
+      n = mine - warp * per < per ? mine - warp * per : per;
+    }
+    it.start = -tile - kExtra;
+    if (lane == 0) *item = it;
+    __syncwarp();
+  } else {
+    // the work in front of each lane's requests: every warp for itself
+    uint64_t before = 0, all;
+    {
+      uint64_t mine = 0;
+      bool bad = false;
+      Item it;
+      it.b = static_cast<int64_t>(lane) * p.per_lane;
+      const int64_t b1 = it.b + p.per_lane < p.a.B ? it.b + p.per_lane : p.a.B;
+      for (; it.b < b1; ++it.b) {
+        request<NT>(p, it, &bad);
+        mine += count(p, it);
+      }
+      if (bad && blockIdx.x == 0 && warp == 0) atomicOr(p.a.err, kErrBadCache);
+      before = mine;
+      if (!__any_sync(kFull, mine >> 26 != 0)) {
+        uint32_t sum = static_cast<uint32_t>(mine);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t x = __shfl_up_sync(kFull, sum, o);
+          if (lane >= o) sum += x;
+        }
+        before = sum;
+      } else {
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint64_t x = __shfl_up_sync(kFull, before, o);
+          if (lane >= o) before += x;
+        }
+      }
+      all = __shfl_sync(kFull, before, 31);
+      before -= mine;
+    }
+    // equal runs: a block's, and of that a warp's; the longer ones are spread over the blocks
+    if (all >> 32 == 0) {
+      const uint32_t x = static_cast<uint32_t>(all), y = __umulhi(x, p.by_grid);  // one too few at most
+      r = x - y * nb;
+      q = r >= nb ? y + 1 : y;
+      r = r >= nb ? r - nb : r;
+    } else {
+      q = all / nb;
+      r = static_cast<uint32_t>(all - q * nb);
+    }
+    const uint32_t r0 = share(blockIdx.x), r1 = share(blockIdx.x + 1);
+    const uint64_t block0 = q * blockIdx.x + r0;
+    run = q + r1 - r0;
+    const uint64_t per = (run + Sh::kWarps - 1) / Sh::kWarps, skip = static_cast<uint64_t>(warp) * per;
+    from = block0 + skip;
+    n = skip >= run ? 0 : static_cast<int>(run - skip < per ? run - skip : per);
+    if (n > 0) {
+      Item it;
+      tile = place<NT>(p, before, from, it);
+      if (lane == 0) *item = it;
+      __syncwarp();
+    }
+  }
+  // queries as they are loaded: row g (+ 8 x), channels 32 b + 8 t ..
   auto load_queries = [&](const Item& it, uint4 (&qv)[NT][NB]) {
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
@@ -270,12 +352,6 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
         qv[x][b] = on ? *reinterpret_cast<const uint4*>(row + 32 * b) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
-  if (n > 0) {
-    Item it;
-    tile = place<NT>(p, before, from, it);
-    if (lane == 0) *item = it;
-    __syncwarp();
-  }
 
   // loads: lane l finds the source of every 32nd tile, from the current item on, and starts its copy
   const uint8_t* src = nullptr;
@@ -291,7 +367,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
       src = nullptr;
       load = x < it.tiles && it.start + kExtra + x < n;
       if (load && it.len > 0) {
-        const uint32_t tpp = static_cast<uint32_t>(p.a.page) / 32, page_at = static_cast<uint32_t>(x) / tpp;
+        const uint32_t tpp = static_cast<uint32_t>(p.a.page) / 32;
+        const uint32_t page_at = tpp == 1 ? static_cast<uint32_t>(x) : static_cast<uint32_t>(__umul64hi(static_cast<uint32_t>(x), p.by_tpp));
         const int64_t page = p.a.block_table[it.b * p.a.width + page_at];
         if (page >= 0 && page < p.a.pages)
           src = p.a.cache + page * p.a.page_stride +
@@ -603,12 +680,13 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
       break;
     }
     Item it = *item;
-    const bool whole = tile == tiles, rows = whole && !front;
-    more = whole && it.start + tiles + 2 * kExtra < n;
+    const bool whole = tile == tiles, rows = !kAlone && whole && !front;
+    more = !kAlone && whole && it.start + tiles + 2 * kExtra < n;
     put(more ? aside + warp * Sh::kPart : reinterpret_cast<float*>(ring), rows);
-    if (!rows && lane == 0)
+    if (!kAlone && !rows && lane == 0)
       rec[2 * warp + (more ? 0 : 1)] = {it.h, it.group, it.lq,
-                                        kPartHeld | (front ? kPartFromFront : 0) | (whole ? 0 : kPartGoesOn), it.q0};
+                                        kPartHeld | (front ? kPartFromFront : 0) | (whole ? 0 : kPartGoesOn), it.q0,
+                                        static_cast<int64_t>(from) + it.start + it.tiles + kExtra};
     if (more) {
       next_item<NT>(p, it);
       __syncwarp();  // every lane has read the old one
@@ -619,12 +697,53 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     }
   }
   __syncthreads();
+  constexpr int E = D / 32;
+  auto write_row = [&](int lq, int h, int group, int64_t q0, int row, float sum, const float (&acc)[E]) {
+    int query;
+    int64_t head;
+    if (row_at<NT>(p, lq, h, group, row, &query, &head)) {
+      const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.a.o + (q0 + query) * p.a.st[2] + head * p.a.st[3] + E * lane);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    }
+  };
+  if constexpr (kAlone) {
+    // the block's warps, then the cluster's blocks, which share the rows.  (After a wait that gave up
+    // the rows hold anything, but no block may leave the others waiting.)
+    for (int row = warp; row < Sh::kRows; row += Sh::kWarps) {
+      float top, sum, acc[E];
+      auto member = [&](int m) { return reinterpret_cast<const float*>(sm + m * Sh::kRing) + row * Sh::kPad; };
+      add_up<D>(lane, users, member, top, sum, acc);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(aside + row * Sh::kPad + E * lane + e) = make_float2(acc[e], acc[e + 1]);
+      if (lane == 0) *reinterpret_cast<float2*>(aside + row * Sh::kPad + D) = make_float2(top, sum);
+    }
+    cluster_sync();
+    const int c = p.cluster, rank = static_cast<int>(blockIdx.x) % c;
+    const Item it = *reinterpret_cast<const Item*>(sm + Sh::kOffItem);
+    for (int row = rank + c * warp; row < Sh::kRows; row += c * Sh::kWarps) {
+      const float* mine = aside + row * Sh::kPad;
+      float top = kNone, sum = 0.0f, acc[E] = {};
+      for (int x = 0; x < c; ++x) top = fmaxf(top, peer_load(mine + D, x));
+#pragma unroll 4
+      for (int x = 0; x < c; ++x) {
+        const float by = ex2(peer_load(mine + D, x) - top);
+        sum = fmaf(peer_load(mine + D + 1, x), by, sum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(peer_load(mine + E * lane + e, x), by, acc[e]);
+      }
+      write_row(it.lq, it.h, it.group, it.q0, row, sum, acc);
+    }
+    cluster_sync();  // no block leaves while another reads its shared memory
+    return;
+  }
   if (abort_flag != 0) return;
 
   // The block's chains: a run at a warp's end and those of the warps behind it while it goes on, in the
   // end one put aside.  A warp takes one row of a chain at a time.
-  Record out[2];
-  out[0].flags = out[1].flags = 0;
+  Record out;
+  out.flags = 0;
   const int fa = lane < Sh::kWarps ? rec[2 * lane].flags : 0, fe = lane < Sh::kWarps ? rec[2 * lane + 1].flags : 0;
   const unsigned asides = __ballot_sync(kFull, fa != 0), ends = __ballot_sync(kFull, fe != 0);
   const unsigned fronts = __ballot_sync(kFull, (fe & kPartFromFront) != 0), onward = __ballot_sync(kFull, (fe & kPartGoesOn) != 0);
@@ -632,7 +751,6 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
   int task = 0;
 #pragma unroll 1
   for (unsigned todo = (ends & (~fronts | 1u)) << 1 | (asides & 1u); todo != 0; todo &= todo - 1) {
-    constexpr int E = D / 32;
     const int w1 = __ffs(todo) - 1, w0 = w1 > 0 ? w1 - 1 : 0;  // 0: the run that warp 0 put aside, alone
     const int n_end = w1 > 0 ? __ffs(stops >> w0) : 0;         // warps whose runs at the end belong to it
     const bool tail = w1 == 0 || ((onward >> (w0 + n_end - 1) & 1u) != 0 && (asides >> (w0 + n_end) & 1u) != 0);
@@ -640,124 +758,104 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     const int end = tail ? 0 : rec[2 * (w0 + n_end - 1) + 1].flags;  // what is put aside does not go on
     const int v = w0 + n_end, members = n_end + (tail ? 1 : 0);
     const bool from_front = (who.flags & kPartFromFront) != 0, goes_on = (end & kPartGoesOn) != 0;
-    who.flags = kPartHeld | (from_front ? kPartFromFront : 0) | (goes_on ? kPartGoesOn : 0);
-    if (from_front) out[0] = who;
-    else if (goes_on) out[1] = who;
+    if (goes_on && !from_front) out = who;
 #pragma unroll 1
     for (int row = (warp + Sh::kWarps - task % Sh::kWarps) % Sh::kWarps; row < Sh::kRows; row += Sh::kWarps) {
       auto member = [&](int m) {
         return reinterpret_cast<const float*>(m < n_end ? sm + (w0 + m) * Sh::kRing : sm + Sh::kOffAside + v * Sh::kPart * 4) + row * Sh::kPad;
       };
-      const float2 ml = lane < members ? *reinterpret_cast<const float2*>(member(lane) + D) : make_float2(kNone, 0.0f);
-      float top = ml.x, acc[E] = {};
-#pragma unroll
-      for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
-      const float by = ex2(ml.x - top);
-      float sum = ml.y * by;
-#pragma unroll
-      for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(kFull, sum, i);
-#pragma unroll 4
-      for (int m = 0; m < members; ++m) {
-        const float* from_m = member(m) + E * lane;
-        const float by_m = __shfl_sync(kFull, by, m);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 x = *reinterpret_cast<const float2*>(from_m + e);
-          acc[e] = fmaf(x.x, by_m, acc[e]);
-          acc[e + 1] = fmaf(x.y, by_m, acc[e + 1]);
-        }
-      }
+      float top, sum, acc[E];
+      add_up<D>(lane, members, member, top, sum, acc);
       if (from_front || goes_on) {
         float* dst = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (from_front ? 0 : 1)) * Sh::kPart + row * Sh::kPad;
 #pragma unroll
         for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(dst + E * lane + e) = make_float2(acc[e], acc[e + 1]);
         if (lane == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(top, sum);
       } else {
-        int query;
-        int64_t head;
-        if (row_at<NT>(p, who.lq, who.h, who.group, row, &query, &head)) {
-          const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-          uint32_t* dst = reinterpret_cast<uint32_t*>(p.a.o + (who.q0 + query) * p.a.st[2] + head * p.a.st[3] + E * lane);
-#pragma unroll
-          for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-        }
+        write_row(who.lq, who.h, who.group, who.q0, row, sum, acc);
       }
     }
     task += Sh::kRows;
   }
-  if (threadIdx.x == 0) {
-    p.meta[2 * blockIdx.x] = out[0];
-    p.meta[2 * blockIdx.x + 1] = out[1];
+  if (warp != 0) return;
+  if (out.flags != 0) {  // the last block whose run begins in front of the item's end
+    int last = static_cast<int>(blockIdx.x);
+    for (uint32_t k0 = blockIdx.x + 1; k0 < nb; k0 += 32) {
+      const uint32_t k = k0 + lane;
+      const unsigned in = __ballot_sync(kFull, k < nb && static_cast<int64_t>(q * k + share(k)) < out.end);
+      last += __popc(in);
+      if (in != kFull) break;
+    }
+    out.end = last;
   }
+  if (lane == 0) p.meta[blockIdx.x] = out;
+  // a block without work adds nothing to a run that passes it
+  if (run == 0 && lane < Sh::kRows)
+    *reinterpret_cast<float2*>(p.part + static_cast<int64_t>(blockIdx.x) * 2 * Sh::kPart + lane * Sh::kPad + D) = make_float2(kNone, 0.0f);
 }
 
-// Runs that cross blocks: block x joins the one that begins in block x of the attention kernel, row
-// y.  Its members are found by all lanes at once, and each warp adds every fourth: their loads do
-// not wait for one another.
-constexpr int kJoinWarps = 4;
+// Runs that cross blocks: block x joins the one that begins in block x of the attention kernel.  The
+// parts of all its blocks are loaded at once, a few warps to a row (a trip to another SM's results
+// takes about a microsecond: two of them, the record and the parts, are all there is).
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const __grid_constant__ Kv4Params p) {
+__global__ void __launch_bounds__(1024) kv4_join_kernel(const __grid_constant__ Kv4Params p) {
   using Sh = Kv4Shape<D, NT>;
-  constexpr int E = D / 32;
-  __shared__ int slots[kMaxBlocks];
-  __shared__ float2 ml_s[kMaxBlocks];
-  __shared__ float acc_s[kJoinWarps][D];
-  __shared__ float sum_s[kJoinWarps];
+  constexpr int E = D / 32, kW = 32 / Sh::kRows, kAhead = 16 / E;  // warps of a row, parts in flight
+  __shared__ float acc_s[32][D];
+  __shared__ float2 ml_s[32];
   pdl_wait();
-  const int x = static_cast<int>(blockIdx.x), nb = static_cast<int>(gridDim.x), row = static_cast<int>(blockIdx.y);
+  const int x = static_cast<int>(blockIdx.x);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  const Record who = p.meta[2 * x + 1];
+  const Record who = p.meta[x];
   if (who.flags == 0) return;
-  int query;
-  int64_t head;
-  if (!row_at<NT>(p, who.lq, who.h, who.group, row, &query, &head)) return;
-  int n = 1;  // members
-  bool open = true;
-  for (int b0 = x + 1; b0 < nb && open; b0 += 32) {
-    const int flags = b0 + lane < nb ? p.meta[2 * (b0 + lane)].flags : 0;  // 0: a block without work
-    const unsigned held = __ballot_sync(kFull, flags != 0), ends = __ballot_sync(kFull, flags != 0 && (flags & kPartGoesOn) == 0);
-    const unsigned mine = ends != 0 ? held & (ends ^ (ends - 1)) : held;  // up to the first that ends
-    if (((mine >> lane) & 1u) != 0 && warp == 0) slots[n + __popc(mine & ((1u << lane) - 1))] = 2 * (b0 + lane);
-    n += __popc(mine);
-    open = ends == 0;
-  }
-  if (threadIdx.x == 0) slots[0] = 2 * x + 1;
-  __syncthreads();
-  for (int m = static_cast<int>(threadIdx.x); m < n; m += 32 * kJoinWarps)
-    ml_s[m] = *reinterpret_cast<const float2*>(p.part + static_cast<int64_t>(slots[m]) * Sh::kPart + row * Sh::kPad + D);
-  __syncthreads();
-  float top = kNone;
-  for (int m = lane; m < n; m += 32) top = fmaxf(top, ml_s[m].x);
+  const int row = warp / kW, w0 = row * kW, n = static_cast<int>(who.end) - x + 1;
+  float top = kNone, sum = 0.0f, acc[E] = {};
+  for (int m0 = warp - w0; m0 < n; m0 += kW * kAhead) {
+    float2 ml[kAhead];
+    float v[kAhead][E];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  float sum = 0.0f, acc[E] = {};
-#pragma unroll 4
-  for (int m = warp; m < n; m += kJoinWarps) {
-    const float* src = p.part + static_cast<int64_t>(slots[m]) * Sh::kPart + row * Sh::kPad + E * lane;
-    const float2 ml = ml_s[m];
-    const float by = ex2(ml.x - top);
-    sum = fmaf(ml.y, by, sum);
+    for (int i = 0; i < kAhead; ++i) {
+      const int m = m0 + i * kW;
+      const float* src = p.part + static_cast<int64_t>(2 * (x + m) + (m == 0 ? 1 : 0)) * Sh::kPart + row * Sh::kPad;
+      ml[i] = make_float2(kNone, 0.0f);
+      if (m < n) {
+        ml[i] = *reinterpret_cast<const float2*>(src + D);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(src + e);
-      acc[e] = fmaf(v.x, by, acc[e]);
-      acc[e + 1] = fmaf(v.y, by, acc[e + 1]);
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(&v[i][e]) = *reinterpret_cast<const float2*>(src + E * lane + e);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (ml[i].y == 0.0f) continue;  // nothing seen, or a block without work, whose place holds anything
+      const float to = fmaxf(top, ml[i].x), old = ex2(top - to), by = ex2(ml[i].x - to);
+      top = to;
+      sum = fmaf(sum, old, ml[i].y * by);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], old, v[i][e] * by);
     }
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) acc_s[warp][E * lane + e] = acc[e];
-  if (lane == 0) sum_s[warp] = sum;
+  if (lane == 0) ml_s[warp] = make_float2(top, sum);
   __syncthreads();
-  for (int c = 2 * static_cast<int>(threadIdx.x); c < D; c += 64 * kJoinWarps) {
+  top = kNone;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) top = fmaxf(top, ml_s[w0 + w].x);
+  int query;
+  int64_t head;
+  if (!row_at<NT>(p, who.lq, who.h, who.group, row, &query, &head)) return;
+  const int c = 2 * (static_cast<int>(threadIdx.x) - 32 * w0);
+  for (int k = c; k < D; k += 64 * kW) {
     float t = 0.0f, u = 0.0f, v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      t += sum_s[w];
-      u += acc_s[w][c];
-      v += acc_s[w][c + 1];
+    for (int w = 0; w < kW; ++w) {
+      const float by = ex2(ml_s[w0 + w].x - top);
+      t = fmaf(ml_s[w0 + w].y, by, t);
+      u = fmaf(acc_s[w0 + w][k], by, u);
+      v = fmaf(acc_s[w0 + w][k + 1], by, v);
     }
     const float inv = t != 0.0f ? 1.0f / t : 0.0f;
-    *reinterpret_cast<uint32_t*>(p.a.o + (who.q0 + query) * p.a.st[2] + head * p.a.st[3] + c) = pack_bf16(u * inv, v * inv);
+    *reinterpret_cast<uint32_t*>(p.a.o + (who.q0 + query) * p.a.st[2] + head * p.a.st[3] + k) = pack_bf16(u * inv, v * inv);
   }
 }
 
@@ -768,11 +866,47 @@ int row_tiles(int64_t G, bool one_query, int64_t d) { return d == 256 || (one_qu
 
 int grid_blocks(const DeviceInfo& dev) { return std::min(dev.sm_count, kMaxBlocks); }
 
+// Blocks of a cluster that takes a group of rows alone, 0 where the work list is better: one group a
+// request and head, all of them at once on the GPU, and few keys for a block even if one request
+// has all that its row of the block table can name (1024: about what the second launch costs; one
+// request of 1000 keys: XX us alone, 10.1 with the list).
+int alone_blocks(const Kv4AttentionArgs& a, int nt, const DeviceInfo& dev) {
+  const int64_t items = a.B * a.Hkv, keys = a.width * a.page;
+  if (a.cu_q != nullptr || a.H / a.Hkv > 8 * nt || items > dev.sm_count) return 0;
+  int64_t c = 8;
+  while (c > 1 && items * c > dev.sm_count) c /= 2;
+  while (c > 1 && c * 64 > keys) c /= 2;  // two tiles a block at least
+  return keys <= c * 1024 ? static_cast<int>(c) : 0;
+}
+
 template <int D, int NT>
 size_t ws_bytes(const DeviceInfo& dev) {
   using Sh = Kv4Shape<D, NT>;
   const size_t blocks = static_cast<size_t>(grid_blocks(dev));
-  return blocks * 2 * (Sh::kPart * 4 + sizeof(Record));
+  return blocks * (2 * Sh::kPart * 4 + sizeof(Record));
+}
+
+template <typename K>
+cudaError_t launch_one(K kernel, int blocks, int threads, size_t smem, int cluster, bool dependent, const Kv4Params& p,
+                       cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  if (dependent) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+  } else if (cluster > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <int D, int NT>
@@ -783,34 +917,33 @@ cudaError_t attention(const Kv4AttentionArgs& a, const DeviceInfo& dev, cudaStre
   p.G = static_cast<int>(a.H / a.Hkv);
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.per_lane = static_cast<int>((a.B + 31) / 32);
-  p.by_G = ~uint64_t{0} / static_cast<uint64_t>(p.G) + 1;  // unused for 1
-  p.by_grid = ~uint64_t{0} / static_cast<uint64_t>(grid_blocks(dev)) + 1;
-  const unsigned blocks = static_cast<unsigned>(grid_blocks(dev));
+  p.by_G = ~uint64_t{0} / static_cast<uint64_t>(p.G) + 1;
+  p.by_tpp = ~uint64_t{0} / static_cast<uint64_t>(a.page / 32) + 1;
+  p.cluster = alone_blocks(a, NT, dev);
+  if (p.cluster > 0) {
+    const auto kernel = kv4_attention_kernel<D, NT, true>;
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), Sh::kSmem, dev.device);
+    if (e != cudaSuccess) return e;
+    return launch_one(kernel, static_cast<int>(a.B * a.Hkv) * p.cluster, Sh::kThreads, Sh::kSmem, p.cluster, false, p, stream);
+  }
+  const int blocks = grid_blocks(dev);
+  p.by_grid = static_cast<uint32_t>((uint64_t{1} << 32) / static_cast<uint64_t>(blocks));
   p.part = static_cast<float*>(a.part);
   p.meta = reinterpret_cast<Record*>(p.part + static_cast<size_t>(blocks) * 2 * Sh::kPart);
-  const auto kernel = kv4_attention_kernel<D, NT>;
+  const auto kernel = kv4_attention_kernel<D, NT, false>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), Sh::kSmem, dev.device);
   if (e != cudaSuccess) return e;
-  kernel<<<blocks, Sh::kThreads, Sh::kSmem, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, Sh::kRows);
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, p);
+  if ((e = launch_one(kernel, blocks, Sh::kThreads, Sh::kSmem, 1, false, p, stream)) != cudaSuccess) return e;
+  return launch_one(kv4_join_kernel<D, NT>, blocks, 1024, 0, 1, true, p, stream);
 }
 
 }  // namespace
 
-size_t kv4_attention_ws_bytes(int64_t H, int64_t Hkv, int64_t d, bool one_query, const DeviceInfo& dev) {
-  const int nt = row_tiles(H / Hkv, one_query, d);
-  if (d == 256) return ws_bytes<256, 1>(dev);
-  if (d == 128) return nt == 1 ? ws_bytes<128, 1>(dev) : ws_bytes<128, 2>(dev);
+size_t kv4_attention_ws_bytes(const Kv4AttentionArgs& a, const DeviceInfo& dev) {
+  const int nt = row_tiles(a.H / a.Hkv, a.cu_q == nullptr, a.d);
+  if (alone_blocks(a, nt, dev) > 0) return 0;
+  if (a.d == 256) return ws_bytes<256, 1>(dev);
+  if (a.d == 128) return nt == 1 ? ws_bytes<128, 1>(dev) : ws_bytes<128, 2>(dev);
   return nt == 1 ? ws_bytes<64, 1>(dev) : ws_bytes<64, 2>(dev);
 }
 
