@@ -74,15 +74,6 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const TableParams p) {
 }
 
 // ---- append ----------------------------------------------------------------------------------
-#ifndef KVRB
-#define KVRB 2
-#endif
-#ifndef KVMINB
-#define KVMINB 7
-#endif
-#ifndef KVRF
-#define KVRF 2
-#endif
 constexpr int kAppendThreads = 128;
 
 struct AppendParams {
@@ -247,7 +238,7 @@ __device__ __forceinline__ void append_queries(const AppendParams& p, uint32_t t
 // The keys or values of a part: d / 8 lanes a head, a chunk of 8 channels each.  kRounds: rounds of a
 // warp, all loaded before the first is worked on.
 template <int D, bool kF32, bool kInterleaved, int kRounds>
-__global__ void __launch_bounds__(kAppendThreads, KVMINB) kv4_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, kF32 ? 6 : 7) kv4_append_kernel(const __grid_constant__ AppendParams p) {
   using Tile = Kv4Tile<D>;
   constexpr int L = D / 8, kTeams = 32 / L;  // lanes of a head, heads of a round
   const Kv4AppendArgs& a = p.a;
@@ -534,7 +525,7 @@ template <int D, bool kF32>
 cudaError_t append(const Kv4AppendArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
   AppendParams p = {};
   p.a = a;
-  constexpr int kTeams = 32 / (D / 8), kMost = kF32 ? KVRF : KVRB;
+  constexpr int kTeams = 32 / (D / 8), kMost = 2;
   p.nq = static_cast<int>((a.H + 2 * kTeams - 1) / (2 * kTeams));
   p.nk = static_cast<int>((a.Hkv + kTeams - 1) / kTeams);
   p.inv_d = 1.0f / D;

@@ -33,9 +33,6 @@
 #include "q8_internal.h"
 #include "q8_kv4.cuh"
 
-#ifndef KVWEXPR
-#define KVWEXPR (D == 64 ? (NT == 2 ? 12 : 16) : D == 128 && NT == 1 ? 12 : 8)
-#endif
 namespace q8 {
 namespace {
 
@@ -52,6 +49,21 @@ __device__ __forceinline__ uint32_t mul_bf16(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// bulk_load of what leaves the L2 first: a cache is read once a step, and what the kernels need again
+// (their code among it) should not have to make room for it
+__device__ __forceinline__ uint64_t read_once() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void bulk_load_once(void* smem_dst, const void* gmem_src, uint32_t bytes, uint64_t* bar,
+                                               uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::
+          "r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(gmem_src)), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
 // an 8 x 8 matrix of 16-bit elements, two of a row to a lane, transposed
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
@@ -61,10 +73,10 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
-#ifndef KVX
-#define KVX 2
-#endif
-constexpr int kExtra = KVX;
+// What a group of rows costs a warp beside its tiles (queries, results), in tiles: the work list counts
+// it in, so that short requests do not hold up the warp that gets many (64 requests of up to 8192
+// keys: 29.0 us, 34 with one, 50 with none).
+constexpr int kExtra = 3;
 constexpr float kNone = -1e30f;     // reference of a row that has seen no key
 constexpr float kLift = 64.0f;      // weights are carried as 2^64 p
 constexpr float kSlack = 10.0f;     // a reference may lag behind the largest score by 2^10
@@ -103,7 +115,8 @@ template <int D, int NT>
 struct Kv4Shape {
   using Tile = Kv4Tile<D>;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kWarps = KVWEXPR;
+  // as many as the registers of a lane allow (128 channels: 12 warps of 168 registers; 16 of 128 spill)
+  static constexpr int kWarps = D == 64 ? (NT == 1 ? 16 : 12) : D == 128 && NT == 1 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPad = D + 4;                         // floats of a row's partial result: o, reference, sum
   static constexpr int kPart = kRows * kPad;                 // floats of a partial result
@@ -204,6 +217,13 @@ __device__ __forceinline__ bool row_at(const Kv4Params& p, int lq, int h, int gr
   *query = static_cast<int>(i);
   *head = static_cast<int64_t>(h) * p.G + (x - i * static_cast<uint32_t>(p.G));
   return i < static_cast<uint32_t>(lq);
+}
+
+// Rows of a group that are a query's.
+template <int NT>
+__device__ __forceinline__ int rows_used(const Kv4Params& p, int lq, int group) {
+  const int64_t left = static_cast<int64_t>(lq) * p.G - static_cast<int64_t>(group) * (8 * NT);
+  return left < 8 * NT ? static_cast<int>(left) : 8 * NT;
 }
 
 // A row of `members` partial results, member(m) the m-th's: reference, sum, the lane's channels.
@@ -354,6 +374,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
   };
 
   // loads: lane l finds the source of every 32nd tile, from the current item on, and starts its copy
+  const uint64_t once = read_once();
   const uint8_t* src = nullptr;
   bool load = false;  // there is such a tile
   auto fill = [&](int i, int ahead) {  // ahead: tiles between the current one and the i-th
@@ -383,7 +404,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
       bad_s[st] = src == nullptr;
       if (src != nullptr) {
         mbar_arrive_expect_tx(&bars[st], Tile::kBytes);
-        bulk_load(ring + st * Tile::kBytes, src, Tile::kBytes, &bars[st]);
+        bulk_load_once(ring + st * Tile::kBytes, src, Tile::kBytes, &bars[st], once);
       } else {
         mbar_arrive(&bars[st]);
       }
@@ -711,7 +732,9 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
   if constexpr (kAlone) {
     // the block's warps, then the cluster's blocks, which share the rows.  (After a wait that gave up
     // the rows hold anything, but no block may leave the others waiting.)
-    for (int row = warp; row < Sh::kRows; row += Sh::kWarps) {
+    const Item it = *reinterpret_cast<const Item*>(sm + Sh::kOffItem);
+    const int used = rows_used<NT>(p, it.lq, it.group);
+    for (int row = warp; row < used; row += Sh::kWarps) {
       float top, sum, acc[E];
       auto member = [&](int m) { return reinterpret_cast<const float*>(sm + m * Sh::kRing) + row * Sh::kPad; };
       add_up<D>(lane, users, member, top, sum, acc);
@@ -721,8 +744,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     }
     cluster_sync();
     const int c = p.cluster, rank = static_cast<int>(blockIdx.x) % c;
-    const Item it = *reinterpret_cast<const Item*>(sm + Sh::kOffItem);
-    for (int row = rank + c * warp; row < Sh::kRows; row += c * Sh::kWarps) {
+    for (int row = rank + c * warp; row < used; row += c * Sh::kWarps) {
       const float* mine = aside + row * Sh::kPad;
       float top = kNone, sum = 0.0f, acc[E] = {};
       for (int x = 0; x < c; ++x) top = fmaxf(top, peer_load(mine + D, x));
@@ -759,8 +781,9 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     const int v = w0 + n_end, members = n_end + (tail ? 1 : 0);
     const bool from_front = (who.flags & kPartFromFront) != 0, goes_on = (end & kPartGoesOn) != 0;
     if (goes_on && !from_front) out = who;
+    const int used = rows_used<NT>(p, who.lq, who.group);
 #pragma unroll 1
-    for (int row = (warp + Sh::kWarps - task % Sh::kWarps) % Sh::kWarps; row < Sh::kRows; row += Sh::kWarps) {
+    for (int row = (warp + Sh::kWarps - task % Sh::kWarps) % Sh::kWarps; row < used; row += Sh::kWarps) {
       auto member = [&](int m) {
         return reinterpret_cast<const float*>(m < n_end ? sm + (w0 + m) * Sh::kRing : sm + Sh::kOffAside + v * Sh::kPart * 4) + row * Sh::kPad;
       };
@@ -775,7 +798,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
         write_row(who.lq, who.h, who.group, who.q0, row, sum, acc);
       }
     }
-    task += Sh::kRows;
+    task += used;
   }
   if (warp != 0) return;
   if (out.flags != 0) {  // the last block whose run begins in front of the item's end
