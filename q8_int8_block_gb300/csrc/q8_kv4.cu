@@ -75,11 +75,13 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const TableParams p) {
 
 // ---- append ----------------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
+constexpr int kTileHeads = 2;  // key/value heads of a block of kv4_append_tiles_kernel
 
 struct AppendParams {
   Kv4AppendArgs a;
   int nq, nk;         // warp rounds of a token's query heads, of its key (and of its value) heads
   int pq, parts;      // warps of its query heads, of all
+  int kv_blocks;      // (tiles) blocks of keys and values
   float inv_d;
 };
 
@@ -235,8 +237,128 @@ __device__ __forceinline__ void append_queries(const AppendParams& p, uint32_t t
   }
 }
 
-// The keys or values of a part: d / 8 lanes a head, a chunk of 8 channels each.  kRounds: rounds of a
-// warp, all loaded before the first is worked on.
+// Keys and values: d / 8 lanes a head, a chunk of 8 channels each.
+//
+// The lane's rotation of one token: halves (the chunk's eight pairs, whose other channel is lane
+// `partner`'s) or neighbours (its four pairs).
+template <bool kInterleaved>
+struct Turn {
+  float cs[8], sn[8];  // no rotation: 1 and 0
+  int partner;
+  bool turns;
+  __device__ __forceinline__ void load(const AppendParams& p, int64_t t, int lane, int c) {
+    const Kv4AppendArgs& a = p.a;
+    const bool upper = !kInterleaved && 16 * c >= a.rot;
+    const int half = a.rot / 2, other = a.rot / 16;
+    turns = 8 * c < a.rot;
+    partner = !kInterleaved && turns ? lane + (upper ? -other : other) : lane;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cs[i] = 1.0f;
+      sn[i] = 0.0f;
+    }
+    if (!turns) return;
+    const float* row = a.table + t * 2 * half;
+    if constexpr (kInterleaved) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(row + 4 * c));
+      const float4 v = __ldg(reinterpret_cast<const float4*>(row + half + 4 * c));
+      cs[0] = u.x; cs[1] = u.y; cs[2] = u.z; cs[3] = u.w;
+      sn[0] = v.x; sn[1] = v.y; sn[2] = v.z; sn[3] = v.w;
+    } else {
+      load8(row + 8 * (upper ? c - other : c), cs);
+      load8(row + half + 8 * (upper ? c - other : c), sn);
+      if (!upper) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sn[i] = -sn[i];  // exact: a cos - b sin is a cos + b (-sin)
+      }
+    }
+  }
+};
+
+// r, and z = x w turned in place.  Products and sums are rounded one by one: the codes are then the
+// same wherever they are formed.
+template <int D, bool kInterleaved>
+__device__ __forceinline__ float norm_and_turn(const AppendParams& p, const Turn<kInterleaved>& rot, const float (&wv)[8],
+                                               float (&z)[8]) {
+  float f = 1.0f;
+  if (p.a.k_weight != nullptr) {
+    float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float2 u = make_float2(z[i], z[i + 1]), v = make_float2(__fmul_rn(u.x, wv[i]), __fmul_rn(u.y, wv[i + 1]));
+      s2 = __ffma2_rn(u, u, s2);
+      z[i] = v.x;
+      z[i + 1] = v.y;
+    }
+    float ss = s2.x + s2.y;
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+    f = rsqrtf(fmaf(ss, p.inv_d, p.a.eps));
+  }
+  if constexpr (kInterleaved) {
+    if (rot.turns) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float u = z[2 * i], v = z[2 * i + 1];
+        z[2 * i] = __fsub_rn(__fmul_rn(u, rot.cs[i]), __fmul_rn(v, rot.sn[i]));
+        z[2 * i + 1] = __fadd_rn(__fmul_rn(u, rot.sn[i]), __fmul_rn(v, rot.cs[i]));
+      }
+    }
+  } else if (p.a.rot > 0) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float2 o = make_float2(__shfl_sync(kFull, z[i], rot.partner), __shfl_sync(kFull, z[i + 1], rot.partner));
+      // scalar products: packed ones are fused into the sums even so
+      const float2 v = __fadd2_rn(make_float2(__fmul_rn(z[i], rot.cs[i]), __fmul_rn(z[i + 1], rot.cs[i + 1])),
+                                  make_float2(__fmul_rn(o.x, rot.sn[i]), __fmul_rn(o.y, rot.sn[i + 1])));
+      z[i] = v.x;
+      z[i + 1] = v.y;
+    }
+  }
+  return f;
+}
+
+// The quantiser: lanes 4 b .. 4 b + 3 of a head hold block b.  The lane's eight codes, and its block's
+// scale.
+__device__ __forceinline__ uint32_t quantise(const float (&z)[8], float f, __nv_bfloat16* scale) {
+  float top = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(z[e]));
+  top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+  const bool zero = top < kKv4Zero;
+  const float inv = zero ? 0.0f : __fdiv_rn(7.0f, top);
+  uint32_t word = 0;
+#pragma unroll
+  for (int e = 6; e >= 0; e -= 2) {
+    // 1.5 2^23 + 8 is even, so adding it rounds as rint does; its bits are 0x4B400000 + code + 8,
+    // and the first part of eight of them, each 16 times the next, is taken off at the end
+    const float2 m = __fadd2_rn(make_float2(__fmul_rn(z[e], inv), __fmul_rn(z[e + 1], inv)), make_float2(12582920.0f, 12582920.0f));
+    word = (word * 16u + __float_as_uint(m.y)) * 16u + __float_as_uint(m.x);
+  }
+  *scale = __float2bfloat16_rn(zero ? 0.0f : __fmul_rn(__fmul_rn(top, f), 1.0f / 7.0f));
+  return word + kCodes;
+}
+
+// Blocks 2 h and 2 h + 1 of a value share words: of a lane's two halves the lane of the other block
+// takes one.  The lane's word is that of channels 64 h + 4 g .. and + 32, g = 2 (c % 4) + b % 2.
+__device__ __forceinline__ uint32_t pair_values(uint32_t word, int b) {
+  const uint32_t got = __shfl_xor_sync(kFull, (b & 1) == 0 ? word >> 16 : word & 0xFFFFu, 4);
+  return (b & 1) == 0 ? (word & 0xFFFFu) | got << 16 : got | (word & 0xFFFF0000u);
+}
+
+// A token's place from its slot; false: it is not kept.
+__device__ __forceinline__ bool token_place(const Kv4AppendArgs& a, int slot, int tile_bytes, uint8_t** tile, int* tok) {
+  const uint32_t page = static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page);
+  const int in_page = static_cast<int>(static_cast<uint32_t>(slot) - page * static_cast<uint32_t>(a.page));
+  *tok = in_page & 31;
+  if (slot < 0 || page >= a.pages) return false;
+  *tile = a.cache + page * a.page_stride + static_cast<int64_t>(in_page >> 5) * tile_bytes;
+  return true;
+}
+
+// A warp takes kRounds rounds of one token's heads, of one kind, and loads them all before the first
+// is worked on.
 template <int D, bool kF32, bool kInterleaved, int kRounds>
 __global__ void __launch_bounds__(kAppendThreads, kF32 ? 6 : 7) kv4_append_kernel(const __grid_constant__ AppendParams p) {
   using Tile = Kv4Tile<D>;
@@ -255,7 +377,6 @@ __global__ void __launch_bounds__(kAppendThreads, kF32 ? 6 : 7) kv4_append_kerne
     return;
   }
   const int r0 = part * kRounds, rounds = p.nk - r0, heads = static_cast<int>(a.Hkv);
-
   Eight<kF32> x[kRounds];
   {
     const void* from = kind == 1 ? a.k : a.v;
@@ -266,78 +387,20 @@ __global__ void __launch_bounds__(kAppendThreads, kF32 ? 6 : 7) kv4_append_kerne
       if (h < heads) x[i].load(from, at + static_cast<int64_t>(h) * D);
     }
   }
-  // the lane's rotation: halves (the chunk's eight pairs) or neighbours (its four pairs)
-  const bool turns = 8 * c < a.rot, upper = !kInterleaved && 16 * c >= a.rot;
-  const int half = a.rot / 2, other = a.rot / 16;
-  const int partner = !kInterleaved && turns ? lane + (upper ? -other : other) : lane;
-  float cs[8], sn[8], wv[8];  // no rotation: 1 and 0
-  const float* w = kind == 1 ? a.k_weight : nullptr;
+  Turn<kInterleaved> rot;
+  float wv[8];
   if (kind == 1) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      cs[i] = 1.0f;
-      sn[i] = 0.0f;
-    }
-    if (turns) {
-      const float* row = a.table + static_cast<int64_t>(t) * 2 * half;
-      if constexpr (kInterleaved) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(row + 4 * c));
-        const float4 v = __ldg(reinterpret_cast<const float4*>(row + half + 4 * c));
-        cs[0] = u.x; cs[1] = u.y; cs[2] = u.z; cs[3] = u.w;
-        sn[0] = v.x; sn[1] = v.y; sn[2] = v.z; sn[3] = v.w;
-      } else {
-        load8(row + 8 * (upper ? c - other : c), cs);
-        load8(row + half + 8 * (upper ? c - other : c), sn);
-        if (!upper) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sn[i] = -sn[i];  // exact: a cos - b sin is a cos + b (-sin)
-        }
-      }
-    }
-    if (w != nullptr) load8(w + 8 * c, wv);
+    rot.load(p, t, lane, c);
+    if (a.k_weight != nullptr) load8(a.k_weight + 8 * c, wv);
   }
-  // r and z = x w of a round, turned.  Products and sums are rounded one by one: the codes are then
-  // the same wherever they are formed.
-  auto normed = [&](float (&z)[8]) {
-    float f = 1.0f;
-    if (w != nullptr) {
-      float ss = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(z[i], z[i], ss);
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-      f = rsqrtf(fmaf(ss, p.inv_d, a.eps));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = __fmul_rn(z[i], wv[i]);
-    }
-    if constexpr (kInterleaved) {
-      if (turns) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = z[2 * i], v = z[2 * i + 1];
-          z[2 * i] = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(v, sn[i]));
-          z[2 * i + 1] = __fadd_rn(__fmul_rn(u, sn[i]), __fmul_rn(v, cs[i]));
-        }
-      }
-    } else if (a.rot > 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_sync(kFull, z[i], partner);
-        z[i] = __fadd_rn(__fmul_rn(z[i], cs[i]), __fmul_rn(o, sn[i]));
-      }
-    }
-    return f;
-  };
-
-  // the token's place: its tile of head 0
   const int slot = a.slots[t];
-  const uint32_t page = static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page);  // behind the cache if slot < 0
-  const int in_page = static_cast<int>(static_cast<uint32_t>(slot) - page * static_cast<uint32_t>(a.page)), tok = in_page & 31;
-  const bool keep = slot >= 0 && page < a.pages;
-  if (slot >= 0 && !keep && lane == 0 && r0 == 0) atomicOr(a.err, kErrBadCache);
-  if (!keep) return;
+  uint8_t* tile0 = nullptr;
+  int tok;
+  if (!token_place(a, slot, Tile::kBytes, &tile0, &tok)) {
+    if (slot >= 0 && lane == 0 && r0 == 0) atomicOr(a.err, kErrBadCache);
+    return;
+  }
   const int64_t head_bytes = a.page / 32 * Tile::kBytes;
-  uint8_t* tile0 = a.cache + page * a.page_stride + static_cast<int64_t>(in_page >> 5) * Tile::kBytes;
   const int b = c >> 2;
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
@@ -346,37 +409,163 @@ __global__ void __launch_bounds__(kAppendThreads, kF32 ? 6 : 7) kv4_append_kerne
     const bool on = h < heads;
     float z[8] = {}, f = 1.0f;
     if (on) x[i].unpack(z);
-    if (kind == 1) f = normed(z);
-    // the quantiser: lanes 4 b .. 4 b + 3 of a head hold block b
-    float top = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(z[e]));
-    top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-    const bool zero = top < kKv4Zero;
-    const float inv = zero ? 0.0f : __fdiv_rn(7.0f, top);
-    uint32_t word = 0;
-#pragma unroll
-    for (int e = 7; e >= 0; --e)
-      // 1.5 2^23 + 8 is even, so adding it rounds as rint does; its bits are 0x4B400000 + code + 8,
-      // and the first part of eight of them, each 16 times the next, is taken off at the end
-      word = word * 16u + __float_as_uint(__fadd_rn(__fmul_rn(z[e], inv), 12582920.0f));
-    word += kCodes;
-    const __nv_bfloat16 sc = __float2bfloat16_rn(zero ? 0.0f : __fmul_rn(__fmul_rn(top, f), 1.0f / 7.0f));
+    if (kind == 1) f = norm_and_turn<D, kInterleaved>(p, rot, wv, z);
+    __nv_bfloat16 sc;
+    uint32_t word = quantise(z, f, &sc);
+    if (kind == 2) word = pair_values(word, b);
     uint8_t* tile = tile0 + h * head_bytes;
-    if (kind == 1) {
-      if (on) {
-        *reinterpret_cast<uint32_t*>(tile + Tile::key_word(tok, c)) = word;
-        if ((c & 3) == 0) *reinterpret_cast<__nv_bfloat16*>(tile + Tile::kKeyScales + Tile::scale(tok, b)) = sc;
+    if (on) {
+      *reinterpret_cast<uint32_t*>(tile + (kind == 1 ? Tile::key_word(tok, c) : Tile::value_word(tok, 2 * (c & 3) + (b & 1), b >> 1))) = word;
+      if ((c & 3) == 0)
+        *reinterpret_cast<__nv_bfloat16*>(tile + (kind == 1 ? Tile::kKeyScales : Tile::kValueScales) + Tile::scale(tok, b)) = sc;
+    }
+  }
+}
+
+// Many tokens: a block takes 32 neighbouring ones of one key/value head, or four parts of queries.
+// What its warps have formed meets in shared memory and is written in the order of the tiles, so
+// that sectors are written whole: the tokens one by one would write 18 sectors each, most of them 2
+// or 8 bytes at a time (8192 tokens of 8 heads of 128: keys and values 16.1 us so, 21.5 one by one).
+template <int D, bool kF32, bool kInterleaved>
+__global__ void __launch_bounds__(kAppendThreads, kF32 ? 6 : 7) kv4_append_tiles_kernel(const __grid_constant__ AppendParams p) {
+  using Tile = Kv4Tile<D>;
+  constexpr int L = D / 8, kTeams = 32 / L, kRounds = 2;
+  const Kv4AppendArgs& a = p.a;
+  const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
+  if (blockIdx.x >= static_cast<uint32_t>(p.kv_blocks)) {
+    const uint32_t unit = (blockIdx.x - static_cast<uint32_t>(p.kv_blocks)) * (kAppendThreads / 32) + warp;
+    const uint32_t t = unit / static_cast<uint32_t>(p.pq);
+    if (t < a.T) append_queries<D, kF32, kInterleaved, kRounds>(p, t, static_cast<int>(unit - t * p.pq), lane);
+    return;
+  }
+  // a token's row: its words in the order of its tile (keys: pieces of kWords, values: of kHalves)
+  constexpr int kStride = D / 8 + 4;
+  __shared__ __align__(16) uint32_t words_s[kTileHeads][2][32][kStride];
+  __shared__ __nv_bfloat16 scales_s[kTileHeads][2][Tile::kBlocks][32];
+  const uint32_t groups = (static_cast<uint32_t>(a.Hkv) + kTileHeads - 1) / kTileHeads, chunk = blockIdx.x / groups;
+  const int64_t h0 = static_cast<int64_t>(blockIdx.x - chunk * groups) * kTileHeads, t0 = static_cast<int64_t>(chunk) * 32;
+  const int heads = a.Hkv - h0 < kTileHeads ? static_cast<int>(a.Hkv - h0) : kTileHeads;
+  const int rows = a.T - t0 < 32 ? static_cast<int>(a.T - t0) : 32;
+  const int c = lane % L, team = lane / L, b = c >> 2;
+  const int slot = lane < rows ? a.slots[t0 + lane] : -1;
+  // 8 rows a warp, kTeams at a time with all of the block's heads
+  float wv[8];
+  if (a.k_weight != nullptr) load8(a.k_weight + 8 * c, wv);
+#pragma unroll 1
+  for (int i = 0; i < 8 / kTeams; ++i) {
+    const int row = 8 * warp + i * kTeams + team;
+    Eight<kF32> xk[kTileHeads], xv[kTileHeads];
+#pragma unroll
+    for (int hh = 0; hh < kTileHeads; ++hh)
+      if (row < rows && hh < heads) {
+        xk[hh].load(a.k, (t0 + row) * a.st[1] + (h0 + hh) * D + 8 * c);
+        xv[hh].load(a.v, (t0 + row) * a.st[2] + (h0 + hh) * D + 8 * c);
       }
-    } else {
-      // blocks 2 h and 2 h + 1 share words: of a lane's two halves the lane of the other block takes one
-      const uint32_t give = (b & 1) == 0 ? word >> 16 : word & 0xFFFFu;
-      const uint32_t got = __shfl_xor_sync(kFull, give, 4);
-      const uint32_t both = (b & 1) == 0 ? (word & 0xFFFFu) | got << 16 : got | (word & 0xFFFF0000u);
-      if (on) {
-        *reinterpret_cast<uint32_t*>(tile + Tile::value_word(tok, 2 * (c & 3) + (b & 1), b >> 1)) = both;
-        if ((c & 3) == 0) *reinterpret_cast<__nv_bfloat16*>(tile + Tile::kValueScales + Tile::scale(tok, b)) = sc;
+    Turn<kInterleaved> rot;
+    rot.load(p, t0 + (row < rows ? row : 0), lane, c);
+#pragma unroll
+    for (int hh = 0; hh < kTileHeads; ++hh) {
+      if (hh >= heads) break;
+      float z[8] = {}, y[8] = {};
+      if (row < rows) {
+        xk[hh].unpack(z);
+        xv[hh].unpack(y);
+      }
+      __nv_bfloat16 sc;
+      const float f = norm_and_turn<D, kInterleaved>(p, rot, wv, z);
+      words_s[hh][0][row][((b >> 2) * 4 + (c & 3)) * Tile::kWords + (b & 3)] = quantise(z, f, &sc);
+      if ((c & 3) == 0) scales_s[hh][0][b][row] = sc;
+      words_s[hh][1][row][(2 * (c & 3) + (b & 1)) * Tile::kHalves + (b >> 1)] = pair_values(quantise(y, 1.0f, &sc), b);
+      if ((c & 3) == 0) scales_s[hh][1][b][row] = sc;
+    }
+  }
+  __syncthreads();
+
+  // neighbours in the cache: the end of one tile, then the beginning of another
+  const int first = __shfl_sync(kFull, slot, 0), tok0 = first & 31, k = 32 - tok0, next = __shfl_sync(kFull, slot, k & 31);
+  const bool follows = lane < k ? static_cast<uint32_t>(slot) == static_cast<uint32_t>(first) + lane
+                                : static_cast<uint32_t>(slot) == static_cast<uint32_t>(next) + lane - k && (next & 31) == 0;
+  uint8_t* tiles[2] = {nullptr, nullptr};
+  int tok;
+  bool ok = token_place(a, first, Tile::kBytes, &tiles[0], &tok);
+  if (k < rows) ok = ok && token_place(a, next, Tile::kBytes, &tiles[1], &tok);
+  const bool in_order = ok && __all_sync(kFull, lane >= rows || follows);
+  for (int hh = 0; hh < heads; ++hh) {
+    const int64_t head_at = (h0 + hh) * (a.page / 32) * Tile::kBytes;
+    const auto& words = words_s[hh];
+    const auto& scales = scales_s[hh];
+    if (in_order) {
+      const int id = static_cast<int>(threadIdx.x);
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        if (part == 1 && k >= rows) break;
+        uint8_t* tile = tiles[part] + head_at;
+        // the row of a token of this tile, outside [0, rows): not one of them
+        auto row_of = [&](int x) { return part == 0 ? x - tok0 : x + k < 32 ? x + k : -1; };
+#pragma unroll
+        for (int i = 0; i < D / kAppendThreads + (D < kAppendThreads ? 1 : 0); ++i) {  // keys: d pieces of 16 bytes
+          const int at = id + i * kAppendThreads;
+          if (at >= D) break;
+          int x, piece;
+          if constexpr (D == 64) {  // rows of two pieces
+            x = at >> 1;
+            piece = at & 1;
+          } else {  // [j][b / 4][n][u]
+            piece = at & 3;
+            x = at >> 2;
+          }
+          int n, j;
+          if constexpr (D == 256) {
+            n = x & 7;
+            piece += ((x >> 3) & 1) * 4;
+            j = x >> 4;
+          } else {
+            n = x & 7;
+            j = x >> 3;
+          }
+          const int row = row_of(8 * (n >> 1) + 2 * j + (n & 1));
+          if (row >= 0 && row < rows)
+            *reinterpret_cast<uint4*>(tile + at * 16) = *reinterpret_cast<const uint4*>(&words[0][row][piece * 4]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // values: 256 pieces of d / 64 words, [2 j + i][g][t]
+          const int at = id + i * kAppendThreads, g = (at >> 2) & 7, row = row_of(8 * (at & 3) + (at >> 5));
+          if (row >= 0 && row < rows) {
+            uint8_t* dst = tile + Tile::kValues + at * 4 * Tile::kHalves;
+            const uint32_t* src = &words[1][row][g * Tile::kHalves];
+            if constexpr (D == 256) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+            else if constexpr (D == 128) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src);
+            else *reinterpret_cast<uint32_t*>(dst) = *src;
+          }
+        }
+        const int row = row_of(lane);
+        if (row >= 0 && row < rows)
+          for (int e = warp; e < 2 * Tile::kBlocks; e += kAppendThreads / 32) {
+            const int kv = e / Tile::kBlocks, blk = e % Tile::kBlocks;
+            *reinterpret_cast<__nv_bfloat16*>(tile + (kv == 0 ? Tile::kKeyScales : Tile::kValueScales) + Tile::scale(lane, blk)) =
+                scales[kv][blk][row];
+          }
+      }
+      continue;
+    }
+    // tokens anywhere: each row by a team
+#pragma unroll 1
+    for (int i = 0; i < 8 / kTeams; ++i) {
+      const int row = 8 * warp + i * kTeams + team;
+      if (row >= rows) continue;
+      uint8_t* tile = nullptr;
+      const int s = a.slots[t0 + row];
+      if (!token_place(a, s, Tile::kBytes, &tile, &tok)) {
+        if (s >= 0 && c == 0 && h0 + hh == 0) atomicOr(a.err, kErrBadCache);
+        continue;
+      }
+      tile += head_at;
+      const int g = 2 * (c & 3) + (b & 1);
+      *reinterpret_cast<uint32_t*>(tile + Tile::key_word(tok, c)) = words[0][row][((b >> 2) * 4 + (c & 3)) * Tile::kWords + (b & 3)];
+      *reinterpret_cast<uint32_t*>(tile + Tile::value_word(tok, g, b >> 1)) = words[1][row][g * Tile::kHalves + (b >> 1)];
+      if ((c & 3) == 0) {
+        *reinterpret_cast<__nv_bfloat16*>(tile + Tile::kKeyScales + Tile::scale(tok, b)) = scales[0][b][row];
+        *reinterpret_cast<__nv_bfloat16*>(tile + Tile::kValueScales + Tile::scale(tok, b)) = scales[1][b][row];
       }
     }
   }
@@ -529,6 +718,18 @@ cudaError_t append(const Kv4AppendArgs& a, const DeviceInfo& dev, cudaStream_t s
   p.nq = static_cast<int>((a.H + 2 * kTeams - 1) / (2 * kTeams));
   p.nk = static_cast<int>((a.Hkv + kTeams - 1) / kTeams);
   p.inv_d = 1.0f / D;
+  const int64_t kv_blocks = (a.T + 31) / 32 * ((a.Hkv + kTileHeads - 1) / kTileHeads);
+  // Tiles where three blocks an SM take them: fewer, each with 32 tokens to go through, end later than
+  // tokens spread over all warps (bfloat16, 32 / 8 heads of 128: 4096 tokens 18.4 us against 21.6, 2048
+  // tokens 13.5 against 12.6; 16 / 16 of 64 from binary32: 4096 15.7 and 17.0, 1024 6.3 and 5.7)
+  if (kv_blocks >= 3 * static_cast<int64_t>(dev.sm_count)) {
+    p.kv_blocks = static_cast<int>(kv_blocks);
+    p.pq = (p.nq + kMost - 1) / kMost;
+    const unsigned grid = static_cast<unsigned>(kv_blocks + (a.T * p.pq + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
+    if (a.interleaved) kv4_append_tiles_kernel<D, kF32, true><<<grid, kAppendThreads, 0, stream>>>(p);
+    else kv4_append_tiles_kernel<D, kF32, false><<<grid, kAppendThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
   const int64_t rounds = a.T * (p.nq + 2 * p.nk), warps = static_cast<int64_t>(dev.sm_count) * 16;
   return rounds >= warps * kMost ? append_rounds<D, kF32, kMost>(p, stream) : append_rounds<D, kF32, 1>(p, stream);
 }

@@ -156,6 +156,39 @@ def test_append(q8, T, H, Hkv, d, rot, page, norm, dtype, interleaved):
     assert torch.equal(again, cache) and (out is None or torch.equal(out, out2))
 
 
+@pytest.mark.parametrize("dtype,interleaved", [(BF16, False), (F32, True)])
+@pytest.mark.parametrize("runs,H,Hkv,d,rot,page", [
+    ([(0, 2050)], 4, 16, 128, 128, 64), ([(77, 700), (5, 1), (31, 33), (64, 320)], 2, 32, 64, 32, 32),
+    ([(13, 1500), (200, 31)], 0, 20, 256, 64, 96), ([(1, 999)], 3, 31, 128, 0, 256), ([(3, 500)], 2, 3, 128, 64, 64)])
+def test_append_of_many_tokens(q8, runs, H, Hkv, d, rot, page, dtype, interleaved):
+    """Packed prompts whose pages lie anywhere: neighbours that end in one tile and go on in another, tiles
+    written in part, tokens that are not kept, and slots in no order at all."""
+    T = sum(n for _, n in runs)
+    q, k, v, (qw, kw) = fused_rows(T, H, Hkv, d, dtype, seed=T)
+    need = [-(-(a + n) // page) for a, n in runs]
+    pages = sum(need) + 2
+    perm = torch.randperm(pages, generator=torch.Generator().manual_seed(T)).tolist()
+    slots, at = [], 0
+    for (a, n), m in zip(runs, need):
+        slots += [perm[at + t // page] * page + t % page for t in range(a, a + n)]
+        at += m
+    table = table_of(T, rot)
+    for case in ("runs", "holes", "anywhere"):
+        if case == "holes":
+            slots[40], slots[100:140], slots[T - 1] = -1, [-5] * 40, pages * page
+        elif case == "anywhere":
+            slots = torch.randperm(pages * page, generator=torch.Generator().manual_seed(3))[:T].tolist()
+        g = torch.Generator(device="cuda").manual_seed(1)
+        cache = torch.randint(0, 256, q8.q8_kv4_cache_shape(pages, page, Hkv, d), generator=g, device="cuda", dtype=torch.uint8)
+        before = cache.clone()
+        out = q8.q8_kv4_append(k, v, cache, i32(slots), table=table, q=q if H else None, q_weight=qw if H else None,
+                               k_weight=kw, interleaved=interleaved)
+        assert q8.q8_device_error() == (1 << 10 if case == "holes" else 0)
+        check_cache(cache, before, slots, k, v, kw, table, interleaved, page)
+        if H:
+            check_q(out, q, qw, table, interleaved)
+
+
 def test_append_of_zeros_ties_and_extremes(q8):
     d, page = 128, 32
     x = torch.zeros(6, 1, d, device="cuda")
