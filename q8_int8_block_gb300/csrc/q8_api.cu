@@ -743,7 +743,8 @@ q8_status q8_kv4_attention(const uint16_t* q, const uint8_t* cache, int64_t page
                            const int64_t* strides, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (B < 0 || B >= kSizeLimit || Tq < 0 || Tq > kSizeLimit || H < 0 || Hkv <= 0 || H > kSizeLimit || H % Hkv != 0 ||
       H / Hkv > 128 || (cu_q == nullptr && Tq != B) || !table_ok(B, width, page) ||
-      static_cast<double>(Tq + B) * static_cast<double>(H) > kRowLimit)
+      static_cast<double>(Tq + B) * static_cast<double>(H) > kRowLimit ||
+      static_cast<double>(Tq + B) * static_cast<double>(H) * static_cast<double>(width * (page / 32) + 4) > 2199023255552.0)
     return Q8_ERR_SHAPE;
   q8_status st = check_cache(cache, page_stride, pages, page, Hkv, d);
   if (st == Q8_ERR_SHAPE) return st;

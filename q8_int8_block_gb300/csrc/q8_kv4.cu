@@ -718,11 +718,11 @@ cudaError_t append(const Kv4AppendArgs& a, const DeviceInfo& dev, cudaStream_t s
   p.nq = static_cast<int>((a.H + 2 * kTeams - 1) / (2 * kTeams));
   p.nk = static_cast<int>((a.Hkv + kTeams - 1) / kTeams);
   p.inv_d = 1.0f / D;
-  const int64_t kv_blocks = (a.T + 31) / 32 * ((a.Hkv + kTileHeads - 1) / kTileHeads);
-  // Tiles where three blocks an SM take them: fewer, each with 32 tokens to go through, end later than
-  // tokens spread over all warps (bfloat16, 32 / 8 heads of 128: 4096 tokens 18.4 us against 21.6, 2048
-  // tokens 13.5 against 12.6; 16 / 16 of 64 from binary32: 4096 15.7 and 17.0, 1024 6.3 and 5.7)
-  if (kv_blocks >= 3 * static_cast<int64_t>(dev.sm_count)) {
+  // Tiles from 24 K channels of keys an SM on: fewer blocks, each with 32 tokens to go through, end
+  // later than tokens spread over all warps (bfloat16, 32 / 8 heads of 128: 4096 tokens 18.4 us against
+  // 21.6, 2048 tokens 13.5 against 12.6; 16 / 16 of 64 from binary32: 4096 15.7 and 17.0, 2048 10.5 both)
+  if (a.T >= 32 && a.T * a.Hkv * D >= 24576 * static_cast<int64_t>(dev.sm_count)) {
+    const int64_t kv_blocks = (a.T + 31) / 32 * ((a.Hkv + kTileHeads - 1) / kTileHeads);
     p.kv_blocks = static_cast<int>(kv_blocks);
     p.pq = (p.nq + kMost - 1) / kMost;
     const unsigned grid = static_cast<unsigned>(kv_blocks + (a.T * p.pq + kAppendThreads / 32 - 1) / (kAppendThreads / 32));

@@ -760,7 +760,10 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     cluster_sync();  // no block leaves while another reads its shared memory
     return;
   }
-  if (abort_flag != 0) return;
+  if (abort_flag != 0) {  // the join must not take what an earlier call has left for a record
+    if (threadIdx.x == 0) p.meta[blockIdx.x].flags = 0;
+    return;
+  }
 
   // The block's chains: a run at a warp's end and those of the warps behind it while it goes on, in the
   // end one put aside.  A warp takes one row of a chain at a time.
@@ -831,7 +834,7 @@ __global__ void __launch_bounds__(1024) kv4_join_kernel(const __grid_constant__ 
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const Record who = p.meta[x];
   if (who.flags == 0) return;
-  const int row = warp / kW, w0 = row * kW, n = static_cast<int>(who.end) - x + 1;
+  const int row = warp / kW, w0 = row * kW, n = min(static_cast<int>(who.end), static_cast<int>(gridDim.x) - 1) - x + 1;
   float top = kNone, sum = 0.0f, acc[E] = {};
   for (int m0 = warp - w0; m0 < n; m0 += kW * kAhead) {
     float2 ml[kAhead];

@@ -158,7 +158,7 @@ def test_append(q8, T, H, Hkv, d, rot, page, norm, dtype, interleaved):
 
 @pytest.mark.parametrize("dtype,interleaved", [(BF16, False), (F32, True)])
 @pytest.mark.parametrize("runs,H,Hkv,d,rot,page", [
-    ([(0, 2050)], 4, 16, 128, 128, 64), ([(77, 700), (5, 1), (31, 33), (64, 320)], 2, 32, 64, 32, 32),
+    ([(0, 2050)], 4, 16, 128, 128, 64), ([(77, 700), (5, 1), (31, 33), (64, 320)], 2, 64, 64, 32, 32),
     ([(13, 1500), (200, 31)], 0, 20, 256, 64, 96), ([(1, 999)], 3, 31, 128, 0, 256), ([(3, 500)], 2, 3, 128, 64, 64)])
 def test_append_of_many_tokens(q8, runs, H, Hkv, d, rot, page, dtype, interleaved):
     """Packed prompts whose pages lie anywhere: neighbours that end in one tile and go on in another, tiles
@@ -354,6 +354,38 @@ HEADS = [(32, 8, 128), (4, 4, 64), (16, 4, 256), (9, 3, 128), (8, 1, 64), (5, 1,
 @pytest.mark.parametrize("lens,page", [([1], 32), ([31, 32, 33], 32), ([1000], 64), ([0, 5, 0, 700, 64, 65], 96)])
 def test_one_query_each(q8, H, Hkv, d, lens, page):
     run(q8, lens, None, page, H, Hkv, d, seed=len(lens))
+
+
+@pytest.mark.parametrize("H,Hkv,d", HEADS)
+@pytest.mark.parametrize("lens,page", [([1], 32), ([0, 33, 500, 32], 64), ([2000], 32)])
+def test_wide_block_tables(q8, H, Hkv, d, lens, page):
+    """Tables that could name far more keys than there are: the work list instead of clusters."""
+    cache, bt, kv = make(lens, page, Hkv, d, seed=5)
+    wide = torch.full((len(lens), 5000), -7, device="cuda", dtype=I32)
+    wide[:, :bt.shape[1]] = bt
+    q = queries(len(lens), H, d)
+    want = expected(q, kv, list(range(len(lens) + 1)), d ** -0.5)
+    for table in (bt, wide):
+        R.assert_within(q8.q8_kv4_attention(q, cache, table, i32(lens)), *want, "attention")
+    assert q8.q8_kv4_attention_workspace_size(len(lens), 5000, page, H, Hkv, d) > 0
+    if H // Hkv <= 8:
+        assert q8.q8_kv4_attention_workspace_size(1, 4, 32, H, Hkv, d) == 0
+    assert q8.q8_device_error() == 0
+
+
+def test_workspace_of_the_caller(q8):
+    lens, H, Hkv, d = [3000, 70], 8, 2, 128
+    cache, bt, kv = make(lens, 64, Hkv, d)
+    q = queries(2, H, d)
+    wide = torch.cat((bt, torch.full((2, 300), -1, device="cuda", dtype=I32)), 1).contiguous()
+    need = q8.q8_kv4_attention_workspace_size(2, wide.shape[1], 64, H, Hkv, d)
+    for fill in (0, 255):  # whatever an earlier call has left there
+        ws = torch.full((need,), fill, device="cuda", dtype=torch.uint8)
+        o = q8.q8_kv4_attention(q, cache, wide, i32(lens), workspace=ws)
+        R.assert_within(o, *expected(q, kv, [0, 1, 2], d ** -0.5))
+    with pytest.raises(q8.Q8Error, match="NOMEM"):
+        q8.q8_kv4_attention(q, cache, wide, i32(lens), workspace=ws[:need - 16])
+    assert q8.q8_device_error() == 0
 
 
 @pytest.mark.parametrize("H,Hkv,d", HEADS)
