@@ -655,8 +655,9 @@ def q8_kv4_append(k, v, cache, slots, table=None, q=None, q_weight=None, k_weigh
         H = q.shape[1]
         sq = _heads("q", q, dtype, (T, H, d), dev)
         if q_out is None:
-            q_out = _empty((T, H, d), torch.bfloat16, q.device, stream)
-        sqo = _heads("q_out", q_out, torch.bfloat16, (T, H, d), dev)
+            q_out, sqo = _empty((T, H, d), torch.bfloat16, q.device, stream), (H * d, d)
+        else:
+            sqo = _heads("q_out", q_out, torch.bfloat16, (T, H, d), dev)
         if H > 1 and (sq[1] != d or sqo[1] != d):
             raise ValueError("q, q_out: the heads of a token must be contiguous")
         pq, po = q.data_ptr(), q_out.data_ptr()
@@ -664,13 +665,14 @@ def q8_kv4_append(k, v, cache, slots, table=None, q=None, q_weight=None, k_weigh
         raise ValueError("q_out: given without q")
     rot, pt = 0, None
     if table is not None:
+        shape = table.shape
         if table.dtype is not f32:
             raise TypeError(f"table: expected torch.float32, got {table.dtype}")
-        if table.dim() != 3 or table.shape[:2] != (T, 2):
-            raise ValueError(f"table: expected shape ({T}, 2, rot/2), got {tuple(table.shape)}")
+        if len(shape) != 3 or shape[0] != T or shape[1] != 2:
+            raise ValueError(f"table: expected shape ({T}, 2, rot/2), got {tuple(shape)}")
         if table.get_device() != dev or not table.is_contiguous():
             raise ValueError(f"table: must be a contiguous CUDA tensor on the current device (cuda:{dev})")
-        rot, pt = 2 * table.shape[2], table.data_ptr()
+        rot, pt = 2 * shape[2], table.data_ptr()
     page_stride, pages, page, heads = _kv4_cache(cache, d, dev)
     if heads != Hkv:
         raise ValueError(f"cache: expected {Hkv} key/value heads, got {heads}")
@@ -683,6 +685,15 @@ def q8_kv4_append(k, v, cache, slots, table=None, q=None, q_weight=None, k_weigh
     if status:
         raise Q8Error(status, "q8_kv4_append")
     return q_out
+
+
+def _rows(name, t, dtype, shape, dev):
+    """t, a contiguous tensor of this type and shape on CUDA device dev."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous CUDA tensor of shape {shape} on the current device (cuda:{dev})")
+    return t
 
 
 def q8_kv4_gather(cache, block_table, cu, tokens, first=None, out_dtype=torch.bfloat16, k=None, v=None, stream=None):
@@ -699,22 +710,15 @@ def q8_kv4_gather(cache, block_table, cu, tokens, first=None, out_dtype=torch.bf
         raise ValueError("cu: expected at least one entry")
     pc, (pb, width) = _vector("cu", cu, torch.int32, n, dev), _block_table(block_table, n - 1, dev)
     shape = (tokens, Hkv, d)
-    out = []
-    for name, t in (("k", k), ("v", v)):
-        if t is None:
-            t = _empty(shape, out_dtype, cache.device, stream)
-        elif t.dtype is not out_dtype:
-            raise TypeError(f"{name}: expected {out_dtype}, got {t.dtype}")
-        elif t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"{name}: a contiguous CUDA tensor of shape {shape} on the current device (cuda:{dev})")
-        out.append(t)
+    k = _empty(shape, out_dtype, cache.device, stream) if k is None else _rows("k", k, out_dtype, shape, dev)
+    v = _empty(shape, out_dtype, cache.device, stream) if v is None else _rows("v", v, out_dtype, shape, dev)
     status = _L.q8_kv4_gather(
         cache.data_ptr(), page_stride, pages, page, pb, width,
-        None if first is None else _vector("first", first, torch.int32, n - 1, dev), pc, out[0].data_ptr(),
-        out[1].data_ptr(), DTYPES[out_dtype], n - 1, tokens, Hkv, d, _stream_on(stream, dev))
+        None if first is None else _vector("first", first, torch.int32, n - 1, dev), pc, k.data_ptr(),
+        v.data_ptr(), DTYPES[out_dtype], n - 1, tokens, Hkv, d, _stream_on(stream, dev))
     if status:
         raise Q8Error(status, "q8_kv4_gather")
-    return out[0], out[1]
+    return k, v
 
 
 def q8_kv4_attention_workspace_size(B, width, page, H, Hkv, d, one_query=True) -> int:

@@ -894,15 +894,18 @@ int grid_blocks(const DeviceInfo& dev) { return std::min(dev.sm_count, kMaxBlock
 
 // Blocks of a cluster that takes a group of rows alone, 0 where the work list is better: one group a
 // request and head, all of them at once on the GPU, and few keys for a block even if one request
-// has all that its row of the block table can name (1024: about what the second launch costs; one
-// request of 1000 keys: XX us alone, 10.1 with the list).
+// has all that its row of the block table can name.  Device time alone and with the list, lengths
+// spread over the logarithm up to the table's: 1 request of 8192 tokens, 32 / 8 heads of 128, 8 blocks a
+// cluster 10.1 and 11.0 us, of 16384 14.2 and 13.4; 4 requests of up to 4096, 4 blocks 10.1 both; 16 of
+// 1536, one block 10.3 and 9.8; the second launch and the workspace take the host about 5 us more.
 int alone_blocks(const Kv4AttentionArgs& a, int nt, const DeviceInfo& dev) {
-  const int64_t items = a.B * a.Hkv, keys = a.width * a.page;
-  if (a.cu_q != nullptr || a.H / a.Hkv > 8 * nt || items > dev.sm_count) return 0;
+  const int64_t items = a.B * a.Hkv, keys = a.width * a.page, sms = dev.sm_count;
+  if (a.cu_q != nullptr || a.H / a.Hkv > 8 * nt || items > sms) return 0;
   int64_t c = 8;
-  while (c > 1 && items * c > dev.sm_count) c /= 2;
+  // clusters do not fill the GPU's parts: 16 of 8 blocks take a second wave
+  while (c > 1 && 8 * items * c > (c == 8 ? 6 : 7) * sms) c /= 2;
   while (c > 1 && c * 64 > keys) c /= 2;  // two tiles a block at least
-  return keys <= c * 1024 ? static_cast<int>(c) : 0;
+  return keys <= c * 1536 ? static_cast<int>(c) : 0;
 }
 
 template <int D, int NT>
