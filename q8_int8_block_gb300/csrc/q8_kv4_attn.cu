@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
   };
 
   const unsigned pick = (g & 1) != 0 ? 0x3244u : 0x1044u;  // the lane's token of a pair, as binary32
-  auto work = [&](const uint8_t* at0, int key0, bool bad) {  // 32 keys from key0 on
+  auto work = [&](uint8_t* at0, int key0, bool bad) {  // 32 keys from key0 on
     // scores: rows of a product are the keys 8 (g / 2) + 2 j + g % 2 of j = 2 jp (elements 0, 1) and
     // 2 jp + 1 (2, 3), columns the rows 2 t, 2 t + 1 (+ 8 x)
     float2 s[NT][2][2];
@@ -524,20 +524,23 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
         }
       }
     }
-    // keys that a row does not see; values behind the last key may hold anything
-    uint32_t keep[4] = {kFull, kFull, kFull, kFull};
+    // keys that a row does not see; values behind the last key may hold anything: their scales become 0
     if (bad || key0 + 32 > lim0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int key = key0 + 8 * (g >> 1) + 2 * j + (g & 1), pair = key0 + 8 * t + 2 * j;
+        const int key = key0 + 8 * (g >> 1) + 2 * j + (g & 1);
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
           if (bad || key >= lim[x][0]) s[x][j >> 1][j & 1].x = -INFINITY;
           if (bad || key >= lim[x][1]) s[x][j >> 1][j & 1].y = -INFINITY;
         }
-        if (bad || pair >= len) keep[j] &= 0xFFFF0000u;
-        if (bad || pair + 1 >= len) keep[j] &= 0x0000FFFFu;
       }
+      if (bad || key0 + lane >= len) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) *reinterpret_cast<uint16_t*>(at0 + Tile::kValueScales + Tile::scale(lane, b)) = 0;
+      }
+      fence_proxy_async_smem();  // before the next copy into the stage
+      __syncwarp();
     }
     // the reference follows the largest score only when that has run ahead
     float top[NT][2];
@@ -606,10 +609,9 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
         const int h = b >> 1;
         const unsigned half = (b & 1) == 0 ? 0x5410u : 0x7632u;
         const uint32_t u0 = __byte_perm(v[0][h], v[1][h], half), u1 = __byte_perm(v[2][h], v[3][h], half);
-        const uint32_t s0 = sc.x & keep[2 * k], s1 = sc.y & keep[2 * k + 1];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-          const uint32_t b0 = mul_bf16(pw[x][2 * k], s0), b1 = mul_bf16(pw[x][2 * k + 1], s1);
+          const uint32_t b0 = mul_bf16(pw[x][2 * k], sc.x), b1 = mul_bf16(pw[x][2 * k + 1], sc.y);
           mma_bf16(o[x][b][0], u0 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x000F000Fu, u1 & 0x00F000F0u, b0, b1);
           mma_bf16(o[x][b][1], (u0 >> 8) & 0x000F000Fu, (u0 >> 8) & 0x00F000F0u, (u1 >> 8) & 0x000F000Fu,
                    (u1 >> 8) & 0x00F000F0u, b0, b1);
