@@ -390,8 +390,9 @@ q8_status q8_kv4_gather(const uint8_t* cache, int64_t page_stride, int64_t pages
  *   A sequence that is not inside [0, Tq] or has a negative length is skipped; kv_len[b] outside
  *     [0, width * page] is taken as the nearest length inside; tokens of a page outside the cache
  *     are not seen.  Each sets bit 10.
- *   Rows of the cache behind kv_len[b] are not used, whatever they hold.  |q| below 2^90.  o may not
- *   share memory with an input.  (Tq + B) * H * (width * page / 32 + 4) is at most 2^41.
+ *   Rows of the cache behind kv_len[b] are not used, whatever they hold.  |q| below 2^90, |v| below
+ *   2^50 (sums of values are kept to 2^-80 beside their own rounding).  o may not share memory with an
+ *   input.  (Tq + B) * H * (width * page / 32 + 4) is at most 2^41.
  *   Meant for few queries a request (a decode step, drafted tokens); any number is right, and for
  *     whole chunks of a prompt q8_kv4_gather with q8_prompt_attention is faster.
  * Scores and sums are binary32; a weight, and its product with a value's scale, are each rounded to

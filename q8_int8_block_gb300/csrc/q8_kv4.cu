@@ -9,18 +9,22 @@
 // Table: cosine and sine of positions[axis[i]][t] * inv_freq[i], once a step for all layers.  The
 // fraction of a turn is a 64-bit fixed-point product (q8_rope_dev.cuh); the nearest quarter is
 // taken off before it becomes binary32, so the rest, at most 1/8 turn, keeps 24 bits of its own
-// and the results are good to about a rounding.
+// and the results are good to about a rounding.  8192 tokens of 64 pairs: 4.1 us.
 //
 // Append: the heads' norm, the rotation and the quantiser in one pass.  Keys: z = x w; pairs turn,
 // every product and sum rounded to binary32; blocks of 32: code = rint(z' * (7 / max |z'|)), scale
 // = max |z'| r / 7 in bfloat16, r = 1 / sqrt(mean x^2 + eps): the norm's factor is one for the
 // head, so it goes into the scales and the codes do not depend on how it was summed.
-// Bound: bytes.  A lane owns 8 channels (one 16-byte load), d / 8 lanes a head; the rotation's
-// partner comes from its lane by shuffle, a block's largest magnitude is a shuffle tree of four
-// lanes.  A warp takes heads of one token, one kind (query, key, value) at a time, and loads the
-// next ones ahead.
+// Bound: bytes (8192 tokens of 32 / 8 heads of 128: 34 us for a floor of 27; the queries alone are at
+// 0.88 of the copy rate, keys and values, 130 instructions for 16 channels of each, at 0.43).
+// Queries: a lane owns the two chunks of 8 channels whose channels pair up, and norm weight and
+// rotation are one matrix a pair.  Keys and values: a lane owns one chunk, the rotation's other
+// channel comes by shuffle, a block's largest magnitude is a shuffle tree of four lanes.  Warps take
+// one kind each, a few heads of a token, or (many tokens) go through tiles of 32 tokens.
 //
-// Gather: rows of keys and values as bfloat16 or binary32.  Bound: the bytes written.
+// Gather: rows of keys and values as bfloat16 or binary32.  Bound: the bytes written (16384 and a few
+// hundred tokens of 8 heads of 128: 14.3 us, 0.90 of the copy rate).
+
 #include <cuda_bf16.h>
 
 #include <algorithm>

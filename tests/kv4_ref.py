@@ -5,14 +5,14 @@ quantiser in binary32 with one rounding per operation, and attention in binary64
 
 Attention.  A weight p_j is rounded to bfloat16, and so is its product with a value's scale (half a
 step, 2^-8 relative, each), and o once: with A = sum p_j |v_j| / sum p_j that is (2 + 2^-8) 2^-8 A
-+ 2^-8 |ref|.  In binary32 the kernel sums nibbles n = code + 8 in 1 .. 15 and takes 8 times the
-other factor's sum off: terms of up to 15 + 8 = 23 times |q_i| s for a score, p_j s for an output,
-instead of |q_i k_i| and p_j |v_j|.  So a score is off by at most (d + 8) 2^-23 scale 23 sum_i
-|q_i| s =: g (the tensor pipe may cut sums off instead of rounding them, hence 2^-23), which takes
-every weight, and so their sum, to between e^-g and e^g times itself: p_j / sum p stays within a
-factor e^(2 g), and o moves by at most (e^(2 g) - 1) A; sums of n weights, the exponential (its
-argument, up to 2^7, rounded to 2^-17) and the division add (n + 64) 2^-22 of A' = 23 sum p_j s /
-sum p_j.
++ 2^-8 |ref|.  In binary32 the kernel sums nibbles n = code + 8 in 1 .. 15 (for outputs every other
+one as (n + 16 n' less n) / 16) and takes 8 times the other factor's sum off: terms of up to 15 + 8,
+or (255 + 15) / 16 + 8, both below 25, times |q_i| s for a score, p_j s for an output, instead of
+|q_i k_i| and p_j |v_j|.  So a score is off by at most (d + 8) 2^-23 scale 25 sum_i |q_i| s =: g
+(the tensor pipe may cut sums off instead of rounding them, hence 2^-23), which takes every weight,
+and so their sum, to between e^-g and e^g times itself: p_j / sum p stays within a factor e^(2 g),
+and o moves by at most (e^(2 g) - 1) A; sums of n weights, the exponential (its argument, up to
+2^7, rounded to 2^-17) and the division add (n + 64) 2^-22 of A' = 25 sum p_j s / sum p_j.
     |o - ref| <= 2^-8 (2 A + |ref|) (1 + 2^-7) + (e^(2 g) - 1) A + (n + 64) 2^-22 A'.
 """
 import torch
@@ -111,8 +111,8 @@ def attention(q, k, v, ks, vs, seen, scale):
         top = x.amax(-1, keepdim=True)
         p = torch.exp(x - top.masked_fill(top == -torch.inf, 0.0))
         p = p / p.sum(-1, keepdim=True).clamp_min(1e-300)
-        g = (d + 8) * 2.0 ** -23 * scale * 23.0 * ((qh.abs() @ sk.T) * seen).amax(-1, keepdim=True)
-        a, wide = p @ vh.abs(), 23.0 * (p @ sv)
+        g = (d + 8) * 2.0 ** -23 * scale * 25.0 * ((qh.abs() @ sk.T) * seen).amax(-1, keepdim=True)
+        a, wide = p @ vh.abs(), 25.0 * (p @ sv)
         o[:, h] = p @ vh
         tol[:, h] = STEP * (2 * a + o[:, h].abs()) * (1 + 2.0 ** -7) + torch.expm1(2 * g) * a + (n + 64) * 2.0 ** -22 * wide
     return o, tol

@@ -472,6 +472,31 @@ def test_strided_queries_outputs_and_pages(q8):
     R.assert_within(want, *expected(q, kv, [0, 1, 2, 3], d ** -0.5))
 
 
+def test_pages_and_rows_far_apart(q8):
+    """Byte offsets of pages, and element offsets of rows, that pass 32 bits."""
+    lens, H, Hkv, d, page = [70, 40], 8, 2, 64, 32
+    cache, bt, kv = make(lens, page, Hkv, d, extra=0)
+    pages, size, far = cache.shape[0], Hkv * 36 * d, 5 << 28  # 1.25 GiB between pages
+    store = torch.empty((pages - 1) * far + size, device="cuda", dtype=torch.uint8)
+    wide = store.as_strided(cache.shape, (far, 36 * d, 36 * d, 1))
+    wide.copy_(cache)
+    assert (pages - 1) * far > 1 << 32
+    q = queries(2, H, d)
+    rows = torch.empty((1 << 32) + H * d, device="cuda", dtype=BF16).as_strided((2, H, d), (1 << 32, d, 1))
+    rows.copy_(q)
+    for table in (bt, widened(bt)):
+        R.assert_within(q8.q8_kv4_attention(rows, wide, table, i32(lens)), *expected(q, kv, [0, 1, 2], d ** -0.5))
+    out = torch.zeros((1 << 32) + H * d, device="cuda", dtype=BF16).as_strided((2, H, d), (1 << 32, d, 1))
+    R.assert_within(q8.q8_kv4_attention(q, cache, bt, i32(lens), o=out), *expected(q, kv, [0, 1, 2], d ** -0.5))
+    k, v = q8.q8_kv4_gather(wide, bt, i32([0, 70, 110]), 110, out_dtype=F32)
+    assert torch.equal(k, torch.cat([x[0] for x in kv])) and torch.equal(v, torch.cat([x[1] for x in kv]))
+    slot = int(bt[1, 1]) * page + 9
+    x = torch.randn(1, Hkv, d, device="cuda")
+    q8.q8_kv4_append(x, x, wide, i32([slot]))
+    q8.q8_kv4_append(x, x, cache, i32([slot]))
+    assert torch.equal(wide, cache) and q8.q8_device_error() == 0
+
+
 def test_nothing_to_do(q8):
     cache, bt, _ = make([5], 32, 2, 64)
     q = queries(0, 4, 64)
@@ -492,9 +517,10 @@ def test_the_same_every_time(q8):
     """Sums are taken in an order fixed by the lengths."""
     cache, bt, _ = make([3000, 50, 700], 64, 4, 128, seed=2)
     q = queries(3, 16, 128)
-    first = q8.q8_kv4_attention(q, cache, bt, i32([3000, 50, 700]))
-    for _ in range(20):
-        assert torch.equal(q8.q8_kv4_attention(q, cache, bt, i32([3000, 50, 700])), first)
+    for table in (bt, widened(bt)):
+        first = q8.q8_kv4_attention(q, cache, table, i32([3000, 50, 700]))
+        for _ in range(20):
+            assert torch.equal(q8.q8_kv4_attention(q, cache, table, i32([3000, 50, 700])), first)
 
 
 # ---- as they are used --------------------------------------------------------------------------
@@ -567,9 +593,53 @@ def test_a_decode_loop_and_its_graph(q8):
     assert width == bt.shape[1] and q8.q8_device_error() == 0
 
 
+def widened(bt, width=3000):
+    """The block table with room for many more pages: calls go through the work list."""
+    return torch.cat((bt, torch.full((bt.shape[0], width - bt.shape[1]), 2 ** 30, device="cuda", dtype=I32)), 1).contiguous()
+
+
+@pytest.mark.parametrize("news", [None, [1, 3, 0, 2]])
+def test_a_graph_of_the_work_list(q8, news):
+    """Captured once, replayed with other lengths, queries and pages, among other work on the stream."""
+    H, Hkv, d, page, B = 16, 4, 128, 64, 4
+    sets = []
+    for i, lens in enumerate(([5000, 3, 700, 64], [1, 4000, 33, 2], [600, 610, 620, 6300])):
+        cache, bt, kv = make(lens, page, Hkv, d, seed=i, extra=3)
+        sets.append((lens, cache, widened(bt, 200), kv, queries(B if news is None else sum(news), H, d, seed=i)))
+    pages = max(s[1].shape[0] for s in sets)
+    cache = torch.zeros((pages, *sets[0][1].shape[1:]), device="cuda", dtype=torch.uint8)
+    bt, q, n = torch.empty_like(sets[0][2]), torch.empty_like(sets[0][4]), i32([0] * B)
+    cu = None if news is None else i32(cum(news))
+
+    def load(s):
+        cache[:s[1].shape[0]].copy_(s[1])
+        bt.copy_(s[2])
+        q.copy_(s[4])
+        n.copy_(i32(s[0]))
+
+    load(sets[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        q8.q8_kv4_attention(q, cache, bt, n, cu_q=cu)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = q8.q8_kv4_attention(q, cache, bt, n, cu_q=cu)
+        twice = o * 2
+    for s in sets + sets[:1]:
+        load(s)
+        graph.replay()
+        want = expected(s[4], s[3], cum(news) if news else list(range(B + 1)), d ** -0.5)
+        R.assert_within(o, *want, "replay")
+        assert torch.equal(twice, o * 2)
+    assert q8.q8_device_error() == 0
+
+
 def test_streams_overlap(q8):
     """Two calls on two streams at once, each with a workspace of its own."""
     sets = [make([2000 + 100 * i, 50], 64, 4, 128, seed=i) for i in range(2)]
+    sets = [(c, widened(bt), kv) for c, bt, kv in sets]
     qs = [queries(2, 16, 128, seed=i) for i in range(2)]
     ns = [i32([2000 + 100 * i, 50]) for i in range(2)]
     want = [q8.q8_kv4_attention(q, c, bt, n) for q, (c, bt, _), n in zip(qs, sets, ns)]
