@@ -395,8 +395,8 @@ q8_status q8_kv4_gather(const uint8_t* cache, int64_t page_stride, int64_t pages
  *   input.  (Tq + B) * H * (width * page / 32 + 4) is at most 2^41.
  *   Meant for few queries a request (a decode step, drafted tokens); any number is right, and for
  *     whole chunks of a prompt q8_kv4_gather with q8_prompt_attention is faster.
- * Scores and sums are binary32; a weight, and its product with a value's scale, are each rounded to
- * bfloat16; o is rounded once.  The order of all sums is fixed by the lengths.
+ * Scores and sums are binary32; the product of a weight and a value's scale is rounded to bfloat16
+ * (once), and o once.  The order of all sums is fixed by the lengths.
  * workspace: at least q8_kv4_attention_workspace_size() bytes, 16-byte aligned (one_query: cu_q is
  * NULL; NULL where that size is 0).  Calls that overlap in time need one each.  Never allocates.
  */

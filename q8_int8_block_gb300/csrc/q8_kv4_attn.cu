@@ -10,16 +10,17 @@
 // (weights), which keeps every sum far inside binary32.  What is left is linear and comes last:
 //   scores   s_b (sum q n - 8 sum q): the second sum belongs to the query, the block's scale is
 //            applied to the binary32 sum of the block;
-//   output   the value's scale multiplies the weight, w = bf16(bf16(p) s_b), and
+//   output   the value's scale multiplies the weight, w = bf16(p s_b), and
 //            sum w (n - 8) = sum w n - 8 sum w: the second sum is one more product, whose
 //            constant operand has a row for each block of 32 channels.
-// The weight and its product with the scale are each rounded to bfloat16 (the other attention kernels
-// round once): products of binary32 would take 60 more instructions a tile of about 400.  All sums are
-// binary32.  Over the measured cases the error against binary64 is 0.0018 to 0.0022 of the output's
-// norm, of which the bfloat16 output's own rounding is 0.0016.
+// Weights change lanes between the two products as bfloat16: the leading 8 bits and the rest apart, so
+// that w is rounded once, as in the other attention kernels (rounding p as well took 3 % off the
+// time: 64 x 16384 tokens 190 us against 198).  All sums are binary32.  Over the measured cases the error
+// against binary64 is 0.0017 to 0.0020 of the output's norm, of which the bfloat16 output's own
+// rounding is 0.0016.
 //
 // Bound: the cache's bytes, 9/8 d for a key and head.  At the copy rate an SM gets 41 elements a
-// clock, so instructions are nearly as scarce as bytes: about 400 warp instructions a tile of 32 keys
+// clock, so instructions are nearly as scarce as bytes: about 430 warp instructions a tile of 32 keys
 // of 128 channels where the copy rate leaves 800 issue slots, half of them on the integer pipe,
 // whose rate is half (53 % busy).
 //
@@ -29,9 +30,9 @@
 // request the partial results meet in the block's shared memory, and what crosses blocks goes to
 // a second kernel.  Small calls are one launch of clusters instead (alone_blocks).
 //
-// Measured (device time, 32 / 8 heads of 128): 64 requests of 16384 tokens 190 us (6.4 TB/s, 0.95 of the
-// measured copy rate), 256 of 2048 106 us (0.85), one of 131072 and one short one 33.5 us (0.67: 4 us to
-// the first tile, 6 from the last to the end of the second launch), one of 1000 6.4 us.
+// Measured (device time, 32 / 8 heads of 128): 64 requests of 16384 tokens 198 us (6.1 TB/s, 0.91 of the
+// measured copy rate), 256 of 2048 111 us (0.81), one of 131072 and one short one 34.5 us (0.65: 4 us to
+// the first tile, 6 from the last to the end of the second launch), one of 1000 6.3 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -54,6 +55,11 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 }
 __device__ __forceinline__ uint32_t mul_bf16(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t fma_bf16(uint32_t a, uint32_t b, uint32_t c) {  // a b + c, rounded once
+  const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&c));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 // bulk_load of what leaves the L2 first: a cache is read once a step, and what the kernels need again
@@ -82,7 +88,7 @@ __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x 
 
 // What a group of rows costs a warp beside its tiles (queries, results), in tiles: the work list counts
 // it in, so that short requests do not hold up the warp that gets many (64 requests of up to 8192
-// keys: 29.0 us, 34 with one, 50 with none).
+// keys: 28.5 us; at the time it was brought in 30 with three, 34 with one, 50 with none).
 constexpr int kExtra = 3;
 constexpr float kNone = -1e30f;     // reference of a row that has seen no key
 constexpr float kLift = 64.0f;      // weights are carried as 2^64 p
@@ -583,7 +589,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
             }
         }
     }
-    uint32_t pw[NT][4];  // weights as B operands: row g (+ 8 x), keys 8 t + 2 j, + 1
+    // weights as B operands: row g (+ 8 x), keys 8 t + 2 j, + 1; their leading 8 bits, and the rest
+    uint32_t pw[NT][4], pr[NT][4];
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -592,7 +599,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
         const float a = ex2(fmaf(v.x, f[x][0], -ref[x][0])), b = ex2(fmaf(v.y, f[x][1], -ref[x][1]));
         l[x][0] += a;
         l[x][1] += b;
-        pw[x][j] = transpose_8x8(pack_bf16(a, b));
+        pw[x][j] = transpose_8x8(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632));
+        pr[x][j] = transpose_8x8(pack_bf16(a - bf16_hi(__float_as_uint(a)), b - bf16_hi(__float_as_uint(b))));
       }
     const uint8_t* values = at0 + Tile::kValues + lane * Tile::kHalves * 4;
 #pragma unroll
@@ -619,7 +627,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
         const uint32_t u0 = __byte_perm(v[0][h], v[1][h], half), u1 = __byte_perm(v[2][h], v[3][h], half);
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-          const uint32_t b0 = mul_bf16(pw[x][2 * k], sc.x), b1 = mul_bf16(pw[x][2 * k + 1], sc.y);
+          const uint32_t b0 = fma_bf16(pw[x][2 * k], sc.x, mul_bf16(pr[x][2 * k], sc.x));
+          const uint32_t b1 = fma_bf16(pw[x][2 * k + 1], sc.y, mul_bf16(pr[x][2 * k + 1], sc.y));
           // rows g: a nibble n; rows g + 8: the byte n + 16 n' that it is in, parted in the sums
           mma_bf16(o[x][b][0], u0 & 0x000F000Fu, u0 & 0x00FF00FFu, u1 & 0x000F000Fu, u1 & 0x00FF00FFu, b0, b1);
           const uint32_t y0 = __byte_perm(u0, 0u, 0x4341), y1 = __byte_perm(u1, 0u, 0x4341);

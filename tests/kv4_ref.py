@@ -3,9 +3,9 @@
 A tile of 32 tokens, byte by byte (index arrays from loops over the format's definition), the
 quantiser in binary32 with one rounding per operation, and attention in binary64.
 
-Attention.  A weight p_j is rounded to bfloat16, and so is its product with a value's scale (half a
-step, 2^-8 relative, each), and o once: with A = sum p_j |v_j| / sum p_j that is (2 + 2^-8) 2^-8 A
-+ 2^-8 |ref|.  In binary32 the kernel sums nibbles n = code + 8 in 1 .. 15 (for outputs every other
+Attention.  The product of a weight p_j and a value's scale is rounded to bfloat16 (half a step, 2^-8
+relative; the weight's own leading bits and rest leave 2^-14 of it beside that), and o once: with A =
+sum p_j |v_j| / sum p_j that is below 2^-8 (A + |ref|) (1 + 2^-5).  In binary32 the kernel sums nibbles n = code + 8 in 1 .. 15 (for outputs every other
 one as (n + 16 n' less n) / 16) and takes 8 times the other factor's sum off: terms of up to 15 + 8,
 or (255 + 15) / 16 + 8, both below 25, times |q_i| s for a score, p_j s for an output, instead of
 |q_i k_i| and p_j |v_j|.  So a score is off by at most (d + 8) 2^-23 scale 25 sum_i |q_i| s =: g
@@ -13,7 +13,7 @@ or (255 + 15) / 16 + 8, both below 25, times |q_i| s for a score, p_j s for an o
 and so their sum, to between e^-g and e^g times itself: p_j / sum p stays within a factor e^(2 g),
 and o moves by at most (e^(2 g) - 1) A; sums of n weights, the exponential (its argument, up to
 2^7, rounded to 2^-17) and the division add (n + 64) 2^-22 of A' = 25 sum p_j s / sum p_j.
-    |o - ref| <= 2^-8 (2 A + |ref|) (1 + 2^-7) + (e^(2 g) - 1) A + (n + 64) 2^-22 A'.
+    |o - ref| <= 2^-8 (A + |ref|) (1 + 2^-5) + (e^(2 g) - 1) A + (n + 64) 2^-22 A'.
 """
 import torch
 
@@ -114,5 +114,5 @@ def attention(q, k, v, ks, vs, seen, scale):
         g = (d + 8) * 2.0 ** -23 * scale * 25.0 * ((qh.abs() @ sk.T) * seen).amax(-1, keepdim=True)
         a, wide = p @ vh.abs(), 25.0 * (p @ sv)
         o[:, h] = p @ vh
-        tol[:, h] = STEP * (2 * a + o[:, h].abs()) * (1 + 2.0 ** -7) + torch.expm1(2 * g) * a + (n + 64) * 2.0 ** -22 * wide
+        tol[:, h] = STEP * (a + o[:, h].abs()) * (1 + 2.0 ** -5) + torch.expm1(2 * g) * a + (n + 64) * 2.0 ** -22 * wide
     return o, tol
