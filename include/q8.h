@@ -361,7 +361,7 @@ q8_status q8_rope_table(const int32_t* positions, int64_t axes, const double* in
  *   A key's z is turned with every product and sum rounded to binary32, a value's z is v.  Blocks of
  *     32 channels: codes rint(fl(z * fl(7 / amax))) in [-7, 7], amax = max |z|; scale
  *     bfloat16(fl(fl(amax * r) * fl(1 / 7))); amax < 2^-120 makes zeros.  Codes do not depend on
- *     how r was summed.
+ *     how r was summed.  A block with a NaN or an infinity reads back without a finite channel.
  */
 q8_status q8_kv4_append(const void* q, const void* k, const void* v, q8_dtype xtype, const int64_t* strides,
                         const float* q_weight, const float* k_weight, float eps, const float* table, int64_t rot,

@@ -209,6 +209,44 @@ def test_append_of_zeros_ties_and_extremes(q8):
     assert torch.equal(k, v) and bool(torch.isfinite(k).all())
 
 
+@pytest.mark.parametrize("T", [5, 4800])  # a warp a token; tiles through shared memory
+@pytest.mark.parametrize("dtype,odd", [(BF16, math.nan), (BF16, -math.inf), (F32, math.nan), (F32, math.inf)])
+def test_append_keeps_what_is_not_finite(q8, T, dtype, odd):
+    H, Hkv, d, page = 2, 8, 128, 64
+    assert T < 100 or T * Hkv * d >= 24576 * torch.cuda.get_device_properties(0).multi_processor_count
+    q, k, v, _ = fused_rows(T, H, Hkv, d, dtype, seed=1)
+    q, k, v = q.clone(), k.clone(), v.clone()
+    slots, bt, cu = i32(list(range(T))), i32([list(range(-(-T // page)))]), i32([0, T])
+    caches = [torch.zeros(q8.q8_kv4_cache_shape(-(-T // page), page, Hkv, d), device="cuda", dtype=torch.uint8) for _ in range(2)]
+    table = table_of(T, 32)
+    clean = q8.q8_kv4_append(k, v, caches[0], slots, table=table, q=q)
+    k[1, 3, 70], v[2, 7, 5], k[4, 0, 3], q[3, 1, 100], q[0, 0, 2] = odd, odd, odd, odd, odd
+    out = q8.q8_kv4_append(k, v, caches[1], slots, table=table, q=q)
+    rows = [q8.q8_kv4_gather(c, bt, cu, T, out_dtype=F32) for c in caches]
+    where = [torch.zeros(T, Hkv, d, device="cuda", dtype=torch.bool) for _ in range(2)]
+    where[0][1, 3, 64:96], where[0][4, 0, :32], where[1][2, 7, :32] = True, True, True  # whole blocks
+    for i in range(2):
+        assert not rows[1][i][where[i]].isfinite().any()
+        assert torch.equal(rows[0][i][~where[i]], rows[1][i][~where[i]])
+    # queries: the channel, and its pair's other one where it turns
+    at = torch.zeros(T, H, d, device="cuda", dtype=torch.bool)
+    at[3, 1, 100] = at[0, 0, 2] = at[0, 0, 18] = True
+    assert not out[at].isfinite().any() and torch.equal(out[~at], clean[~at])
+    assert q8.q8_device_error() == 0
+
+
+def test_append_with_no_angle(q8):
+    T, Hkv, d = 3, 2, 64
+    _, k, v, (_, kw) = fused_rows(T, 1, Hkv, d, BF16, seed=2)
+    inv = torch.ones(16, device="cuda", dtype=torch.float64)
+    inv[9] = math.inf
+    table = q8.q8_rope_table(i32([1, 2, 3]), inv)
+    cache = torch.zeros(q8.q8_kv4_cache_shape(1, 32, Hkv, d), device="cuda", dtype=torch.uint8)
+    q8.q8_kv4_append(k, v, cache, i32([0, 1, 2]), table=table, k_weight=kw)
+    gk, gv = q8.q8_kv4_gather(cache, i32([[0]]), i32([0, T]), T)
+    assert not gk[..., :32].isfinite().any() and gk[..., 32:].isfinite().all() and gv.isfinite().all()
+
+
 def test_append_in_place_repeated_and_strided(q8):
     T, H, Hkv, d, page = 9, 4, 2, 128, 32
     q, k, v, (qw, kw) = fused_rows(T, H, Hkv, d, BF16, seed=5)
