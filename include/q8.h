@@ -390,6 +390,8 @@ q8_status q8_kv4_gather(const uint8_t* cache, int64_t page_stride, int64_t pages
  *   A sequence that is not inside [0, Tq] or has a negative length is skipped; kv_len[b] outside
  *     [0, width * page] is taken as the nearest length inside; tokens of a page outside the cache
  *     are not seen.  Each sets bit 10.
+ *   A value that is not finite makes NaN of the rows of o that see it, and of no others; so does a key,
+ *   if its score is not -infinity.
  *   Rows of the cache behind kv_len[b] are not used, whatever they hold.  |q| below 2^90, |v| below
  *   2^50 (sums of values are kept to 2^-80 beside their own rounding).  o may not share memory with an
  *   input.  (Tq + B) * H * (width * page / 32 + 4) is at most 2^41.

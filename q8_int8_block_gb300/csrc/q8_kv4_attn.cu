@@ -549,9 +549,29 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
           if (bad || key >= lim[x][1]) s[x][j >> 1][j & 1].y = -INFINITY;
         }
       }
-      if (bad || key0 + lane >= len) {
+      uint16_t* scales = reinterpret_cast<uint16_t*>(at0 + Tile::kValueScales + Tile::scale(lane, 0));
+      bool drop = bad || key0 + lane >= len;
+      if constexpr (NT == 2 || D == 256) {
+        // a value that is not finite, of a token that not every row sees: 0 times its scale would reach
+        // them all.  The rows that see the token become NaN here.
+        bool odd = false;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) *reinterpret_cast<uint16_t*>(at0 + Tile::kValueScales + Tile::scale(lane, b)) = 0;
+        for (int b = 0; b < NB; ++b) odd = odd || (scales[32 * b] & 0x7F80u) == 0x7F80u;
+        odd = odd && !drop && key0 + lane >= lim0;
+        drop = drop || odd;
+        const unsigned at = __ballot_sync(kFull, odd);
+        if (at != 0) {
+          const int first = key0 + __ffs(at) - 1;
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (lim[x][r] > first) bias[x][r] = bias[x][2 + r] = NAN;
+        }
+      }
+      if (drop) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) scales[32 * b] = 0;
       }
       fence_proxy_async_smem();  // before the next copy into the stage
       __syncwarp();

@@ -434,6 +434,32 @@ def test_several_queries(q8, H, Hkv, d, lens, news, page):
     run(q8, lens, news, page, H, Hkv, d, seed=len(lens))
 
 
+@pytest.mark.parametrize("H,Hkv,d", HEADS)
+@pytest.mark.parametrize("odd", [math.nan, math.inf])
+def test_unseen_tokens_that_are_not_finite(q8, H, Hkv, d, odd):
+    """A drafted token's key or value that is not finite stays out of the queries in front of it; what
+    sees it is NaN in all its channels."""
+    lens, news, page = [70, 33, 5, 64], [6, 4, 5, 1], 32
+    cache, bt, kv = make(lens, page, Hkv, d)
+    cu = cum(news)
+    q = queries(cu[-1], H, d)
+    o, tol = expected(q, kv, cu, d ** -0.5)
+    bad, lost = (torch.zeros(q.shape, dtype=torch.bool, device="cuda") for _ in range(2))
+    tiles = cache.view(cache.shape[0], Hkv, page // 32, 36 * d).clone()
+    scales = [tiles[..., at:at + 2 * d].view(BF16).view(cache.shape[0], Hkv, page // 32, d // 32, 32) for at in (16 * d, 34 * d)]
+    for b, pos, h, blk, kind in ((0, 66, 0, d // 32 - 1, 1), (0, 68, Hkv - 1, 0, 0), (1, 32, Hkv - 1, 1, 1), (1, 31, 0, 0, 1), (2, 3, 0, 1, 1)):
+        scales[kind][int(bt[b, pos // page]), h, 0, blk, pos % page] = odd
+        first = max(0, pos - (lens[b] - news[b]))  # the first query that sees it
+        heads = slice(h * (H // Hkv), (h + 1) * (H // Hkv))
+        bad[cu[b] + first:cu[b + 1], heads] = True
+        if kind == 1 or math.isnan(odd):  # infinity times a negative sum is the score of a key that counts for nothing
+            lost[cu[b] + first:cu[b + 1], heads] = True
+    got = q8.q8_kv4_attention(q, tiles, bt, i32(lens), cu_q=i32(cu))
+    assert q8.q8_device_error() == 0
+    assert got[lost].isnan().all()
+    R.assert_within(got[~bad], o[~bad], tol[~bad], "queries that do not see it")
+
+
 @pytest.mark.parametrize("H,Hkv,d,news", [(32, 8, 128, None), (16, 16, 64, None), (16, 4, 256, None), (16, 2, 128, 3), (8, 2, 64, 5)])
 def test_long_and_many(q8, H, Hkv, d, news):
     """Runs of the work list that begin and end anywhere: one long request, and many of all lengths."""
