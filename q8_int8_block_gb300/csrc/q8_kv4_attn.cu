@@ -273,7 +273,6 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
   using Sh = Kv4Shape<D, NT>;
   using Tile = Kv4Tile<D>;
   constexpr int NB = Tile::kBlocks, S = Sh::kStages;
-  if constexpr (!kAlone) pdl_launch_dependents();
   extern __shared__ __align__(16) uint8_t sm[];
   __shared__ int abort_flag;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
@@ -296,6 +295,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     fence_barrier_init();
   }
   __syncthreads();  // no wait looks at the flag before it is cleared
+  pdl_wait();
+  if constexpr (!kAlone) pdl_launch_dependents();
   if constexpr (kAlone) {
     // equal runs of the group's tiles: a block's, and of that a warp's
     const uint32_t c = static_cast<uint32_t>(p.cluster), x = blockIdx.x / c, rank = blockIdx.x - x * c;
@@ -956,24 +957,23 @@ size_t ws_bytes(const DeviceInfo& dev) {
 }
 
 template <typename K>
-cudaError_t launch_one(K kernel, int blocks, int threads, size_t smem, int cluster, bool dependent, const Kv4Params& p,
+cudaError_t launch_one(K kernel, int blocks, int threads, size_t smem, int cluster, const Kv4Params& p,
                        cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  if (dependent) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
-  } else if (cluster > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
   }
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
@@ -993,7 +993,7 @@ cudaError_t attention(const Kv4AttentionArgs& a, const DeviceInfo& dev, cudaStre
     const auto kernel = kv4_attention_kernel<D, NT, true>;
     const cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), Sh::kSmem, dev.device);
     if (e != cudaSuccess) return e;
-    return launch_one(kernel, static_cast<int>(a.B * a.Hkv) * p.cluster, Sh::kThreads, Sh::kSmem, p.cluster, false, p, stream);
+    return launch_one(kernel, static_cast<int>(a.B * a.Hkv) * p.cluster, Sh::kThreads, Sh::kSmem, p.cluster, p, stream);
   }
   const int blocks = grid_blocks(dev);
   p.by_grid = static_cast<uint32_t>((uint64_t{1} << 32) / static_cast<uint64_t>(blocks));
@@ -1002,8 +1002,8 @@ cudaError_t attention(const Kv4AttentionArgs& a, const DeviceInfo& dev, cudaStre
   const auto kernel = kv4_attention_kernel<D, NT, false>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), Sh::kSmem, dev.device);
   if (e != cudaSuccess) return e;
-  if ((e = launch_one(kernel, blocks, Sh::kThreads, Sh::kSmem, 1, false, p, stream)) != cudaSuccess) return e;
-  return launch_one(kv4_join_kernel<D, NT>, blocks, 1024, 0, 1, true, p, stream);
+  if ((e = launch_one(kernel, blocks, Sh::kThreads, Sh::kSmem, 1, p, stream)) != cudaSuccess) return e;
+  return launch_one(kv4_join_kernel<D, NT>, blocks, 1024, 0, 1, p, stream);
 }
 
 }  // namespace

@@ -700,6 +700,56 @@ def test_a_graph_of_the_work_list(q8, news):
     assert q8.q8_device_error() == 0
 
 
+@pytest.mark.parametrize("B,wide", [(1, False), (1, True), (4, False), (4, True)])
+def test_layers_one_behind_the_other(q8, B, wide):
+    """Kernels of a step may start while the ones in front of them end: layers of projections, rotations,
+    cache and attention without a pause, waited for one by one, and captured, give the same bits."""
+    H, Hkv, d, page, layers, n = 8, 2, 128, 32, 6, 40
+    g = torch.Generator(device="cuda").manual_seed(3)
+    inv = 1e6 ** (-torch.arange(0, d, 2, device="cuda", dtype=torch.float64) / d)
+    kv_len, pos = i32([n + 1] * B), i32([n] * B)
+    ws = [[q8.q8_quantize_weights(torch.randn(rows, H * d, generator=g, device="cuda") * 0.03) for rows in ((H + 2 * Hkv) * d, H * d)]
+          for _ in range(layers)]
+    x0 = torch.randn(B, H * d, generator=g, device="cuda").to(BF16)
+    kw = 1 + 0.1 * torch.randn(d, generator=g, device="cuda")
+    made = [make([n] * B, page, Hkv, d, seed=i, extra=0)[:2] for i in range(layers)]
+    start = [cache for cache, _ in made]
+    tables = [(widened(bt) if wide else bt, bt[:, n // page] * page + n % page) for _, bt in made]
+
+    def go(caches, wait):
+        x, out = x0, []
+        for (wqkv, wo), cache, (bt, place) in zip(ws, caches, tables):
+            table = q8.q8_rope_table(pos, inv)
+            wait()
+            y = q8.q8_linear_ex(x, *wqkv).view(B, H + 2 * Hkv, d)
+            wait()
+            q = q8.q8_kv4_append(y[:, H:H + Hkv], y[:, H + Hkv:], cache, place, table=table, q=y[:, :H], q_weight=kw, k_weight=kw)
+            wait()
+            o = q8.q8_kv4_attention(q, cache, bt, kv_len)
+            wait()
+            x = q8.q8_linear_ex(o.view(B, H * d), *wo).to(BF16)
+            wait()
+            out += [q, o, x]
+        return out
+
+    slow = [c.clone() for c in start]
+    want = go(slow, torch.cuda.synchronize)
+    assert all(x.isfinite().all() for x in want)
+    for _ in range(5):
+        fast = [c.clone() for c in start]
+        assert all(torch.equal(a, b) for a, b in zip(go(fast, lambda: None) + fast, want + slow))
+    fast = [c.clone() for c in start]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = go(fast, lambda: None)
+    for _ in range(5):
+        for c, s in zip(fast, start):
+            c.copy_(s)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got + fast, want + slow))
+    assert q8.q8_device_error() == 0
+
+
 def test_streams_overlap(q8):
     """Two calls on two streams at once, each with a workspace of its own."""
     sets = [make([2000 + 100 * i, 50], 64, 4, 128, seed=i) for i in range(2)]
