@@ -16,7 +16,7 @@
 // = max |z'| r / 7 in bfloat16, r = 1 / sqrt(mean x^2 + eps): the norm's factor is one for the
 // head, so it goes into the scales and the codes do not depend on how it was summed.
 // Bound: bytes (8192 tokens of 32 / 8 heads of 128: 34 us for a floor of 27; the queries alone are at
-// 0.88 of the copy rate, keys and values, 130 instructions for 16 channels of each, at 0.43).
+// 0.88 of the copy rate, keys and values, bound by their instructions, at 0.50).
 // Queries: a lane owns the two chunks of 8 channels whose channels pair up, and norm weight and
 // rotation are one matrix a pair.  Keys and values: a lane owns one chunk, the rotation's other
 // channel comes by shuffle, a block's largest magnitude is a shuffle tree of four lanes.  Warps take
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const TableParams p) {
 
 // ---- append ----------------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
-constexpr int kTileHeads = 2;  // key/value heads of a block of kv4_append_tiles_kernel
+constexpr int kTileHeads = 2;  // key/value heads of a block of kv4_append_tiles_kernel: four vectors, quantise_four's
 
 struct AppendParams {
   Kv4AppendArgs a;
@@ -333,6 +333,23 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {  // NaN if one o
   return c;
 }
 
+// Of a block: what its channels are multiplied by, its scale.
+__device__ __forceinline__ float per_code(float top) { return top < kKv4Zero ? 0.0f : __fdiv_rn(7.0f, top); }
+__device__ __forceinline__ __nv_bfloat16 block_scale(float top, float f) {
+  return __float2bfloat16_rn(top < kKv4Zero ? 0.0f : __fmul_rn(__fmul_rn(top, f), 1.0f / 7.0f));
+}
+__device__ __forceinline__ uint32_t codes(const float (&z)[8], float per) {
+  uint32_t word = 0;
+#pragma unroll
+  for (int e = 6; e >= 0; e -= 2) {
+    // 1.5 2^23 + 8 is even, so adding it rounds as rint does; its bits are 0x4B400000 + code + 8,
+    // and the first part of eight of them, each 16 times the next, is taken off at the end
+    const float2 m = __fadd2_rn(make_float2(__fmul_rn(z[e], per), __fmul_rn(z[e + 1], per)), make_float2(12582920.0f, 12582920.0f));
+    word = (word * 16u + __float_as_uint(m.y)) * 16u + __float_as_uint(m.x);
+  }
+  return word + kCodes;
+}
+
 // The quantiser: lanes 4 b .. 4 b + 3 of a head hold block b.  The lane's eight codes, and its block's
 // scale.  A block with a NaN or an infinity has that for its scale, and any codes.
 __device__ __forceinline__ uint32_t quantise(const float (&z)[8], float f, __nv_bfloat16* scale) {
@@ -341,18 +358,28 @@ __device__ __forceinline__ uint32_t quantise(const float (&z)[8], float f, __nv_
   for (int e = 0; e < 8; ++e) top = max_or_nan(top, fabsf(z[e]));
   top = max_or_nan(top, __shfl_xor_sync(kFull, top, 1));
   top = max_or_nan(top, __shfl_xor_sync(kFull, top, 2));
-  const bool zero = top < kKv4Zero;
-  const float inv = zero ? 0.0f : __fdiv_rn(7.0f, top);
-  uint32_t word = 0;
+  *scale = block_scale(top, f);
+  return codes(z, per_code(top));
+}
+
+// Four of them at once: each of a block's lanes (u = lane % 4) takes one's largest magnitude, and so
+// its division and scale, and passes the quotient on.
+__device__ __forceinline__ void quantise_four(const float (&z)[4][8], int u, float f, uint32_t (&word)[4], __nv_bfloat16* scale) {
+  float top[4];
 #pragma unroll
-  for (int e = 6; e >= 0; e -= 2) {
-    // 1.5 2^23 + 8 is even, so adding it rounds as rint does; its bits are 0x4B400000 + code + 8,
-    // and the first part of eight of them, each 16 times the next, is taken off at the end
-    const float2 m = __fadd2_rn(make_float2(__fmul_rn(z[e], inv), __fmul_rn(z[e + 1], inv)), make_float2(12582920.0f, 12582920.0f));
-    word = (word * 16u + __float_as_uint(m.y)) * 16u + __float_as_uint(m.x);
+  for (int v = 0; v < 4; ++v) {
+    top[v] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top[v] = max_or_nan(top[v], fabsf(z[v][e]));
   }
-  *scale = __float2bfloat16_rn(zero ? 0.0f : __fmul_rn(__fmul_rn(top, f), 1.0f / 7.0f));
-  return word + kCodes;
+  const bool odd = (u & 1) != 0, high = (u & 2) != 0;
+  const float lo = max_or_nan(odd ? top[1] : top[0], __shfl_xor_sync(kFull, odd ? top[0] : top[1], 1));
+  const float hi = max_or_nan(odd ? top[3] : top[2], __shfl_xor_sync(kFull, odd ? top[2] : top[3], 1));
+  const float mine = max_or_nan(high ? hi : lo, __shfl_xor_sync(kFull, high ? lo : hi, 2));
+  *scale = block_scale(mine, f);
+  const float per = per_code(mine);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) word[v] = codes(z[v], __shfl_sync(kFull, per, v, 4));
 }
 
 // Blocks 2 h and 2 h + 1 of a value share words: of a lane's two halves the lane of the other block
@@ -442,7 +469,7 @@ __global__ void __launch_bounds__(kAppendThreads, kF32 ? 6 : 7) kv4_append_kerne
 // Many tokens: a block takes 32 neighbouring ones of one key/value head, or four parts of queries.
 // What its warps have formed meets in shared memory and is written in the order of the tiles, so
 // that sectors are written whole: the tokens one by one would write 18 sectors each, most of them 2
-// or 8 bytes at a time (8192 tokens of 8 heads of 128: keys and values 16.1 us so, 21.5 one by one).
+// or 8 bytes at a time (8192 tokens of 8 heads of 128: keys and values 14.1 us so, 21.5 one by one).
 template <int D, bool kF32, bool kInterleaved>
 __global__ void __launch_bounds__(kAppendThreads, kF32 ? 6 : 7) kv4_append_tiles_kernel(const __grid_constant__ AppendParams p) {
   using Tile = Kv4Tile<D>;
@@ -471,29 +498,30 @@ __global__ void __launch_bounds__(kAppendThreads, kF32 ? 6 : 7) kv4_append_tiles
 #pragma unroll 1
   for (int i = 0; i < 8 / kTeams; ++i) {
     const int row = 8 * warp + i * kTeams + team;
-    Eight<kF32> xk[kTileHeads], xv[kTileHeads];
-#pragma unroll
-    for (int hh = 0; hh < kTileHeads; ++hh)
-      if (row < rows && hh < heads) {
-        xk[hh].load(a.k, (t0 + row) * a.st[1] + (h0 + hh) * D + 8 * c);
-        xv[hh].load(a.v, (t0 + row) * a.st[2] + (h0 + hh) * D + 8 * c);
-      }
-    Turn<kInterleaved> rot;
-    rot.load(p, t0 + (row < rows ? row : 0), lane, c);
+    const int64_t t = t0 + (row < rows ? row : rows - 1);  // behind the last row or head: that one again
+    Eight<kF32> x[4];                                      // keys of both heads, values of both
 #pragma unroll
     for (int hh = 0; hh < kTileHeads; ++hh) {
-      if (hh >= heads) break;
-      float z[8] = {}, y[8] = {};
-      if (row < rows) {
-        xk[hh].unpack(z);
-        xv[hh].unpack(y);
-      }
-      __nv_bfloat16 sc;
-      const float f = norm_and_turn<D, kInterleaved>(p, rot, wv, z);
-      words_s[hh][0][row][((b >> 2) * 4 + (c & 3)) * Tile::kWords + (b & 3)] = quantise(z, f, &sc);
-      if ((c & 3) == 0) scales_s[hh][0][b][row] = sc;
-      words_s[hh][1][row][(2 * (c & 3) + (b & 1)) * Tile::kHalves + (b >> 1)] = pair_values(quantise(y, 1.0f, &sc), b);
-      if ((c & 3) == 0) scales_s[hh][1][b][row] = sc;
+      const int64_t at = (h0 + (hh < heads ? hh : 0)) * D + 8 * c;
+      x[hh].load(a.k, t * a.st[1] + at);
+      x[2 + hh].load(a.v, t * a.st[2] + at);
+    }
+    Turn<kInterleaved> rot;
+    rot.load(p, t, lane, c);
+    float z[4][8], f[kTileHeads];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v].unpack(z[v]);
+#pragma unroll
+    for (int hh = 0; hh < kTileHeads; ++hh) f[hh] = norm_and_turn<D, kInterleaved>(p, rot, wv, z[hh]);
+    const int u = c & 3;
+    uint32_t word[4];
+    __nv_bfloat16 sc;
+    quantise_four(z, u, (u & 2) != 0 ? 1.0f : (u & 1) != 0 ? f[1] : f[0], word, &sc);
+    scales_s[u & 1][u >> 1][b][row] = sc;
+#pragma unroll
+    for (int hh = 0; hh < kTileHeads; ++hh) {
+      words_s[hh][0][row][((b >> 2) * 4 + u) * Tile::kWords + (b & 3)] = word[hh];
+      words_s[hh][1][row][(2 * u + (b & 1)) * Tile::kHalves + (b >> 1)] = pair_values(word[2 + hh], b);
     }
   }
   __syncthreads();
@@ -752,11 +780,12 @@ cudaError_t append(const Kv4AppendArgs& a, const DeviceInfo& dev, cudaStream_t s
   p.nq = static_cast<int>((a.H + 2 * kTeams - 1) / (2 * kTeams));
   p.nk = static_cast<int>((a.Hkv + kTeams - 1) / kTeams);
   p.inv_d = 1.0f / D;
-  // Tiles from 24 K channels of keys an SM on: fewer blocks, each with 32 tokens to go through, end
-  // later than tokens spread over all warps (bfloat16, 32 / 8 heads of 128: 4096 tokens 18.4 us against
-  // 21.6, 2048 tokens 13.5 against 12.6; 16 / 16 of 64 from binary32: 4096 15.7 and 17.0, 2048 10.5 both)
-  if (a.T >= 32 && a.T * a.Hkv * D >= 24576 * static_cast<int64_t>(dev.sm_count)) {
-    const int64_t kv_blocks = (a.T + 31) / 32 * ((a.Hkv + kTileHeads - 1) / kTileHeads);
+  // Tiles where their blocks are two an SM: fewer, each with 32 tokens to go through, end later than
+  // tokens spread over all warps (bfloat16, 32 / 8 heads of 128: 372 blocks 14.4 us against 16.7, 256 blocks
+  // 12.6 and 12.4, 128 blocks 9.1 and 6.8; 16 / 4 of 256: 256 blocks 21.8 both; 16 / 16 of 64 from
+  // binary32: 512 blocks 9.4 and 10.0, 256 blocks 5.4 both)
+  const int64_t kv_blocks = (a.T + 31) / 32 * ((a.Hkv + kTileHeads - 1) / kTileHeads);
+  if (a.T >= 32 && kv_blocks >= 2 * static_cast<int64_t>(dev.sm_count)) {
     p.kv_blocks = static_cast<int>(kv_blocks);
     p.pq = (p.nq + kMost - 1) / kMost;
     const unsigned grid = static_cast<unsigned>(kv_blocks + (a.T * p.pq + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
