@@ -750,6 +750,55 @@ def test_layers_one_behind_the_other(q8, B, wide):
     assert q8.q8_device_error() == 0
 
 
+@pytest.mark.parametrize("wide", [False, True])
+def test_captured_behind_copies_and_joins(q8, wide):
+    """Calls that follow a fill, a copy, a copy on another stream or two streams at once, eager and captured."""
+    lens, page, H, Hkv, d = [40, 64], 32, 8, 2, 128
+    source, bt, kv = make(lens, page, Hkv, d)
+    bt = widened(bt) if wide else bt
+    T, n, cu = 2, i32([41, 65]), i32([0, 41, 106])
+    q, k, v, (qw, kw) = fused_rows(T, H, Hkv, d, BF16, seed=9)
+    used = {int(p) for p in bt[:, :2].flatten().tolist() if 0 <= p < source.shape[0]}
+    free = [p for p in range(source.shape[0]) if p not in used]
+    bt[1, 2] = free[0]
+    slots = i32([int(bt[0, 1]) * page + 8, free[0] * page])
+    pos, inv = i32([40, 64]), 1e4 ** (-torch.arange(d // 2, device="cuda", dtype=torch.float64) / 64)
+    host = source.cpu().pin_memory()
+    cache, rows = torch.empty_like(source), [torch.empty(106, Hkv, d, device="cuda", dtype=BF16) for _ in range(2)]
+    side = torch.cuda.Stream()
+
+    def go():
+        main = torch.cuda.current_stream()
+        cache.copy_(host, non_blocking=True)  # a copy in front of the table
+        table = q8.q8_rope_table(pos, inv)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            qs = q.clone()
+            cache[:, :, :, :16].copy_(source[:, :, :, :16])
+        main.wait_stream(side)  # two streams in front of the append
+        qr = q8.q8_kv4_append(k, v, cache, slots, table=table, q=qs, q_weight=qw, k_weight=kw)
+        for r in rows:
+            r.zero_()  # a fill in front of the gather
+        q8.q8_kv4_gather(cache, bt, cu, 106, k=rows[0], v=rows[1])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            other = q8.q8_kv4_attention(qr, cache, bt, n)
+        o = q8.q8_kv4_attention(qr, cache, bt, n)
+        main.wait_stream(side)
+        return [qr, o, other, *rows, cache]
+
+    eager = [x.clone() for x in go()]
+    assert all(x.isfinite().all() for x in eager[:5]) and torch.equal(eager[1], eager[2])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = go()
+    for _ in range(3):
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, eager))
+    assert q8.q8_device_error() == 0
+
+
 def test_streams_overlap(q8):
     """Two calls on two streams at once, each with a workspace of its own."""
     sets = [make([2000 + 100 * i, 50], 64, 4, 128, seed=i) for i in range(2)]
