@@ -31,8 +31,8 @@
 // a second kernel.  Small calls are one launch of clusters instead (alone_blocks).
 //
 // Measured (device time, 32 / 8 heads of 128): 64 requests of 16384 tokens 198 us (6.1 TB/s, 0.91 of the
-// measured copy rate), 256 of 2048 111 us (0.81), one of 131072 and one short one 34.5 us (0.65: 4 us to
-// the first tile, 6 from the last to the end of the second launch), one of 1000 6.3 us.
+// measured copy rate), 256 of 2048 111 us (0.82), one of 131072 and one short one 34.5 us (0.65: 4 us to
+// the first tile, 6 from the last to the end of the second launch), one of 1000 6.0 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -294,8 +294,10 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     for (int i = 0; i < S; ++i) mbar_init(&bars[i], 1);
     fence_barrier_init();
   }
-  __syncthreads();  // no wait looks at the flag before it is cleared
-  pdl_wait();
+  // what the kernels in front have written is there for the whole grid once one warp has waited (waited
+  // for by every thread the work list's loop is compiled 1 % slower: 64 x 16384 tokens 201 us against 198)
+  if (kAlone || warp == 0) pdl_wait();
+  __syncthreads();  // nor does a wait look at the flag before it is cleared
   if constexpr (!kAlone) pdl_launch_dependents();
   if constexpr (kAlone) {
     // equal runs of the group's tiles: a block's, and of that a warp's
