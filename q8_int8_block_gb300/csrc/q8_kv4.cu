@@ -142,8 +142,10 @@ __device__ __forceinline__ void join_pairs(float (&a)[8], float (&b)[8]) {
     b[i] = x[8 + i];
   }
 }
+// (Here and in the gather plain loads, not the read-only path: these kernels start while the one in
+// front, which may be writing what they read, still runs, and a read-only load may move across the wait.)
 __device__ __forceinline__ void load8(const float* s, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(s)), b = __ldg(reinterpret_cast<const float4*>(s) + 1);
+  const float4 a = reinterpret_cast<const float4*>(s)[0], b = reinterpret_cast<const float4*>(s)[1];
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
@@ -269,8 +271,8 @@ struct Turn {
     if (!turns) return;
     const float* row = a.table + t * 2 * half;
     if constexpr (kInterleaved) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(row + 4 * c));
-      const float4 v = __ldg(reinterpret_cast<const float4*>(row + half + 4 * c));
+      const float4 u = *reinterpret_cast<const float4*>(row + 4 * c);
+      const float4 v = *reinterpret_cast<const float4*>(row + half + 4 * c);
       cs[0] = u.x; cs[1] = u.y; cs[2] = u.z; cs[3] = u.w;
       sn[0] = v.x; sn[1] = v.y; sn[2] = v.z; sn[3] = v.w;
     } else {
@@ -700,10 +702,10 @@ __global__ void __launch_bounds__(kGatherThreads) kv4_gather_kernel(const __grid
       on[e] = tile != nullptr;
       kw[e] = vw[e] = ks[e] = vs[e] = 0;
       if (on[e]) {
-        kw[e] = __ldg(reinterpret_cast<const uint32_t*>(tile + Tile::key_word(tok, c)));
-        vw[e] = __ldg(reinterpret_cast<const uint32_t*>(tile + Tile::value_word(tok, 2 * u + (b & 1), b >> 1)));
-        ks[e] = __ldg(reinterpret_cast<const uint16_t*>(tile + Tile::kKeyScales + Tile::scale(tok, b)));
-        vs[e] = __ldg(reinterpret_cast<const uint16_t*>(tile + Tile::kValueScales + Tile::scale(tok, b)));
+        kw[e] = *reinterpret_cast<const uint32_t*>(tile + Tile::key_word(tok, c));
+        vw[e] = *reinterpret_cast<const uint32_t*>(tile + Tile::value_word(tok, 2 * u + (b & 1), b >> 1));
+        ks[e] = *reinterpret_cast<const uint16_t*>(tile + Tile::kKeyScales + Tile::scale(tok, b));
+        vs[e] = *reinterpret_cast<const uint16_t*>(tile + Tile::kValueScales + Tile::scale(tok, b));
       }
     }
 #pragma unroll
