@@ -90,9 +90,13 @@ __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x 
 // it in, so that short requests do not hold up the warp that gets many (64 requests of up to 8192
 // keys: 28.5 us; at the time it was brought in 30 with three, 34 with one, 50 with none).
 constexpr int kExtra = 3;
-constexpr float kNone = -1e30f;     // reference of a row that has seen no key
-constexpr float kLift = 64.0f;      // weights are carried as 2^64 p
-constexpr float kSlack = 10.0f;     // a reference may lag behind the largest score by 2^10
+// Weights are 2^((s - ref) f) of the sums s before their factor f (in units of log2): s - ref is exact
+// where it is small, however large the scores are (a reference in units of log2 is itself rounded, for
+// scores of 2^31 by more than the weights' range).
+constexpr float kNone = -3.402823466e38f;  // reference of a row that has seen no key: below every finite sum
+constexpr float kLift = 64.0f;             // weights are carried as 2^64 p
+constexpr float kSlack = 10.0f;            // a reference may lag behind the largest score by 2^10
+constexpr float kMostFactor = 3.402823466e38f;
 
 struct Kv4Params {
   Kv4AttentionArgs a;
@@ -131,7 +135,7 @@ struct Kv4Shape {
   // as many as the registers of a lane allow (128 channels: 12 warps of 168 registers; 16 of 128 spill)
   static constexpr int kWarps = D == 64 ? (NT == 1 ? 16 : 12) : D == 128 && NT == 1 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kPad = D + 4;                         // floats of a row's partial result: o, reference, sum
+  static constexpr int kPad = D + 4;                         // floats of a row's partial result: o, reference, sum, f
   static constexpr int kPart = kRows * kPad;                 // floats of a partial result
   static constexpr int kStages = (225 * 1024 / kWarps - kPart * 4) / Tile::kBytes;
   static constexpr int kRing = kStages * Tile::kBytes;       // of a warp
@@ -239,15 +243,18 @@ __device__ __forceinline__ int rows_used(const Kv4Params& p, int lq, int group) 
   return left < 8 * NT ? static_cast<int>(left) : 8 * NT;
 }
 
-// A row of `members` partial results, member(m) the m-th's: reference, sum, the lane's channels.
+// A row of `members` partial results, member(m) the m-th's: reference, sum, f (the same in all), the lane's
+// channels.
 template <int D, typename F>
-__device__ __forceinline__ void add_up(int lane, int members, const F& member, float& top, float& sum, float (&acc)[D / 32]) {
+__device__ __forceinline__ void add_up(int lane, int members, const F& member, float& top, float& sum, float& f,
+                                       float (&acc)[D / 32]) {
   constexpr int E = D / 32;
-  const float2 ml = lane < members ? *reinterpret_cast<const float2*>(member(lane) + D) : make_float2(kNone, 0.0f);
+  const float4 ml = lane < members ? *reinterpret_cast<const float4*>(member(lane) + D) : make_float4(kNone, 0.0f, 0.0f, 0.0f);
   top = ml.x;
+  f = __shfl_sync(kFull, ml.z, 0);
 #pragma unroll
   for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
-  const float by = ex2(ml.x - top);
+  const float by = ex2((ml.x - top) * f);
   sum = ml.y * by;
 #pragma unroll
   for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(kFull, sum, i);
@@ -430,7 +437,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
 
   uint32_t qb[NT][NB][2][2];   // queries as B operands: block, product, (nibbles 0 / 2, 1 / 3) with (4 / 6, 5 / 7)
   float2 qsum[NT][NB];         // -8 2^-133 sum of a block's queries, rows 2 t and 2 t + 1
-  float f[NT][2];              // scores of these rows in units of log2
+  float f[NT][2];              // what makes these rows' sums scores in units of log2
   int lim[NT][2], lim0 = 0;    // keys that they see; that the first row sees
   float ref[NT][2], l[NT][2];
   float o[NT][NB][2][4], bias[NT][4];
@@ -455,7 +462,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
       // 2^e at most the row's largest: times 2^(100 - e) (a row below 2^-27 keeps smaller values)
       const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -27);
       const float up = __uint_as_float(static_cast<uint32_t>(100 - e + 127) << 23);
-      const float fg = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(33 + e, 127) + 127) << 23);
+      const float fg = fminf(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(33 + e, 127) + 127) << 23), kMostFactor);
       int query;
       int64_t head;
       const bool on = row_at<NT>(p, it.lq, it.h, it.group, g + 8 * x, &query, &head);
@@ -587,7 +594,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
       top[x][0] = fmaxf(fmaxf(s[x][0][0].x, s[x][0][1].x), fmaxf(s[x][1][0].x, s[x][1][1].x));
       top[x][1] = fmaxf(fmaxf(s[x][0][0].y, s[x][0][1].y), fmaxf(s[x][1][0].y, s[x][1][1].y));
 #pragma unroll
-      for (int r = 0; r < 2; ++r) grow = grow || fmaf(top[x][r], f[x][r], -ref[x][r]) > kLift + kSlack;
+      for (int r = 0; r < 2; ++r) grow = grow || (top[x][r] - ref[x][r]) * f[x][r] > kSlack;
     }
     if (__any_sync(kFull, grow)) {
 #pragma unroll
@@ -597,8 +604,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
           float m = top[x][r];
 #pragma unroll
           for (int i = 4; i < 32; i <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, i));
-          m = fmaxf(ref[x][r], fmaf(m, f[x][r], -kLift));
-          const float by = ex2(ref[x][r] - m);
+          m = fmaxf(ref[x][r], m);
+          const float by = ex2((ref[x][r] - m) * f[x][r]);
           ref[x][r] = m;
           l[x][r] *= by;
           bias[x][r] *= by;
@@ -618,8 +625,9 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 v = s[x][j >> 1][j & 1];
-        const float a = ex2(fmaf(v.x, f[x][0], -ref[x][0])), b = ex2(fmaf(v.y, f[x][1], -ref[x][1]));
+        const float2 v = __fadd2_rn(s[x][j >> 1][j & 1], make_float2(-ref[x][0], -ref[x][1]));
+        const float2 e = __ffma2_rn(v, make_float2(f[x][0], f[x][1]), make_float2(kLift, kLift));
+        const float a = ex2(e.x), b = ex2(e.y);
         l[x][0] += a;
         l[x][1] += b;
         pw[x][j] = transpose_8x8(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632));
@@ -678,7 +686,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     return sum * k2m64;
   };
   Record* rec = reinterpret_cast<Record*>(sm + Sh::kOffRec);  // [warp][2]: put aside, at the end
-  // The end of a run: a whole group of rows goes to o, others to `part`, row by row o, reference and sum.
+  // The end of a run: a whole group of rows goes to o, others to `part`, row by row o, reference, sum and f.
   auto put = [&](float* part, bool rows) {
     const Item it = *item;
 #pragma unroll
@@ -694,7 +702,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
         const bool on = row_at<NT>(p, it.lq, it.h, it.group, r, &query, &head);
         uint16_t* dst = p.a.o + (it.q0 + query) * p.a.st[2] + head * p.a.st[3] + 4 * g;
         float* row = part + r * Sh::kPad;
-        if (!rows && g == 0) *reinterpret_cast<float2*>(row + D) = make_float2(ref[x][e] + kLift, sum);
+        if (!rows && g == 0) *reinterpret_cast<float4*>(row + D) = make_float4(ref[x][e], sum, f[x][e], 0.0f);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           float v[4];
@@ -778,22 +786,23 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     const Item it = *reinterpret_cast<const Item*>(sm + Sh::kOffItem);
     const int used = rows_used<NT>(p, it.lq, it.group);
     for (int row = warp; row < used; row += Sh::kWarps) {
-      float top, sum, acc[E];
+      float top, sum, fr, acc[E];
       auto member = [&](int m) { return reinterpret_cast<const float*>(sm + m * Sh::kRing) + row * Sh::kPad; };
-      add_up<D>(lane, users, member, top, sum, acc);
+      add_up<D>(lane, users, member, top, sum, fr, acc);
 #pragma unroll
       for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(aside + row * Sh::kPad + E * lane + e) = make_float2(acc[e], acc[e + 1]);
-      if (lane == 0) *reinterpret_cast<float2*>(aside + row * Sh::kPad + D) = make_float2(top, sum);
+      if (lane == 0) *reinterpret_cast<float4*>(aside + row * Sh::kPad + D) = make_float4(top, sum, fr, 0.0f);
     }
     cluster_sync();
     const int c = p.cluster, rank = static_cast<int>(blockIdx.x) % c;
     for (int row = rank + c * warp; row < used; row += c * Sh::kWarps) {
       const float* mine = aside + row * Sh::kPad;
       float top = kNone, sum = 0.0f, acc[E] = {};
+      const float fr = peer_load(mine + D + 2, 0);  // the first block has a tile
       for (int x = 0; x < c; ++x) top = fmaxf(top, peer_load(mine + D, x));
 #pragma unroll 4
       for (int x = 0; x < c; ++x) {
-        const float by = ex2(peer_load(mine + D, x) - top);
+        const float by = ex2((peer_load(mine + D, x) - top) * fr);
         sum = fmaf(peer_load(mine + D + 1, x), by, sum);
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(peer_load(mine + E * lane + e, x), by, acc[e]);
@@ -833,13 +842,13 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
       auto member = [&](int m) {
         return reinterpret_cast<const float*>(m < n_end ? sm + (w0 + m) * Sh::kRing : sm + Sh::kOffAside + v * Sh::kPart * 4) + row * Sh::kPad;
       };
-      float top, sum, acc[E];
-      add_up<D>(lane, members, member, top, sum, acc);
+      float top, sum, fr, acc[E];
+      add_up<D>(lane, members, member, top, sum, fr, acc);
       if (from_front || goes_on) {
         float* dst = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (from_front ? 0 : 1)) * Sh::kPart + row * Sh::kPad;
 #pragma unroll
         for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(dst + E * lane + e) = make_float2(acc[e], acc[e + 1]);
-        if (lane == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(top, sum);
+        if (lane == 0) *reinterpret_cast<float4*>(dst + D) = make_float4(top, sum, fr, 0.0f);
       } else {
         write_row(who.lq, who.h, who.group, who.q0, row, sum, acc);
       }
@@ -879,6 +888,7 @@ __global__ void __launch_bounds__(1024) kv4_join_kernel(const __grid_constant__ 
   if (who.flags == 0) return;
   const int row = warp / kW, w0 = row * kW, n = min(static_cast<int>(who.end), static_cast<int>(gridDim.x) - 1) - x + 1;
   float top = kNone, sum = 0.0f, acc[E] = {};
+  const float f = p.part[static_cast<int64_t>(2 * x + 1) * Sh::kPart + row * Sh::kPad + D + 2];  // the same in all parts
   for (int m0 = warp - w0; m0 < n; m0 += kW * kAhead) {
     float2 ml[kAhead];
     float v[kAhead][E];
@@ -896,7 +906,7 @@ __global__ void __launch_bounds__(1024) kv4_join_kernel(const __grid_constant__ 
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (ml[i].y == 0.0f) continue;  // nothing seen, or a block without work, whose place holds anything
-      const float to = fmaxf(top, ml[i].x), old = ex2(top - to), by = ex2(ml[i].x - to);
+      const float to = fmaxf(top, ml[i].x), old = ex2((top - to) * f), by = ex2((ml[i].x - to) * f);
       top = to;
       sum = fmaf(sum, old, ml[i].y * by);
 #pragma unroll
@@ -918,7 +928,7 @@ __global__ void __launch_bounds__(1024) kv4_join_kernel(const __grid_constant__ 
     float t = 0.0f, u = 0.0f, v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
-      const float by = ex2(ml_s[w0 + w].x - top);
+      const float by = ex2((ml_s[w0 + w].x - top) * f);
       t = fmaf(ml_s[w0 + w].y, by, t);
       u = fmaf(acc_s[w0 + w][k], by, u);
       v = fmaf(acc_s[w0 + w][k + 1], by, v);
