@@ -96,6 +96,7 @@ constexpr int kExtra = 3;
 constexpr float kNone = -3.402823466e38f;  // reference of a row that has seen no key: below every finite sum
 constexpr float kLift = 64.0f;             // weights are carried as 2^64 p
 constexpr float kSlack = 10.0f;            // a reference may lag behind the largest score by 2^10
+constexpr float kNoPart = -1.0f;           // sum of a partial result that is none
 constexpr float kMostFactor = 3.402823466e38f;
 
 struct Kv4Params {
@@ -869,7 +870,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
   if (lane == 0) p.meta[blockIdx.x] = out;
   // a block without work adds nothing to a run that passes it
   if (run == 0 && lane < Sh::kRows)
-    *reinterpret_cast<float2*>(p.part + static_cast<int64_t>(blockIdx.x) * 2 * Sh::kPart + lane * Sh::kPad + D) = make_float2(kNone, 0.0f);
+    *reinterpret_cast<float2*>(p.part + static_cast<int64_t>(blockIdx.x) * 2 * Sh::kPart + lane * Sh::kPad + D) = make_float2(kNone, kNoPart);
 }
 
 // Runs that cross blocks: block x joins the one that begins in block x of the attention kernel.  The
@@ -896,7 +897,7 @@ __global__ void __launch_bounds__(1024) kv4_join_kernel(const __grid_constant__ 
     for (int i = 0; i < kAhead; ++i) {
       const int m = m0 + i * kW;
       const float* src = p.part + static_cast<int64_t>(2 * (x + m) + (m == 0 ? 1 : 0)) * Sh::kPart + row * Sh::kPad;
-      ml[i] = make_float2(kNone, 0.0f);
+      ml[i] = make_float2(kNone, kNoPart);
       if (m < n) {
         ml[i] = *reinterpret_cast<const float2*>(src + D);
 #pragma unroll
@@ -905,7 +906,7 @@ __global__ void __launch_bounds__(1024) kv4_join_kernel(const __grid_constant__ 
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (ml[i].y == 0.0f) continue;  // nothing seen, or a block without work, whose place holds anything
+      if (ml[i].y == kNoPart) continue;  // its place holds anything
       const float to = fmaxf(top, ml[i].x), old = ex2((top - to) * f), by = ex2((ml[i].x - to) * f);
       top = to;
       sum = fmaf(sum, old, ml[i].y * by);

@@ -73,3 +73,30 @@ def test_values_near_the_largest(q8, lens, news, wide, H, Hkv, d):  # noqa: F811
     assert q8.q8_device_error() == 0
     assert max(float(v.abs().max()) for _, v, _, _ in kv if v.numel()) > 2.0 ** 47
     R.assert_within(got, *expected(q, kv, cu, scale), "large values")
+
+
+@pytest.mark.parametrize("odd", [math.nan, math.inf])
+@pytest.mark.parametrize("Hkv,d,tokens,news", [(1, 128, 19200, [1]), (2, 64, 20000, [1]), (2, 256, 12000, [2]), (1, 128, 40000, None)])
+def test_a_value_among_keys_that_count_for_nothing(q8, Hkv, d, tokens, news, odd):  # noqa: F811
+    """A value that is not finite, in a stretch of keys whose score is -infinity (weight 0) that takes up whole
+    blocks' parts of the request: its rows are NaN all the same, 0 times it."""
+    H = 4 * Hkv
+    cache, bt, _ = make([tokens], 64, Hkv, d, seed=13)
+    if news is None:
+        bt = widened(bt)
+    kc, vc, ks, vs = K.unpack(cache.reshape(-1, 36 * d))
+    n = 64 // 32
+    q = queries(sum(news or [1]), H, d)
+    q[..., :32] = 0
+    q[..., 5] = 1.0            # the first block's scores are its codes times its scale
+    at = torch.arange(tokens // 4, tokens * 3 // 4)
+    tile = (bt[0].cpu()[at // 64].long() * Hkv) * n + at % 64 // 32   # of head 0
+    kc[tile, at % 32, 5] = 1   # -7
+    ks[tile, at % 32, 0] = math.inf
+    mid = len(at) // 2
+    vs[tile[mid], at[mid] % 32, 1] = odd
+    cache = K.pack(kc, vc, ks, vs).view(cache.shape).cuda()
+    got = q8.q8_kv4_attention(q, cache, bt, i32([tokens]), cu_q=i32(cum(news)) if news else None)
+    assert q8.q8_device_error() == 0
+    assert got[:, :4].isnan().all()
+    assert got[:, 4:].isfinite().all()
