@@ -40,6 +40,7 @@
 #include "q8_attn_ptx.cuh"
 #include "q8_internal.h"
 #include "q8_kv4.cuh"
+#include "q8_kv4_ring.h"
 
 namespace q8 {
 namespace {
@@ -144,8 +145,8 @@ struct Kv4Shape {
   static constexpr int kOffRec = kOffAside + kWarps * kPart * 4;
   static constexpr int kOffItem = kOffRec + kWarps * 2 * static_cast<int>(sizeof(Record));
   static constexpr int kOffBar = kOffItem + kWarps * static_cast<int>(sizeof(Item));
-  static constexpr int kOffBad = kOffBar + kWarps * kStages * 8;
-  static constexpr int kSmem = kOffBad + kWarps * kStages * 4;
+  static constexpr int kOffHeld = kOffBar + kWarps * kStages * 8;
+  static constexpr int kSmem = kOffHeld + kWarps * kStages * 4;
   static_assert(kSmem <= 227 * 1024 - 64, "shared memory of a block");
   static_assert(kPart * 4 <= kRing, "a partial result in the ring's place");
   static_assert(kRing % 16 == 0, "alignment of bulk copies");
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int g = lane >> 2, t = lane & 3;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::kOffBar) + warp * S;
-  int* bad_s = reinterpret_cast<int*>(sm + Sh::kOffBad) + warp * S;
+  int* held_s = reinterpret_cast<int*>(sm + Sh::kOffHeld) + warp * S;
   uint8_t* ring = sm + warp * Sh::kRing;
   if (threadIdx.x == 0) abort_flag = 0;
 
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
   // loads: lane l finds the source of every 32nd tile, from the current item on, and starts its copy
   const uint64_t once = read_once();
   const uint8_t* src = nullptr;
-  bool load = false;  // there is such a tile
+  int held = kStageNone;  // what its stage will hold
   auto fill = [&](int i, int ahead) {  // ahead: tiles between the current one and the i-th
     if ((i & 31) == 0) {
       Item it = *item;
@@ -411,8 +412,8 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
         next_item<NT>(p, it);
       }
       src = nullptr;
-      load = x < it.tiles && it.start + kExtra + x < n;
-      if (load && it.len > 0) {
+      const bool in_run = x < it.tiles && it.start + kExtra + x < n;
+      if (in_run && it.len > 0) {
         const uint32_t tpp = static_cast<uint32_t>(p.a.page) / 32;
         const uint32_t page_at = tpp == 1 ? static_cast<uint32_t>(x) : static_cast<uint32_t>(__umul64hi(static_cast<uint32_t>(x), p.by_tpp));
         const int64_t page = p.a.block_table[it.b * p.a.width + page_at];
@@ -422,15 +423,16 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
         else
           atomicOr(p.a.err, kErrBadCache);
       }
+      held = stage_state(in_run, src != nullptr);
       __syncwarp();
     }
-    if (load && lane == (i & 31)) {
+    if (lane == (i & 31)) {
       const int st = i % S;
-      bad_s[st] = src == nullptr;
-      if (src != nullptr) {
+      held_s[st] = held;
+      if (held == kStageTile) {
         mbar_arrive_expect_tx(&bars[st], Tile::kBytes);
         bulk_load_once(ring + st * Tile::kBytes, src, Tile::kBytes, &bars[st], once);
-      } else {
+      } else if (held == kStageNoPage) {
         mbar_arrive(&bars[st]);
       }
     }
@@ -737,7 +739,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     for (; tile < end; ++i) {
       ok = warp_wait(&bars[st], static_cast<uint32_t>(ph), &abort_flag);
       if (!ok) break;
-      work(ring + st * Tile::kBytes, tile * 32, bad_s[st] != 0);
+      work(ring + st * Tile::kBytes, tile * 32, held_s[st] != kStageTile);
       __syncwarp();  // every lane has read the stage
       fill(i + S, S);
       if (++st == S) {
@@ -749,7 +751,7 @@ __global__ void __launch_bounds__(Kv4Shape<D, NT>::kThreads, 1) kv4_attention_ke
     if (!ok) {  // a copy did not come: report it, and wait for those still under way
       report_error(p.a.err, kErrWaitTimeout, &abort_flag);
       for (int k = i; k < i + S; ++k)
-        if ((k >> 5) < ((i + S - 1) >> 5) || __shfl_sync(kFull, load, k & 31)) mbar_wait(&bars[k % S], static_cast<uint32_t>(k / S) & 1u, nullptr);
+        if (stage_completes(held_s[k % S])) mbar_wait(&bars[k % S], static_cast<uint32_t>(k / S) & 1u, nullptr);
       break;
     }
     Item it = *item;

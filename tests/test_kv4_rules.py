@@ -1,6 +1,8 @@
 """Rules of the 4-bit cache's kernels that hold by their sources, checked without a GPU."""
+import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -31,3 +33,36 @@ def test_kernels_that_start_early_use_no_read_only_loads(name):
         found = re.findall(r"__ldg|ld\.global[.\w:]*\.nc|__restrict__", text)
         assert not found, (at, found)
     assert "griddepcontrol.wait" in "".join(source(f)[0] for f in seen)
+
+
+RING = """
+#include "q8_kv4_ring.h"
+// Bit k: the copy of tile at + k is waited for when the wait for tile `at` of a run of `tiles` gives up; of
+// every third tile the page is missing.
+extern "C" unsigned waited_for(int tiles, int stages, int at) {
+  int held[32];
+  auto fill = [&](int i) { held[i % stages] = q8::stage_state(i < tiles, i % 3 != 2); };
+  for (int i = 0; i < stages; ++i) fill(i);
+  for (int i = 0; i < at; ++i) fill(i + stages);
+  unsigned bits = 0;
+  for (int k = 0; k < stages; ++k) bits |= static_cast<unsigned>(q8::stage_completes(held[(at + k) % stages])) << k;
+  return bits;
+}
+"""
+
+
+def test_a_wait_that_gives_up_waits_for_the_copies_under_way(tmp_path):
+    """Those of the run's tiles from the one that did not come to a ring ahead of it, and no others: nobody
+    would complete their phases."""
+    (tmp_path / "ring.cpp").write_text(RING)
+    lib = str(tmp_path / "ring.so")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-I" + CSRC, str(tmp_path / "ring.cpp"), "-o", lib], check=True)
+    waited_for = ctypes.CDLL(lib).waited_for
+    for stages in (2, 3, 4, 7, 10):
+        for tiles in range(1, 101):
+            for at in range(tiles):
+                want = sum(1 << k for k in range(stages) if at + k < tiles)
+                assert waited_for(tiles, stages, at) == want, (stages, tiles, at)
+    text, _ = source("q8_kv4_attn.cu")
+    assert re.search(r"held = stage_state\(in_run, src != nullptr\);", text) and "held_s[st] = held;" in text
+    assert re.search(r"if \(stage_completes\(held_s\[k % S\]\)\) mbar_wait\(&bars\[k % S\]", text)
