@@ -29,6 +29,7 @@
 
 #include "q8_internal.h"
 #include "q8_attn_ptx.cuh"
+#include "q8_launch_ptx.cuh"
 
 namespace q8 {
 namespace {

@@ -1,9 +1,7 @@
 // q8_attn_ptx.cuh -- what the attention kernels use beyond q8_ptx.cuh: bfloat16 MMA descriptors,
-// TMEM stores, the exponential, a warp's wait, dependent launches, the block cluster.
+// TMEM stores, the exponential, a warp's wait.
 #pragma once
 #include <cstdint>
-
-#include <cuda_bf16.h>
 
 #include "q8_ptx.cuh"
 
@@ -60,30 +58,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// two values rounded to bfloat16, lo in the low half
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Launches that depend on the kernel in front of them: that they may begin, and their wait for its end.
-__device__ __forceinline__ void pdl_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// The block cluster: a barrier of all its threads, and a value in the shared memory of CTA `rank`.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float peer_load(const float* own, int rank) {
-  uint32_t at;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(own)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
 }
 
 // every lane of the warp waits; the warp leaves together if any lane's wait gave up

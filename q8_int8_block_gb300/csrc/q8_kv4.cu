@@ -29,9 +29,9 @@
 
 #include <algorithm>
 
-#include "q8_attn_ptx.cuh"
 #include "q8_internal.h"
 #include "q8_kv4.cuh"
+#include "q8_launch_ptx.cuh"
 #include "q8_quant_dev.cuh"
 #include "q8_rope_dev.cuh"
 

@@ -41,6 +41,7 @@
 #include "q8_internal.h"
 #include "q8_kv4.cuh"
 #include "q8_kv4_ring.h"
+#include "q8_launch_ptx.cuh"
 
 namespace q8 {
 namespace {
