@@ -318,7 +318,7 @@ size_t q8_prefix_attention_workspace_size(int64_t B, int64_t P, int64_t cap, int
  * compressed cache ("CUDA inference engine for running Qwen3.5/3.6 hybrid models on mining cards
  * (CMP 100-210)", news.hada.io topic 29953, feature list); this one is written by
  * q8_kv4_append, read by q8_kv4_attention (the newest tokens of each request) and by
- * q8_kv4_gather (keys and values back, as for q8_prompt_attention).
+ * q8_kv4_gather (keys and values back; of 64 or 128 channels as for q8_prompt_attention).
  *
  * cache [pages][Hkv][page / 32][36 d] bytes: page p is at cache + p * page_stride (bytes, a
  *   multiple of 16, at least the page's own Hkv * page / 32 * 36 d), tokens of a page in tiles of
@@ -395,8 +395,9 @@ q8_status q8_kv4_gather(const uint8_t* cache, int64_t page_stride, int64_t pages
  *   Rows of the cache behind kv_len[b] are not used, whatever they hold.  |q| below 2^90, |v| below
  *   2^50 (sums of values are kept to 2^-80 beside their own rounding).  o may not share memory with an
  *   input.  (Tq + B) * H * (width * page / 32 + 4) is at most 2^41.
- *   Meant for few queries a request (a decode step, drafted tokens); any number is right, and for
- *     whole chunks of a prompt q8_kv4_gather with q8_prompt_attention is faster.
+ *   Meant for few queries a request (a decode step, drafted tokens); any number is right.  For whole
+ *     chunks of a prompt q8_kv4_gather with q8_prompt_attention is faster, with heads of 64 or 128
+ *     channels: q8_prompt_attention takes no heads of 256, so this is their only way, 8 rows at a time.
  * Scores and sums are binary32; the product of a weight and a value's scale is rounded to bfloat16
  * (once), and o once.  The order of all sums is fixed by the lengths.
  * workspace: at least q8_kv4_attention_workspace_size() bytes, 16-byte aligned (one_query: cu_q is

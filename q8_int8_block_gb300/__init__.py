@@ -731,7 +731,8 @@ def q8_kv4_attention(q, cache, block_table, kv_len, cu_q=None, scale=None, o=Non
     of each request (the queries' own among them), cu_q int32 [B+1] (None: one query each, Tq = B):
     query i of lq sees the keys j <= i + kv_len - lq -> o [Tq,H,d] bfloat16 (a new o is not
     initialised outside the sequences).  scale None: 1/sqrt(d).  workspace None: allocated here with
-    torch (as a new o, on `stream`)."""
+    torch (as a new o, on `stream`).  For chunks of a prompt q8_kv4_gather and q8_prompt_attention are
+    faster (heads of 64 or 128 channels; of 256 this is the only way)."""
     dev = torch.cuda.current_device()
     Tq, H, d = q.shape
     sq = _heads("q", q, torch.bfloat16, (Tq, H, d), dev)

@@ -66,3 +66,18 @@ def test_a_wait_that_gives_up_waits_for_the_copies_under_way(tmp_path):
     text, _ = source("q8_kv4_attn.cu")
     assert re.search(r"held = stage_state\(in_run, src != nullptr\);", text) and "held_s[st] = held;" in text
     assert re.search(r"if \(stage_completes\(held_s\[k % S\]\)\) mbar_wait\(&bars\[k % S\]", text)
+
+
+def test_the_header_names_the_heads_that_have_a_prompt_path():
+    """q8_kv4_attention's notes send chunks of a prompt to q8_prompt_attention, which takes heads of 64 and 128
+    channels and refuses 256."""
+    import __graft_entry__ as g
+    g.build()
+    import q8_int8_block_gb300 as q8
+    # 0 q 1 k 2 v 3 cu_q 4 cu_k 5 o 6 B 7 Tq 8 Tk 9 H 10 Hkv 11 d 12 scale 13 strides 14 workspace 15 bytes 16 stream
+    at = ctypes.c_void_p(0x10000)
+    refused = {d: q8.lib().q8_prompt_attention(None, at, at, at, at, at, 1, 4, 4, 2, 1, d, 0.1, None, None, 0, None) for d in (64, 128, 256)}
+    assert refused == {64: 1, 128: 1, 256: 2}  # a missing pointer, a size
+    note = open(os.path.join(ROOT, "include", "q8.h")).read().split("q8_kv4_attention --")[1].split("*/")[0]
+    note = " ".join(note.replace("*", " ").split())
+    assert "with heads of 64 or 128 channels: q8_prompt_attention takes no heads of 256" in note
