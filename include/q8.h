@@ -384,7 +384,7 @@ q8_status q8_kv4_gather(const uint8_t* cache, int64_t page_stride, int64_t pages
  * q8_kv4_attention -- attention of each request's newest tokens over its cache.
  *   q, o [Tq][H][d] bfloat16 bits, strides[4] = {q token, q head, o token, o head} in elements (NULL:
  *     contiguous), H / Hkv <= 128.  Request b has the queries cu_q[b] .. cu_q[b + 1] - 1 (cu_q [B + 1]
- *     int32; NULL: one each, Tq == B) and kv_len[b] int32 tokens in the cache, the queries' own
+ *     int32, rising; NULL: one each, Tq == B, and up to a third less time) and kv_len[b] int32 tokens in the cache, the queries' own
  *     among them: its query i of lq sees the keys j <= i + kv_len[b] - lq.  A query that sees no
  *     key gets 0.  Rows of o outside every sequence are left as they are.
  *   A sequence that is not inside [0, Tq] or has a negative length is skipped; kv_len[b] outside

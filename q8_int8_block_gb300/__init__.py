@@ -728,7 +728,8 @@ def q8_kv4_attention_workspace_size(B, width, page, H, Hkv, d, one_query=True) -
 def q8_kv4_attention(q, cache, block_table, kv_len, cu_q=None, scale=None, o=None, workspace=None, stream=None):
     """Attention of each request's newest tokens over its cache: q [Tq,H,d] bfloat16 (strided views are
     fine), cache uint8 of q8_kv4_cache_shape, block_table int32 [B, width], kv_len int32 [B] tokens
-    of each request (the queries' own among them), cu_q int32 [B+1] (None: one query each, Tq = B):
+    of each request (the queries' own among them), cu_q int32 [B+1], rising (None: one query each,
+    Tq = B, and faster):
     query i of lq sees the keys j <= i + kv_len - lq -> o [Tq,H,d] bfloat16 (a new o is not
     initialised outside the sequences).  scale None: 1/sqrt(d).  workspace None: allocated here with
     torch (as a new o, on `stream`).  For chunks of a prompt q8_kv4_gather and q8_prompt_attention are

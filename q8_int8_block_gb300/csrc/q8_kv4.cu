@@ -15,15 +15,16 @@
 // every product and sum rounded to binary32; blocks of 32: code = rint(z' * (7 / max |z'|)), scale
 // = max |z'| r / 7 in bfloat16, r = 1 / sqrt(mean x^2 + eps): the norm's factor is one for the
 // head, so it goes into the scales and the codes do not depend on how it was summed.
-// Bound: bytes (8192 tokens of 32 / 8 heads of 128: 34 us for a floor of 27; the queries alone are at
-// 0.88 of the copy rate, keys and values, bound by their instructions, at 0.50).
+// Bound: bytes (8192 tokens of 32 / 8 heads of 128: 34.2 us for a floor of 27; the queries alone are at
+// 0.89 of the copy rate, keys and values, bound by their instructions, at 0.50).
 // Queries: a lane owns the two chunks of 8 channels whose channels pair up, and norm weight and
 // rotation are one matrix a pair.  Keys and values: a lane owns one chunk, the rotation's other
 // channel comes by shuffle, a block's largest magnitude is a shuffle tree of four lanes.  Warps take
 // one kind each, a few heads of a token, or (many tokens) go through tiles of 32 tokens.
 //
-// Gather: rows of keys and values as bfloat16 or binary32.  Bound: the bytes written (16384 and a few
-// hundred tokens of 8 heads of 128: 13.5 us, 0.95 of the copy rate).
+// Gather: rows of keys and values as bfloat16 or binary32.  Bound: the bytes written (2 contexts of up to 16384
+// tokens, 8 heads of 128: 13.5 us, 0.95 of the copy rate, into rows that the calls before have left in the
+// L2; 14592 tokens 12.0 us into such rows and 15.7 into others).
 
 #include <cuda_bf16.h>
 
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kAppendThreads, kF32 ? 6 : 7) kv4_append_kerne
 // Many tokens: a block takes 32 neighbouring ones of one key/value head, or four parts of queries.
 // What its warps have formed meets in shared memory and is written in the order of the tiles, so
 // that sectors are written whole: the tokens one by one would write 18 sectors each, most of them 2
-// or 8 bytes at a time (8192 tokens of 8 heads of 128: keys and values 14.1 us so, 21.5 one by one).
+// or 8 bytes at a time (8192 tokens of 8 heads of 128: keys and values 14.2 us so, 21.5 one by one).
 template <int D, bool kF32, bool kInterleaved>
 __global__ void __launch_bounds__(kAppendThreads, kF32 ? 6 : 7) kv4_append_tiles_kernel(const __grid_constant__ AppendParams p) {
   using Tile = Kv4Tile<D>;
@@ -748,7 +749,7 @@ __global__ void __launch_bounds__(kGatherThreads) kv4_gather_kernel(const __grid
 
 // A step's kernels follow one another: each may start while the one before ends (it waits for it
 // before it touches memory, and only then lets the next one start).  A decoded token's append and
-// attention, 32 / 8 heads of 128 and 1000 tokens: 8.2 us a layer, 8.7 without.
+// attention, 32 / 8 heads of 128 and 1000 tokens: 8.3 us a layer (8.2 and 8.7 without when it was brought in).
 template <typename P>
 cudaError_t launch_next(void (*kernel)(P), unsigned grid, unsigned threads, const P& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
@@ -792,11 +793,15 @@ cudaError_t append(const Kv4AppendArgs& a, const DeviceInfo& dev, cudaStream_t s
     p.pq = (p.nq + kMost - 1) / kMost;
     const unsigned grid = static_cast<unsigned>(kv_blocks + (a.T * p.pq + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
     // (not launched as the step's small kernels are: its blocks go through many waves, and waiting in
-    // each took 8192 tokens of 32 / 8 heads and their gather from 45.5 us to 48.8)
+    // each took 8192 tokens of 32 / 8 heads and their gather from 45.5 us to 48.8 when it was tried)
     if (a.interleaved) kv4_append_tiles_kernel<D, kF32, true><<<grid, kAppendThreads, 0, stream>>>(p);
     else kv4_append_tiles_kernel<D, kF32, false><<<grid, kAppendThreads, 0, stream>>>(p);
     return cudaGetLastError();
   }
+  // A second round a warp from 32 rounds of heads an SM on (bfloat16, 32 / 8 heads of 128, by one round and by two: 8 rounds
+  // an SM 2.63 us and 2.76, 16 2.98 and 2.94, 24 3.55 and 3.03, 32 3.68 and 3.80, 40 4.34 and 4.00, 96 7.2 and 6.1; 16 / 16 of
+  // 64 from binary32: 8 2.54 and 2.82, 16 2.86 and 3.04, 24 3.44 and 3.17, 32 3.58 and 3.83, 40 4.12 and 3.87; 16 / 4 of 256: 8
+  // 2.61 and 2.79, 32 3.64 and 3.83, 40 4.34 and 4.07)
   const int64_t rounds = a.T * (p.nq + 2 * p.nk), warps = static_cast<int64_t>(dev.sm_count) * 16;
   return rounds >= warps * kMost ? append_rounds<D, kF32, kMost>(p, stream) : append_rounds<D, kF32, 1>(p, stream);
 }
@@ -811,7 +816,11 @@ cudaError_t gather_rows(const Kv4GatherArgs& a, cudaStream_t stream) {
 
 template <int D>
 cudaError_t gather(const Kv4GatherArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  // few rows a warp where 32 would not give every SM eight warps
+  // Few rows a warp where 32 would not give every SM eight warps.  One context, by 32 rows and by few, into rows that
+  // the call before has left in the L2: 8 heads of 128 in bfloat16, 2432 tokens (four warps an SM) 5.2 us and
+  // 3.9, 4864 (eight) 5.9 and 5.4, 7296 6.9 both, 19456 16.1 and 17.5; 16 heads of 64 from 608 tokens (two) 3.6 and 2.9
+  // to 2432 (eight) 4.1 and 3.9, 19456 16.7 and 18.0, in binary32 2432 7.2 and 7.4, 9728 18.0 and 20.3.  Rows in memory,
+  // and heads of 256, keep few rows ahead: 19456 of 8 heads of 128 20.3 and 19.3, 9728 of 4 of 256 14.9 and 10.9.
   return (a.T + 31) / 32 * a.Hkv < 8 * static_cast<int64_t>(dev.sm_count) ? gather_rows<D, true>(a, stream) : gather_rows<D, false>(a, stream);
 }
 

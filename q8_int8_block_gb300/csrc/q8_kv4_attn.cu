@@ -16,13 +16,13 @@
 // Weights change lanes between the two products as bfloat16: the leading 8 bits and the rest apart, so
 // that w is rounded once, as in the other attention kernels (rounding p as well took 3 % off the
 // time: 64 x 16384 tokens 190 us against 198).  All sums are binary32.  Over the measured cases the error
-// against binary64 is 0.0017 to 0.0020 of the output's norm, of which the bfloat16 output's own
+// against binary64 is 0.0017 to 0.0019 of the output's norm, of which the bfloat16 output's own
 // rounding is 0.0016.
 //
-// Bound: the cache's bytes, 9/8 d for a key and head.  At the copy rate an SM gets 41 elements a
-// clock, so instructions are nearly as scarce as bytes: about 430 warp instructions a tile of 32 keys
-// of 128 channels where the copy rate leaves 800 issue slots, half of them on the integer pipe,
-// whose rate is half (53 % busy).
+// Bound: the cache's bytes, 9/8 d for a key and head.  At the copy rate (6694.8 GB/s over 152 SMs at 2070 MHz)
+// an SM gets 21.3 bytes, 38 elements, a clock, a tile of 32 keys of 128 channels in 217: 866 issue slots,
+// for 535 warp instructions with everything around the loop (16 x 16384 tokens; many of them on the
+// integer pipe, whose rate is half: 51 % busy).
 //
 // Split.  The work is the list of (request, head, rows, tile of 32 keys), and every warp takes an
 // equal run of it, wherever that begins and ends: lengths do not matter.  A warp has a ring of
@@ -31,8 +31,8 @@
 // a second kernel.  Small calls are one launch of clusters instead (alone_blocks).
 //
 // Measured (device time, 32 / 8 heads of 128): 64 requests of 16384 tokens 198 us (6.1 TB/s, 0.91 of the
-// measured copy rate), 256 of 2048 111 us (0.82), one of 131072 and one short one 34.5 us (0.65: 4 us to
-// the first tile, 6 from the last to the end of the second launch), one of 1000 6.0 us.
+// measured copy rate), 256 of 2048 111 us (0.82), 2 of up to 131072 34.2 us (0.66: 4 us to the first
+// tile, 6 from the last to the end of the second launch), one of 1000 6.2 us by a cluster, 3.4 more by the list.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -89,8 +89,9 @@ __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x 
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
 // What a group of rows costs a warp beside its tiles (queries, results), in tiles: the work list counts
-// it in, so that short requests do not hold up the warp that gets many (64 requests of up to 8192
-// keys: 28.5 us; at the time it was brought in 30 with three, 34 with one, 50 with none).
+// it in, so that short requests do not hold up the warp that gets many (64 requests of up to 8192 keys,
+// with one, two, three, four, six: 32.0, 29.5, 28.8, 29.0, 30.6 us; 2 of up to 131072 37.9, 34.6, 34.7, 35.4,
+// 35.7; 64 of 2048 36.9, 36.6, 36.3, 37.5, 37.6).
 constexpr int kExtra = 3;
 // Weights are 2^((s - ref) f) of the sums s before their factor f (in units of log2): s - ref is exact
 // where it is small, however large the scores are (a reference in units of log2 is itself rounded, for
@@ -944,7 +945,9 @@ __global__ void __launch_bounds__(1024) kv4_join_kernel(const __grid_constant__ 
 
 // ---- host ------------------------------------------------------------------------------------
 // Rows of a group: 8, or 16 where a request's rows may be more (256 channels: 8, sixteen would
-// not fit the registers).
+// not fit the registers).  64 requests of 4096 tokens, 16 rows against two groups of 8: 4 heads of 128 a group and 4 new
+// tokens 92.9 us and 109.3, 16 heads a group 92.5 and 109.3, of 64 channels 59.2 and 70.8.  How many queries a request
+// has is not known here: with cu_q, 8 rows or fewer pay for 16 (one new token of 4 heads of 128 89.5 us, 60.1 by 8).
 int row_tiles(int64_t G, bool one_query, int64_t d) { return d == 256 || (one_query && G <= 8) ? 1 : 2; }
 
 int grid_blocks(const DeviceInfo& dev) { return std::min(dev.sm_count, kMaxBlocks); }
@@ -954,7 +957,8 @@ int grid_blocks(const DeviceInfo& dev) { return std::min(dev.sm_count, kMaxBlock
 // has all that its row of the block table can name.  Device time alone and with the list, lengths
 // spread over the logarithm up to the table's: 1 request of 8192 tokens, 32 / 8 heads of 128, 8 blocks a
 // cluster 10.1 and 11.0 us, of 16384 14.2 and 13.4; 4 requests of up to 4096, 4 blocks 10.1 both; 16 of
-// 1536, one block 10.3 and 9.8; the second launch and the workspace take the host about 5 us more.
+// 1536, one block 10.3 and 9.8; the second launch and the workspace take the host about 5 us more.  (The
+// lengths themselves are not known here: one request of 1000 behind a table of 16384 or more gets the list.)
 int alone_blocks(const Kv4AttentionArgs& a, int nt, const DeviceInfo& dev) {
   const int64_t items = a.B * a.Hkv, keys = a.width * a.page, sms = dev.sm_count;
   if (a.cu_q != nullptr || a.H / a.Hkv > 8 * nt || items > sms) return 0;
