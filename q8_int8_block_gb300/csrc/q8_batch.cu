@@ -448,14 +448,16 @@ __global__ void __maxnreg__(kMaxRegs)
 // writes them as two 8-byte halves: K 8 sub..+3 to piece 2 (sub & 1), K 8 sub+4..+7 to
 // piece 2 (sub & 1) + 1, in the piece's first half for sub < 2, second half otherwise.
 // kCodes: the input is int8 codes already (block-sum mode); no scales.
-// gamma / r: the RMSNorm prologue (nullptr: none): codes of fl32(x * gamma), scale d * r[m].
+// gamma / r: the RMSNorm prologue (nullptr: none): codes of fl32(x * gamma), scale d * r[m].  (The
+// kernel in front writes r while this one runs: it is not __restrict__, and read as volatile, so that the
+// load is no read-only one and stays behind the wait.)
 template <typename InT, bool kCodes>
 __global__ void __launch_bounds__(256) quantize_batch_kernel(const InT* __restrict__ x,
                                                              uint16_t* __restrict__ xb,
                                                              float* __restrict__ xbd, int M,
                                                              int TP, int nb,
                                                              const float* __restrict__ gamma,
-                                                             const float* __restrict__ r) {
+                                                             const float* r) {
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int sub = lane & 3;
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(256) quantize_batch_kernel(const InT* __restri
       d = quantize_block_x4(v, group_mask, q);
       if (r != nullptr) {
         pdl_wait();  // r comes from the row-RMS kernel this one may overlap
-        d = __fmul_rn(d, r[m]);
+        d = __fmul_rn(d, *static_cast<const volatile float*>(r + m));
       }
     }
     const int p0 = 2 * (sub & 1);

@@ -68,6 +68,10 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// aux of output i (0 when the epilogue takes none) by a plain load: this kernel starts while the one in front,
+// which may be writing aux, still runs, and a read-only load may move across the wait.
+__device__ __forceinline__ float late_aux(const Epilogue& e, int64_t i) { return e.op == kEpiNone ? 0.0f : e.aux[i]; }
+
 __device__ __forceinline__ int4 lds128(const void* p) { return *reinterpret_cast<const int4*>(p); }
 
 // kXP > 0: one token, K <= 512 * kXP; each lane always covers the same K positions, so it
@@ -188,8 +192,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeParams 
             for (int t = 0; t < MT; ++t)
               if (t == tb) ss[t] += s2;
             const int k = (blk % nb) * kQK + sub * 8;
-            const float4 g0 = __ldg(reinterpret_cast<const float4*>(p.pro.gamma + k));
-            const float4 g1 = __ldg(reinterpret_cast<const float4*>(p.pro.gamma + k) + 1);
+            const float4 g0 = reinterpret_cast<const float4*>(p.pro.gamma + k)[0];
+            const float4 g1 = reinterpret_cast<const float4*>(p.pro.gamma + k)[1];
             const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], g[i]);
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeParams 
       const int64_t n = r0 + j;
       float ax = 0.0f;  // lane t < M: aux of output (t, n), loaded before the row's weights land
       if constexpr (!kBlockSums && kFused) {
-        if (lane < M) ax = epi_aux(p.epi, static_cast<int64_t>(lane) * N + n);
+        if (lane < M) ax = late_aux(p.epi, static_cast<int64_t>(lane) * N + n);
       }
       const int st = j / R;
       const int s = st % S;

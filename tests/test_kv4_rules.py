@@ -35,6 +35,18 @@ def test_kernels_that_start_early_use_no_read_only_loads(name):
     assert "griddepcontrol.wait" in "".join(source(f)[0] for f in seen)
 
 
+def test_linears_that_start_early_use_no_read_only_loads_of_what_is_in_front():
+    """The same for the decode kernel (its norm's weights, its epilogue's input) and for the factor that the
+    batch kernel's quantiser takes from the kernel in front."""
+    decode, batch = source("q8_decode.cu")[0], source("q8_batch.cu")[0]
+    assert not re.search(r"__ldg|ld\.global[.\w:]*\.nc|__restrict__|epi_aux", decode) and "late_aux(p.epi" in decode
+    assert "return e.op == kEpiNone ? 0.0f : e.aux[i];" in decode
+    args = re.search(r"void __launch_bounds__\(256\) quantize_batch_kernel\((.*?)\) \{", batch, flags=re.S)[1]
+    assert re.search(r"const float\* r$", args)
+    reads = re.findall(r"[^\n]*(?:\br ?\+ m\b|\br\[m\])[^\n]*", batch)
+    assert reads == ["        d = __fmul_rn(d, *static_cast<const volatile float*>(r + m));"]
+
+
 RING = """
 #include "q8_kv4_ring.h"
 // Bit k: the copy of tile at + k is waited for when the wait for tile `at` of a run of `tiles` gives up; of
