@@ -47,6 +47,15 @@ def test_linears_that_start_early_use_no_read_only_loads_of_what_is_in_front():
     assert reads == ["        d = __fmul_rn(d, *static_cast<const volatile float*>(r + m));"]
 
 
+def test_the_batch_kernel_knows_its_epilogue_input_only_behind_the_wait():
+    """Its loads of aux may be read-only ones, which move freely: the address they take comes out of a statement
+    that stays behind the wait."""
+    kernel = source("q8_batch.cu")[0]
+    wait = re.search(r"pdl_wait\(\);\s*if constexpr \(!kBlockSums && kFused\)", kernel).start()
+    known = kernel.index('asm volatile("" : "+l"(epi.aux));')
+    assert wait < known < kernel.index("epi_aux(epi,") and "epi_aux(p.epi" not in kernel
+
+
 RING = """
 #include "q8_kv4_ring.h"
 // Bit k: the copy of tile at + k is waited for when the wait for tile `at` of a run of `tiles` gives up; of
